@@ -10,3 +10,5 @@ from . import binding  # noqa: F401
 from .binding import (HMError, LibraryMissing, ModalHyena, hm_desc, hyena_filter_materialize,  # noqa: F401
                       hyena_modal_decode_step, hyena_modal_prefill, hyena_modal_prefill_workspace,
                       make_desc)
+from .beam import BeamSearch  # noqa: F401
+from .linear_attention import LinearAttention  # noqa: F401

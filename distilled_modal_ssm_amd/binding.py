@@ -24,6 +24,8 @@ HM_MAX_MODES = 64
 HM_F32, HM_BF16 = 0, 1
 HM_OK, HM_ERR_INVALID_ARG, HM_ERR_UNSUPPORTED, HM_ERR_WORKSPACE, HM_ERR_HIP = range(5)
 HM_PREFILL_AUTO, HM_PREFILL_SCAN, HM_PREFILL_MFMA = 0, 1, 2
+HM_LINATTN_MAX_DIM = 256
+HM_BEAM_MAX = 64
 HM_NOALLOC_SCRATCH_BYTES = 16 << 20  # per-GPU scratch of hyena_modal_prefill_noalloc
 ALGOS = {"auto": HM_PREFILL_AUTO, "scan": HM_PREFILL_SCAN, "mfma": HM_PREFILL_MFMA}
 
@@ -60,6 +62,12 @@ EXPORTS = (
     "hyena_hankel_singular_values",
     "hyena_modal_order",
     "hyena_modal_fit_init",
+    "hyena_linattn_prefill_workspace",
+    "hyena_linattn_prefill",
+    "hyena_linattn_decode_step",
+    "hyena_beam_select_workspace",
+    "hyena_beam_select",
+    "hyena_beam_reorder",
 )
 
 
@@ -96,6 +104,22 @@ class hm_prefill_info(ctypes.Structure):
                 ("n_chunks", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class hm_linattn_desc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int64),
+        ("heads", ctypes.c_int64),
+        ("q_heads", ctypes.c_int64),
+        ("k_heads", ctypes.c_int64),
+        ("v_heads", ctypes.c_int64),
+        ("key_dim", ctypes.c_int64),
+        ("value_dim", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -112,7 +136,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 "(or __graft_entry__.build()); there is no CPU fallback")
         lib = ctypes.CDLL(path)
         i64, p, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
-        D = ctypes.POINTER(hm_desc)
+        D, A = ctypes.POINTER(hm_desc), ctypes.POINTER(hm_linattn_desc)
         sig = {
             "hm_abi_version": ([], ctypes.c_int),
             "hm_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -153,6 +177,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "hyena_hankel_singular_values": ([p, i64, i64, p], ctypes.c_int),
             "hyena_modal_order": ([p, i64, i64, i64, ctypes.c_double, p], ctypes.c_int),
             "hyena_modal_fit_init": ([p, i64, i64, i64, f32, p, p, p], ctypes.c_int),
+            "hyena_linattn_prefill_workspace": ([A, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_linattn_prefill": ([A, i64, p, p, i64, p, i64, p, i64, p, i64, p, i64, p, p, p, sz, p],
+                                      ctypes.c_int),
+            "hyena_linattn_decode_step": ([A, p, i64, p, i64, p, i64, p, i64, p, i64, p, p, p, p], ctypes.c_int),
+            "hyena_beam_select_workspace": ([i64, i64, i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_beam_select": ([i64, i64, i64, i64, ctypes.c_int32, p, i64, p, p, i64, p, p, p, p, p, sz, p],
+                                  ctypes.c_int),
+            "hyena_beam_reorder": ([i64, i64, p, i64, p, p, p], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -455,7 +487,97 @@ def hyena_modal_fit_init(h, d: int, r_max: float = 0.9999):
     return poles, res, skip
 
 
+# ----------------------------------------------------------------- linear attention, beam search
+
+
+def make_linattn_desc(batch, heads, key_dim, value_dim, act_dtype, scale, q_heads=None, k_heads=None,
+                      v_heads=None) -> hm_linattn_desc:
+    return hm_linattn_desc(HM_ABI_VERSION, act_dtype, batch, heads, heads if q_heads is None else q_heads,
+                           heads if k_heads is None else k_heads, heads if v_heads is None else v_heads, key_dim,
+                           value_dim, scale, 0)
+
+
+def hyena_linattn_prefill_workspace(desc: hm_linattn_desc, L: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_linattn_prefill_workspace(ctypes.byref(desc), L, ctypes.byref(n)),
+           "hyena_linattn_prefill_workspace")
+    return n.value
+
+
+def hyena_linattn_prefill(desc: hm_linattn_desc, L, lengths, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_decay, y, ld_y,
+                          state_in, state_out, workspace, ws_bytes=None, stream=None) -> None:
+    st = load().hyena_linattn_prefill(ctypes.byref(desc), L, _ptr(lengths), _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v,
+                                      _ptr(log_decay), ld_decay, _ptr(y), ld_y, _ptr(state_in), _ptr(state_out),
+                                      _ptr(workspace), _ws_bytes(workspace, ws_bytes), _stream(stream))
+    _check(st, "hyena_linattn_prefill")
+
+
+def hyena_linattn_decode_step(desc: hm_linattn_desc, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_decay, y, ld_y, state_in,
+                              src_rows, state_out, stream=None) -> None:
+    st = load().hyena_linattn_decode_step(ctypes.byref(desc), _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v,
+                                          _ptr(log_decay), ld_decay, _ptr(y), ld_y, _ptr(state_in), _ptr(src_rows),
+                                          _ptr(state_out), _stream(stream))
+    _check(st, "hyena_linattn_decode_step")
+
+
+def hyena_beam_select_workspace(groups: int, beams: int, vocab: int, select: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_beam_select_workspace(groups, beams, vocab, select, ctypes.byref(n)),
+           "hyena_beam_select_workspace")
+    return n.value
+
+
+def hyena_beam_select(groups, beams, vocab, select, dtype, logits, ld, scores, finished, end_token, out_scores,
+                      out_tokens, out_parents, out_finished, workspace, ws_bytes=None, stream=None) -> None:
+    st = load().hyena_beam_select(groups, beams, vocab, select, dtype, _ptr(logits), ld, _ptr(scores), _ptr(finished),
+                                  end_token, _ptr(out_scores), _ptr(out_tokens), _ptr(out_parents),
+                                  _ptr(out_finished), _ptr(workspace), _ws_bytes(workspace, ws_bytes),
+                                  _stream(stream))
+    _check(st, "hyena_beam_select")
+
+
+def hyena_beam_reorder(groups, beams, parents, buffers, row_bytes, stream=None) -> None:
+    """buffers: device addresses or tensors; row_bytes: as many sizes."""
+    n = len(buffers)
+    if len(row_bytes) != n:
+        raise ValueError("one row size a buffer")
+    st = load().hyena_beam_reorder(groups, beams, _ptr(parents), n, (ctypes.c_void_p * n)(*[_ptr(b) for b in buffers]),
+                                   (ctypes.c_int64 * n)(*row_bytes), _stream(stream))
+    _check(st, "hyena_beam_reorder")
+
+
 # ----------------------------------------------------------------- tensor helpers
+
+
+class _On:
+    """``with _On(device, stream) as s``: makes the device current, with the given
+    stream (a hipStream_t, a torch stream) or else its current one as torch's, so
+    that memory allocated inside belongs to it; s is the hipStream_t."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device, self.stream = device, stream
+        if stream is None:
+            self.guard = torch.cuda.device(device)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.guard = torch.cuda.stream(stream)
+        self.torch = torch
+
+    def __enter__(self):
+        self.guard.__enter__()
+        return int(self.torch.cuda.current_stream(self.device).cuda_stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _expect(name, t, dtype, shape, device):
+    """A contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _row_stride(t, same):

@@ -764,4 +764,199 @@ hm_status hyena_layer_step_bf16(const hm_desc *desc, const void *x, int64_t ldx,
     return err == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
+static hm_status check_linattn(const hm_linattn_desc *d) {
+    if (!d || d->abi_version != HM_ABI_VERSION || d->reserved != 0) return HM_ERR_INVALID_ARG;
+    if (d->act_dtype != HM_F32 && d->act_dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (d->batch < 0 || d->heads < 1 || d->q_heads < 1 || d->k_heads < 1 || d->v_heads < 1 || d->key_dim < 1 ||
+        d->value_dim < 1 || !std::isfinite(d->scale))
+        return HM_ERR_INVALID_ARG;
+    if (d->heads % d->q_heads != 0 || d->heads % d->k_heads != 0 || d->heads % d->v_heads != 0)
+        return HM_ERR_INVALID_ARG;
+    if (d->key_dim > HM_LINATTN_MAX_DIM || d->value_dim > HM_LINATTN_MAX_DIM) return HM_ERR_UNSUPPORTED;
+    if (d->batch > kMaxElems / d->heads || d->batch * d->heads > kMaxElems / (d->key_dim * d->value_dim))
+        return HM_ERR_INVALID_ARG;
+    return HM_OK;
+}
+
+static hm::LinAttnShape linattn_shape(const hm_linattn_desc *d) {
+    hm::LinAttnShape s;
+    s.B = d->batch;
+    s.H = d->heads;
+    s.qh = d->q_heads;
+    s.kh = d->k_heads;
+    s.vh = d->v_heads;
+    s.dk = (int)d->key_dim;
+    s.dv = (int)d->value_dim;
+    s.act = d->act_dtype == HM_BF16 ? hm::kBF16 : hm::kF32;
+    s.scale = d->scale;
+    return s;
+}
+
+// Activations, decay and states of a call over L tokens (1 for a generated token).
+static hm_status linattn_args(const hm_linattn_desc *d, int64_t L, const void *q, int64_t ld_q, const void *k,
+                              int64_t ld_k, const void *v, int64_t ld_v, const float *decay, int64_t ld_decay,
+                              void *y, int64_t ld_y, const float *state_in, float *state_out, hm::LinAttnArgs *a) {
+    const uintptr_t e = d->act_dtype == HM_BF16 ? 2 : 4;
+    if (L > 0) {
+        if (!q || !k || !v || !y) return HM_ERR_INVALID_ARG;
+        if (!aligned(q, e) || !aligned(k, e) || !aligned(v, e) || !aligned(y, e)) return HM_ERR_UNSUPPORTED;
+        if (ld_q < d->q_heads * d->key_dim || ld_k < d->k_heads * d->key_dim || ld_v < d->v_heads * d->value_dim ||
+            ld_y < d->heads * d->value_dim)
+            return HM_ERR_INVALID_ARG;
+        const int64_t rows = kMaxElems / L >= d->batch ? d->batch * L : kMaxElems;
+        for (int64_t ld : {ld_q, ld_k, ld_v, ld_y, ld_decay})
+            if (ld > 0 && rows > kMaxElems / ld) return HM_ERR_INVALID_ARG;
+    }
+    if (decay) {
+        if (ld_decay != 0 && ld_decay < d->heads) return HM_ERR_INVALID_ARG;
+        if (!aligned(decay, 4)) return HM_ERR_UNSUPPORTED;
+    }
+    if (!state_out) return HM_ERR_INVALID_ARG;
+    if (!aligned(state_out, 4) || (state_in && !aligned(state_in, 4))) return HM_ERR_UNSUPPORTED;
+    *a = hm::LinAttnArgs{};
+    a->s = linattn_shape(d);
+    a->L = L;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->ld_q = ld_q;
+    a->ld_k = ld_k;
+    a->ld_v = ld_v;
+    a->decay = decay;
+    a->ld_decay = ld_decay;
+    a->y = y;
+    a->ld_y = ld_y;
+    a->state_in = state_in;
+    a->state_out = state_out;
+    return HM_OK;
+}
+
+hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L, size_t *bytes) {
+    hm_status st = check_linattn(desc);
+    if (st != HM_OK) return st;
+    if (!bytes || L < 0 || L > kMaxElems) return HM_ERR_INVALID_ARG;
+    *bytes = desc->batch > 0 ? hm::linattn_workspace(linattn_shape(desc), L) : 0;
+    return HM_OK;
+}
+
+hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const int32_t *lengths, const void *q,
+                                int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                                const float *log_decay, int64_t ld_decay, void *y, int64_t ld_y,
+                                const float *state_in, float *state_out, void *workspace, size_t ws_bytes,
+                                void *stream) {
+    hm_status st = check_linattn(desc);
+    if (st != HM_OK) return st;
+    if (L < 0 || L > INT32_MAX / 2) return L < 0 ? HM_ERR_INVALID_ARG : HM_ERR_UNSUPPORTED;
+    if (desc->batch == 0) return HM_OK;
+    hm::LinAttnArgs a;
+    if ((st = linattn_args(desc, L, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_decay, y, ld_y, state_in, state_out,
+                           &a)) != HM_OK)
+        return st;
+    if (lengths && !aligned(lengths, 4)) return HM_ERR_UNSUPPORTED;
+    const size_t need = hm::linattn_workspace(a.s, L);
+    if (need > 0) {
+        if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
+        if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;
+    }
+    if (desc->batch * desc->heads > INT32_MAX / 64) return HM_ERR_UNSUPPORTED;  // grid limit
+    a.lengths = lengths;
+    a.ws = static_cast<unsigned char *>(workspace);
+    return hm::launch_linattn_prefill(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, int64_t ld_q, const void *k,
+                                    int64_t ld_k, const void *v, int64_t ld_v, const float *log_decay,
+                                    int64_t ld_decay, void *y, int64_t ld_y, const float *state_in,
+                                    const int32_t *src_rows, float *state_out, void *stream) {
+    hm_status st = check_linattn(desc);
+    if (st != HM_OK) return st;
+    if (desc->batch == 0) return HM_OK;
+    if (!state_in) return HM_ERR_INVALID_ARG;
+    hm::LinAttnArgs a;
+    if ((st = linattn_args(desc, 1, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_decay, y, ld_y, state_in, state_out,
+                           &a)) != HM_OK)
+        return st;
+    if (src_rows) {
+        if (state_in == state_out) return HM_ERR_INVALID_ARG;
+        if (!aligned(src_rows, 4)) return HM_ERR_UNSUPPORTED;
+    }
+    if (desc->batch * desc->heads > INT32_MAX / 64) return HM_ERR_UNSUPPORTED;  // grid limit
+    a.src_rows = src_rows;
+    return hm::launch_linattn_decode(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+static hm_status check_beams(int64_t groups, int64_t beams, int64_t vocab, int64_t select) {
+    if (groups < 0 || beams < 1 || vocab < 1 || select < 1 || beams > HM_BEAM_MAX || select > HM_BEAM_MAX)
+        return HM_ERR_INVALID_ARG;
+    if (vocab > INT32_MAX / beams || groups > INT32_MAX / 64 / beams) return HM_ERR_UNSUPPORTED;
+    if (groups * beams > (int64_t(1) << 42) / vocab) return HM_ERR_UNSUPPORTED;
+    if (select > beams * vocab) return HM_ERR_INVALID_ARG;
+    return HM_OK;
+}
+
+hm_status hyena_beam_select_workspace(int64_t groups, int64_t beams, int64_t vocab, int64_t select, size_t *bytes) {
+    const hm_status st = check_beams(groups, beams, vocab, select);
+    if (st != HM_OK) return st;
+    if (!bytes) return HM_ERR_INVALID_ARG;
+    *bytes = groups > 0 ? hm::beam_select_workspace(groups, beams, vocab, select) : 0;
+    return HM_OK;
+}
+
+hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_t select, int32_t dtype,
+                            const void *logits, int64_t ld, const float *scores, const uint8_t *finished,
+                            int64_t end_token, float *out_scores, int32_t *out_tokens, int32_t *out_parents,
+                            uint8_t *out_finished, void *workspace, size_t ws_bytes, void *stream) {
+    hm_status st = check_beams(groups, beams, vocab, select);
+    if (st != HM_OK) return st;
+    if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (ld < vocab || end_token < -1 || end_token >= vocab || (finished && end_token < 0)) return HM_ERR_INVALID_ARG;
+    if (groups == 0) return HM_OK;
+    if (!logits || !scores || !out_scores || !out_tokens || !out_parents) return HM_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype == HM_BF16 ? 2 : 4) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
+        !aligned(out_tokens, 4) || !aligned(out_parents, 4))
+        return HM_ERR_UNSUPPORTED;
+    if (groups * beams > kMaxElems / ld) return HM_ERR_INVALID_ARG;
+    const size_t need = hm::beam_select_workspace(groups, beams, vocab, select);
+    if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;
+    hm::BeamSelectArgs a;
+    a.groups = groups;
+    a.beams = beams;
+    a.vocab = vocab;
+    a.select = select;
+    a.act = dtype == HM_BF16 ? hm::kBF16 : hm::kF32;
+    a.logits = logits;
+    a.ld = ld;
+    a.scores = scores;
+    a.finished = finished;
+    a.end_token = end_token;
+    a.out_scores = out_scores;
+    a.out_tokens = out_tokens;
+    a.out_parents = out_parents;
+    a.out_finished = out_finished;
+    a.ws = static_cast<unsigned char *>(workspace);
+    return hm::launch_beam_select(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n, void *const *buffers,
+                             const int64_t *row_bytes, void *stream) {
+    const hm_status st = check_beams(groups, beams, 1, 1);
+    if (st != HM_OK) return st;
+    if (n < 0 || (n > 0 && (!buffers || !row_bytes))) return HM_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < n; ++i) {
+        if (row_bytes[i] < 0 || (groups > 0 && row_bytes[i] > kMaxElems / (groups * beams))) return HM_ERR_INVALID_ARG;
+        if (groups > 0 && row_bytes[i] > 0 && !buffers[i]) return HM_ERR_INVALID_ARG;
+    }
+    if (groups == 0 || n == 0) return HM_OK;
+    if (!parents) return HM_ERR_INVALID_ARG;
+    if (groups > 65535) return HM_ERR_UNSUPPORTED;  // grid limits
+    for (int64_t i = 0; i < n; ++i)
+        if (row_bytes[i] > int64_t(1) << 36) return HM_ERR_UNSUPPORTED;
+    if (!aligned(parents, 4)) return HM_ERR_UNSUPPORTED;
+    return hm::launch_beam_reorder(groups, beams, parents, n, buffers, row_bytes,
+                                   static_cast<hipStream_t>(stream)) == hipSuccess
+               ? HM_OK
+               : HM_ERR_HIP;
+}
+
 }  // extern "C"

@@ -340,6 +340,51 @@ struct AdamArgs {
 };
 hipError_t launch_distill_adam(const AdamArgs &a, hipStream_t stream);
 
+// Linear attention with a decay.
+struct LinAttnShape {
+    int64_t B, H, qh, kh, vh;
+    int dk, dv;
+    int act;
+    float scale;
+};
+struct LinAttnArgs {
+    LinAttnShape s;
+    int64_t L;             // tokens of a prompt
+    const int32_t *lengths;  // nullable
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    const float *decay;    // nullable
+    int64_t ld_decay;      // 0: one a head
+    void *y;
+    int64_t ld_y;
+    const float *state_in;  // nullable for a prompt
+    float *state_out;
+    const int32_t *src_rows;  // nullable; one token only
+    unsigned char *ws;
+};
+size_t linattn_workspace(const LinAttnShape &s, int64_t L);
+hipError_t launch_linattn_prefill(const LinAttnArgs &a, hipStream_t stream);
+hipError_t launch_linattn_decode(const LinAttnArgs &a, hipStream_t stream);
+
+// Beam search.
+struct BeamSelectArgs {
+    int64_t groups, beams, vocab, select;
+    int act;
+    const void *logits;
+    int64_t ld;
+    const float *scores;
+    const uint8_t *finished;  // nullable
+    int64_t end_token;
+    float *out_scores;
+    int32_t *out_tokens, *out_parents;
+    uint8_t *out_finished;    // nullable
+    unsigned char *ws;
+};
+size_t beam_select_workspace(int64_t groups, int64_t beams, int64_t vocab, int64_t select);
+hipError_t launch_beam_select(const BeamSelectArgs &a, hipStream_t stream);
+hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n, void *const *buffers,
+                               const int64_t *row_bytes, hipStream_t stream);
+
 // ---------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error; none synchronises.
 

@@ -527,6 +527,135 @@ hm_status hyena_modal_order(const float *h, int64_t H, int64_t L, int64_t n, dou
 hm_status hyena_modal_fit_init(const float *h, int64_t H, int64_t L, int64_t d, float r_max, float *poles,
                                float *residues, float *skip);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay, the matrix-state layer that hybrid stacks put
+ * beside the modal operator (the state-space duality post of the Telegram
+ * digest and the Based blog repost describe such layers; both keep a state of
+ * constant size, as the modal operator does).  Per batch row and head, with a
+ * state S [key_dim][value_dim]:
+ *     S_t = exp(a_t) S_{t-1} + k_t v_t^T,      y_t = scale * S_t^T q_t.
+ * ------------------------------------------------------------------------ */
+
+#define HM_LINATTN_MAX_DIM 256 /* largest key_dim and value_dim */
+
+/* Sizes: batch >= 0, heads >= 1 (one state and one decay each).  q, k and v may
+ * have fewer heads: q_heads, k_heads and v_heads divide heads, and head h reads
+ * head h * q_heads / heads of q (so neighbouring heads share), k and v alike. */
+typedef struct hm_linattn_desc {
+    int32_t abi_version; /* must be HM_ABI_VERSION */
+    int32_t act_dtype;   /* hm_dtype of q, k, v, y */
+    int64_t batch;
+    int64_t heads;
+    int64_t q_heads, k_heads, v_heads;
+    int64_t key_dim, value_dim; /* 1 .. HM_LINATTN_MAX_DIM */
+    float scale;                /* finite */
+    int32_t reserved;           /* 0 */
+} hm_linattn_desc;
+
+/* Workspace bytes of hyena_linattn_prefill for this descriptor and prompt
+ * length L >= 0 (0 is possible).  Pure host computation. */
+hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L, size_t *bytes);
+
+/*
+ * The recurrence over a prompt of L tokens, and the state after it.
+ *   lengths   [batch] int32 or NULL (every row has L tokens).  Row b's tokens
+ *             from lengths[b] on are not read (their contents do not matter),
+ *             do not move the state, and get y = 0.  A value outside 0 .. L
+ *             counts as the nearer of the two.
+ *   q         [batch][L][ld_q], head g's elements at g * key_dim ..; k the same
+ *             with k_heads and ld_k, v with v_heads, value_dim and ld_v.
+ *   log_decay float32 a: [heads] with ld_decay = 0 (one decay a head),
+ *             [batch][L][ld_decay] (one a token and head), or NULL (none).
+ *             a <= 0 is expected; a = -infinity forgets the state (a new
+ *             document begins there).  exp(a) below 1e-300 counts as 0.
+ *   y         [batch][L][ld_y], heads * value_dim columns.
+ *   state_in  [batch][heads][key_dim][value_dim] float32, or NULL for zero.
+ *   state_out the state after each row's last token (may equal state_in).
+ *   workspace 256-byte aligned scratch, hyena_linattn_prefill_workspace bytes.
+ * Sums and the state are float32.  The prompt runs in chunks on the matrix
+ * cores: decays inside a chunk are formed from float64 sums of a, float32
+ * operands keep about 24 significant bits, and of bfloat16 ones only what the
+ * chunk rounds on its way to y (never to the state) has fewer.
+ */
+hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const int32_t *lengths,
+                                const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *v, int64_t ld_v, const float *log_decay, int64_t ld_decay,
+                                void *y, int64_t ld_y, const float *state_in, float *state_out,
+                                void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One generated token for every batch row: the recurrence once, all float32.
+ *   q [batch][ld_q], k, v, y alike; log_decay [heads] with ld_decay = 0,
+ *   [batch][ld_decay], or NULL.
+ *   src_rows  [batch] int32 or NULL: row b continues row src_rows[b] of
+ *             state_in (the parent of a beam), so a search needs no pass that
+ *             reorders these states.  A value outside 0 .. batch-1 counts as b.
+ *   state_in, state_out  as in hyena_linattn_prefill.  state_out may equal
+ *             state_in only without src_rows (else HM_ERR_INVALID_ARG); they
+ *             must not overlap otherwise.
+ */
+hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, int64_t ld_q,
+                                    const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                                    const float *log_decay, int64_t ld_decay, void *y, int64_t ld_y,
+                                    const float *state_in, const int32_t *src_rows, float *state_out,
+                                    void *stream);
+
+/* ------------------------------------------------------------------------
+ * Beam search over generated tokens: the choice of the continuations, and the
+ * move of the layers' states to where their beams went.
+ * ------------------------------------------------------------------------ */
+
+#define HM_BEAM_MAX 64 /* most beams of a group, and most continuations selected */
+
+/*
+ * For every group of beams, the `select` best continuations (beam k, token v) by
+ *     score = scores[k] + log softmax(logits[k])[v],
+ * best first; equal scores in the order of (k, v).
+ *   logits    [groups * beams][ld] of dtype (hm_dtype), vocab columns used.
+ *             -infinity takes a token out; NaN counts as -infinity.  +infinity:
+ *             such tokens share the whole probability of their row.
+ *   scores    [groups][beams] float32; -infinity for a beam that is not alive
+ *             (its logits are not read).  Not NaN or +infinity.
+ *   finished  [groups][beams] bytes or NULL: a nonzero beam has ended.  Its
+ *             logits are not read; its one continuation is end_token at its own
+ *             score, all others have score -infinity.
+ *   end_token in 0 .. vocab-1, or -1 for none (then finished must be NULL).
+ *   out_scores, out_tokens, out_parents (beam in the group), out_finished (the
+ *   parent had ended, or the token is end_token): [groups][select] float32,
+ *   int32, int32, bytes.  out_finished may be NULL; out_scores may equal scores.
+ * Continuations of score -infinity are returned only where fewer than select
+ * have another.  Softmax statistics and scores are float32; two continuations
+ * whose scores differ by no more than their rounding may come in either order.
+ *   1 <= beams, select <= HM_BEAM_MAX, select <= beams * vocab (else
+ *   HM_ERR_INVALID_ARG), beams * vocab < 2^31, groups * beams < 2^31 / 64,
+ *   groups * beams * vocab <= 2^42 (else HM_ERR_UNSUPPORTED).  ld >= vocab.
+ *   workspace: hyena_beam_select_workspace bytes, 256-byte aligned, scratch.
+ */
+hm_status hyena_beam_select_workspace(int64_t groups, int64_t beams, int64_t vocab, int64_t select,
+                                      size_t *bytes);
+
+hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_t select, int32_t dtype,
+                            const void *logits, int64_t ld, const float *scores, const uint8_t *finished,
+                            int64_t end_token, float *out_scores, int32_t *out_tokens,
+                            int32_t *out_parents, uint8_t *out_finished, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * Rows of states moved to their beams, in place, for n buffers:
+ *     buffer row g * beams + k  <-  old row g * beams + parents[g][k].
+ *   parents   [groups][beams] int32 on the device.  A value outside
+ *             0 .. beams-1 leaves its row as it is.
+ *   buffers   n device pointers, row_bytes n sizes, both HOST arrays (read
+ *             before the call returns): buffer i has groups * beams rows of
+ *             row_bytes[i] bytes, one after the other (a modal state, its
+ *             deferred u_prev and rho, a linear-attention state, ...).
+ * Rows that stay are neither read nor written.  Buffers must not overlap.
+ * n < 0, row_bytes[i] < 0, null pointers -> HM_ERR_INVALID_ARG; groups > 65535,
+ * row_bytes[i] > 2^36 -> HM_ERR_UNSUPPORTED.
+ */
+hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n,
+                             void *const *buffers, const int64_t *row_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,153 @@
+"""Linear attention's and beam search's entry points without a GPU: every refusal
+comes from the host checks, before any HIP call, and empty problems succeed."""
+
+import ctypes
+import math
+import os
+
+import pytest
+
+from distilled_modal_ssm_amd import binding as hb
+
+FAKE = 0x10000  # never dereferenced: every call below ends in the host checks
+BAD, NO, WS = hb.HM_ERR_INVALID_ARG, hb.HM_ERR_UNSUPPORTED, hb.HM_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(hb.LIB_PATH):
+        from distilled_modal_ssm_amd import build
+        build.build()
+    return hb.load()
+
+
+def _refused(status, call, *args, **kw):
+    with pytest.raises(hb.HMError) as e:
+        call(*args, **kw)
+    assert e.value.status == status, (kw, e.value)
+
+
+def _desc(**kw):
+    base = dict(batch=2, heads=8, key_dim=64, value_dim=48, act_dtype=hb.HM_BF16, scale=0.125)
+    later = {k: kw.pop(k) for k in ("abi_version", "reserved") if k in kw}
+    d = hb.make_linattn_desc(**{**base, **kw})
+    for k, v in later.items():
+        setattr(d, k, v)
+    return d
+
+
+DESCS = [
+    (dict(abi_version=9), BAD), (dict(reserved=1), BAD), (dict(act_dtype=5), NO), (dict(batch=-1), BAD),
+    (dict(heads=0), BAD), (dict(q_heads=3), BAD), (dict(k_heads=16), BAD), (dict(v_heads=0), BAD),
+    (dict(key_dim=0), BAD), (dict(key_dim=257), NO), (dict(value_dim=300), NO), (dict(value_dim=-1), BAD),
+    (dict(scale=math.inf), BAD), (dict(scale=math.nan), BAD), (dict(batch=1 << 40), BAD),
+]
+
+
+def _prefill(desc, L=100, **kw):
+    a = dict(lengths=None, q=FAKE, ld_q=512, k=FAKE, ld_k=512, v=FAKE, ld_v=384, log_decay=FAKE, ld_decay=8, y=FAKE,
+             ld_y=384, state_in=None, state_out=FAKE, workspace=None, ws_bytes=0, stream=0)
+    hb.hyena_linattn_prefill(desc, L, **{**a, **kw})
+
+
+def _token(desc, **kw):
+    a = dict(q=FAKE, ld_q=512, k=FAKE, ld_k=512, v=FAKE, ld_v=384, log_decay=FAKE, ld_decay=0, y=FAKE, ld_y=384,
+             state_in=FAKE, src_rows=None, state_out=FAKE, stream=0)
+    hb.hyena_linattn_decode_step(desc, **{**a, **kw})
+
+
+@pytest.mark.parametrize("kw,status", DESCS)
+def test_linattn_descriptor(kw, status):
+    d = _desc(**kw)
+    _refused(status, hb.hyena_linattn_prefill_workspace, d, 10)
+    _refused(status, _prefill, d)
+    _refused(status, _token, d)
+
+
+ROWS = [
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD), (dict(y=None), BAD), (dict(state_out=None), BAD),
+    (dict(q=FAKE + 1), NO), (dict(y=FAKE + 1), NO), (dict(state_out=FAKE + 2), NO), (dict(log_decay=FAKE + 2), NO),
+    (dict(ld_q=511), BAD), (dict(ld_k=0), BAD), (dict(ld_v=-384), BAD), (dict(ld_y=383), BAD), (dict(ld_decay=7), BAD),
+    (dict(ld_decay=-1), BAD), (dict(ld_q=1 << 50), BAD), (dict(state_in=FAKE + 1), NO),
+]
+
+
+@pytest.mark.parametrize("kw,status", ROWS)
+def test_linattn_arguments(kw, status):
+    _refused(status, _prefill, _desc(), **kw)
+    _refused(status, _token, _desc(), **kw)
+
+
+def test_linattn_own_arguments():
+    _refused(BAD, _prefill, _desc(), L=-1)
+    _refused(NO, _prefill, _desc(), L=1 << 40, ld_decay=0)
+    _refused(NO, _prefill, _desc(), lengths=FAKE + 2)
+    _refused(BAD, hb.hyena_linattn_prefill_workspace, _desc(), -1)
+    _refused(BAD, _token, _desc(), state_in=None)
+    _refused(BAD, _token, _desc(), src_rows=FAKE)  # in place
+    _refused(NO, _token, _desc(), src_rows=FAKE + 1, state_out=2 * FAKE)
+    st = hb.load().hyena_linattn_prefill_workspace(ctypes.byref(_desc()), 10, None)
+    assert st == BAD
+
+
+def test_linattn_workspace():
+    """A long prompt of few heads is cut into segments, whose states need memory; a missing or small one is refused."""
+    d = _desc(batch=1, heads=2, key_dim=128, value_dim=128)
+    n = hb.hyena_linattn_prefill_workspace(d, 60000)
+    assert n >= 0 and hb.hyena_linattn_prefill_workspace(_desc(batch=0), 60000) == 0
+    assert hb.hyena_linattn_prefill_workspace(d, 1) == 0
+    if n:
+        _refused(WS, _prefill, d, L=60000, workspace=None)
+        _refused(WS, _prefill, d, L=60000, workspace=FAKE, ws_bytes=n - 1)
+        _refused(NO, _prefill, d, L=60000, workspace=FAKE + 16, ws_bytes=n)
+
+
+def test_empty_problems_need_no_gpu():
+    _prefill(_desc(batch=0), q=None, k=None, v=None, y=None, state_out=None)
+    _token(_desc(batch=0), q=None, k=None, v=None, y=None, state_in=None, state_out=None)
+    hb.hyena_beam_select(0, 4, 100, 4, hb.HM_F32, None, 100, None, None, -1, None, None, None, None, None, 0, stream=0)
+    hb.hyena_beam_reorder(0, 4, None, [], [], stream=0)
+    hb.hyena_beam_reorder(3, 4, None, [], [], stream=0)
+
+
+SIZES = [(-1, 4, 100, 4, BAD), (1, 0, 100, 4, BAD), (1, 65, 100, 4, BAD), (1, 4, 0, 4, BAD), (1, 4, 100, 0, BAD),
+         (1, 4, 100, 65, BAD), (1, 1, 3, 4, BAD), (1, 64, 1 << 26, 4, NO), (1 << 30, 4, 100, 4, NO),
+         (1 << 22, 4, 1 << 24, 4, NO)]
+
+
+@pytest.mark.parametrize("G,K,V,n,status", SIZES)
+def test_beam_sizes(G, K, V, n, status):
+    _refused(status, hb.hyena_beam_select_workspace, G, K, V, n)
+    _refused(status, hb.hyena_beam_select, G, K, V, n, hb.HM_F32, FAKE, V, FAKE, None, -1, FAKE, FAKE, FAKE, FAKE, FAKE,
+             1 << 40, stream=0)
+
+
+def _select(**kw):
+    a = dict(groups=2, beams=4, vocab=1000, select=4, dtype=hb.HM_F32, logits=FAKE, ld=1000, scores=FAKE, finished=None,
+             end_token=-1, out_scores=FAKE, out_tokens=FAKE, out_parents=FAKE, out_finished=FAKE, workspace=FAKE,
+             ws_bytes=1 << 30, stream=0)
+    hb.hyena_beam_select(**{**a, **kw})
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=3), NO), (dict(ld=999), BAD), (dict(end_token=1000), BAD), (dict(end_token=-2), BAD),
+    (dict(finished=FAKE), BAD), (dict(logits=None), BAD), (dict(scores=None), BAD), (dict(out_scores=None), BAD),
+    (dict(out_tokens=None), BAD), (dict(out_parents=None), BAD), (dict(logits=FAKE + 2), NO),
+    (dict(dtype=hb.HM_BF16, logits=FAKE + 1), NO), (dict(scores=FAKE + 1), NO), (dict(out_parents=FAKE + 2), NO),
+    (dict(workspace=None), WS), (dict(ws_bytes=8), WS), (dict(workspace=FAKE + 8), NO), (dict(ld=1 << 50), BAD),
+])
+def test_beam_select_arguments(kw, status):
+    _refused(status, _select, **kw)
+
+
+@pytest.mark.parametrize("args,status", [
+    ((2, 4, None, [FAKE], [16]), BAD), ((2, 4, FAKE + 1, [FAKE], [16]), NO), ((2, 4, FAKE, [None], [16]), BAD),
+    ((2, 4, FAKE, [FAKE], [-1]), BAD), ((-2, 4, FAKE, [FAKE], [16]), BAD), ((2, 65, FAKE, [FAKE], [16]), BAD),
+    ((65536, 4, FAKE, [FAKE], [16]), NO), ((1, 4, FAKE, [FAKE], [(1 << 36) + 1]), NO), ((2, 4, FAKE, [FAKE], [1 << 60]), BAD),
+])
+def test_beam_reorder_arguments(args, status):
+    _refused(status, hb.hyena_beam_reorder, *args, stream=0)
+    with pytest.raises(ValueError):
+        hb.hyena_beam_reorder(2, 4, FAKE, [FAKE], [], stream=0)
+    assert hb.load().hyena_beam_reorder(2, 4, FAKE, -1, None, None, None) == BAD
+    assert hb.load().hyena_beam_reorder(2, 4, FAKE, 1, None, None, None) == BAD
