@@ -1,6 +1,39 @@
 // linattn.hip -- linear attention with a decay: the recurrence over a prompt
 // and for one generated token.  Per batch row and head, S [dk][dv]:
 //     S_t = exp(a_t) S_{t-1} + k_t v_t^T,      y_t = scale * S_t^T q_t.
+//
+// Prompt.  In chunks of C tokens, with S the state entering the chunk, G_t the
+// sum of a up to and with token t of the chunk, and E = G at the chunk's end:
+//     y_t = scale ( exp(G_t) S^T q_t + sum_{s<=t} exp(G_t - G_s) (q_t . k_s) v_s )
+//     S'  = exp(E) S + sum_s k_s (exp(E - G_s) v_s)^T
+// which are four products on the matrix cores: K Q^T (C x C), the weighted
+// result times V, S^T Q^T, and K^T V with V weighted.  All exponents are of
+// sums over later tokens, at most 0 where a is, so nothing overflows.
+//
+// Precision.  bfloat16 parts of operands, float32 accumulation, 16x16x32 MFMAs:
+//   q, k, v      one part (bfloat16) or three (float32: 24 bits);
+//   weighted V   three parts, for both types: the state keeps float32 precision
+//                over any length;
+//   S, weighted K Q^T  as operands of y only: three parts (float32), one
+//                (bfloat16: each adds a rounding like that of y itself, so y's
+//                error is at most 1.41 of the one its own rounding makes);
+//   products of parts i and j are left out where i + j > 2 (below 2^-24).
+// G is summed in float64 and the state's factor exp(E) has two float32 parts: a
+// head that forgets slowly multiplies by the same factor for thousands of
+// chunks' worth of tokens, so its rounding would add up.
+//
+// Workgroup: a batch row, a head and 64 value columns, 16 a wave.  The wave's
+// part of the state, [dk][16], stays in the accumulators of the K^T V products
+// from chunk to chunk (lane = value column, registers = key rows).  The key rows
+// of an MFMA tile are chosen so that two tiles' registers are, converted in
+// place, the S^T operand of the next chunk (lane group g: key rows 8g .. 8g+7 of
+// each 32): the state never passes through the LDS.  K and V come out of the LDS
+// transposed (ds_read_b64_tr_b16).
+//
+// A prompt of too few rows and heads to fill the GPU is cut into segments of
+// chunks: the state-only form of the kernel runs over every segment but the last
+// from a zero state (k and v only), a scan joins the states, and the full form
+// starts every segment from its own.
 #include "hm_internal.hpp"
 
 namespace hm {
@@ -13,70 +46,404 @@ __device__ __forceinline__ float bound_decay(float a) { return a < -1000.f ? -10
 
 // ------------------------------------------------------------------ prompt
 
-constexpr int kTok = 16;   // tokens staged at a time
-constexpr int kCols = 64;  // value columns of a workgroup, one a lane
-constexpr int kRows = 64;  // key rows of a wave: four waves cover 256
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// One workgroup for a batch row, head and 64 value columns: token after token,
-// lane = column, wave = 64 key rows whose state the lane holds in registers.
-template <int ACT>
-__global__ __launch_bounds__(kThreads) void linattn_scan_kernel(LinAttnArgs a) {
+// Sum of the products of parts i of a and j of b, the smallest first.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mfma(const uint4 (&a)[NA], const uint4 (&b)[NB], f32x4 c) {
+    constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+    for (int sum = N - 1; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = sum - i;
+            if (j >= 0 && j < NB)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
+                                                            __builtin_bit_cast(bf16x8, b[j]), c, 0, 0, 0);
+        }
+    return c;
+}
+
+// x, y -> their leading bfloat16 parts packed; x, y become what is left.
+__device__ __forceinline__ uint32_t take_part(float &x, float &y) {
+    const uint32_t w = pack_bf16x2(x, y);
+    x -= bf16_lo(w);
+    y -= bf16_hi(w);
+    return w;
+}
+
+template <int N>
+__device__ __forceinline__ void split8(float (&x)[8], uint4 (&out)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        out[n] = make_uint4(take_part(x[0], x[1]), take_part(x[2], x[3]), take_part(x[4], x[5]), take_part(x[6], x[7]));
+}
+
+// 16 bytes of a row from column c on, of n columns (zero past them).  G: bytes
+// that every address and the row's width are a multiple of (16, 8 or an element).
+template <int ACT, int G>
+__device__ __forceinline__ uint4 load_piece(const typename Act<ACT>::T *row, int c, int n) {
+    constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if constexpr (G == 16) {
+        if (c < n) w = *reinterpret_cast<const uint4 *>(row + c);
+    } else if constexpr (G == 8) {
+        if (c < n) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + c);
+            w.x = x.x;
+            w.y = x.y;
+        }
+        if (c + PER / 2 < n) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + c + PER / 2);
+            w.z = x.x;
+            w.w = x.y;
+        }
+    } else {
+        uint32_t x[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (c + e < n) {
+                if constexpr (EB == 2)
+                    x[e / 2] |= (uint32_t)row[c + e] << (16 * (e & 1));
+                else
+                    x[e] = __float_as_uint(row[c + e]);
+            }
+        w = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    return w;
+}
+
+// A piece into its place in the parts' LDS planes.
+template <int ACT, int PLANE>
+__device__ __forceinline__ void store_piece(uint16_t *at, const uint4 w) {
+    if constexpr (ACT == kBF16) {
+        *reinterpret_cast<uint4 *>(at) = w;
+    } else {
+        float x = __uint_as_float(w.x), y = __uint_as_float(w.y), z = __uint_as_float(w.z), u = __uint_as_float(w.w);
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const uint32_t lo = take_part(x, y);
+            *reinterpret_cast<uint2 *>(at + n * PLANE) = make_uint2(lo, take_part(z, u));
+        }
+    }
+}
+
+// Four rows of 16 columns of a plane, transposed: lane i of a group of 16 gets
+// column i.  Each lane names 4 columns of a row: lanes 4j .. 4j+3 row j.
+__device__ __forceinline__ uint2 read_transposed(const uint16_t *at) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+}
+
+constexpr int kVT = 64;  // value columns of a workgroup
+
+struct LinAttnPlan {
+    int64_t segs, seg_chunks;   // segments of the prompt, and chunks of each
+    int chunk;                  // tokens of a chunk
+    int vtiles;                 // workgroups of a row and head
+    size_t off_decay, bytes;    // float [B H][segs][dk][dv] states; float2 [B H][segs] segment factors
+};
+
+template <int ACT, int DK> struct ChunkGeom {
+    static constexpr int C = (ACT == kBF16 && DK <= 128) ? 64 : 32;
+    static constexpr int NP = ACT == kBF16 ? 1 : 3;  // parts of q, k, v, and of what y's products round
+    static constexpr int EB = Act<ACT>::kBytes;
+    // LDS rows in elements: K's are 20 or 44 words past a multiple of 64, so that
+    // the transposed reads' four rows of four 16-byte steps spread over the banks
+    static constexpr int QS = DK + 8;
+    static constexpr int KS = DK + (DK == 32 ? 8 : DK == 64 ? 24 : 40);
+    static constexpr int VS = kVT + 8, PS = C + 8;
+    static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
+    static constexpr int kBytes = 2 * NP * (QP + KP + VP + PP) + C * 16 + 16;
+};
+
+template <int ACT, int DK, int G, bool FULL>
+__global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
     using T = typename Act<ACT>::T;
-    __shared__ float qs[kTok][256], ks[kTok][256], vs[kTok][kCols], as[kTok], part[4][kTok][kCols];
-    const int64_t b = blockIdx.x / a.s.H, h = blockIdx.x - b * a.s.H;
-    const int v0 = blockIdx.y * kCols, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int dk = a.s.dk, dv = a.s.dv, col = v0 + lane;
-    const T *q = static_cast<const T *>(a.q) + b * a.L * a.ld_q + h * a.s.qh / a.s.H * dk;
-    const T *k = static_cast<const T *>(a.k) + b * a.L * a.ld_k + h * a.s.kh / a.s.H * dk;
-    const T *v = static_cast<const T *>(a.v) + b * a.L * a.ld_v + h * a.s.vh / a.s.H * dv;
-    T *y = static_cast<T *>(a.y) + b * a.L * a.ld_y + h * dv;
-    const int64_t sbase = (b * a.s.H + h) * (int64_t)dk * dv;
+    using M = ChunkGeom<ACT, DK>;
+    constexpr int C = M::C, NP = M::NP, PER = 16 / M::EB;
+    constexpr int RP = DK / PER, NQ = C * RP / kThreads, RSTEP = kThreads / RP;     // q, k pieces of a row, a thread
+    constexpr int VP = kVT / PER, NV = C * VP / kThreads, VSTEP = kThreads / VP;    // v pieces
+    constexpr int TT = C / 16, KK = C / 32, PAIRS = DK / 32;
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint16_t *Qs = reinterpret_cast<uint16_t *>(smem), *Ks = Qs + NP * M::QP, *Vs = Ks + NP * M::KP,
+             *Ps = Vs + NP * M::VP;
+    double *Gs = reinterpret_cast<double *>(Ps + NP * M::PP);
+    float *from_start = reinterpret_cast<float *>(Gs + C), *to_end = from_start + C, *factor = to_end + C;
+
+    // neighbouring value tiles of a head and segment on one XCD (workgroups go
+    // round the eight by their index): they read the same q and k
+    const int64_t units = a.s.B * a.s.H * p.segs;
+    const int64_t local = blockIdx.x >> 3, unit = local / p.vtiles * 8 + (blockIdx.x & 7);
+    if (unit >= units) return;
+    const int vt = (int)(local % p.vtiles);
+    const int64_t bh = unit / p.segs, seg = unit - bh * p.segs, b = bh / a.s.H, h = bh - b * a.s.H;
+    if (!FULL && seg == p.segs - 1) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15,
+              lg = lane >> 4;
+    const int dk = a.s.dk, dv = a.s.dv, v0 = vt * kVT, vcols = dv - v0 < kVT ? dv - v0 : kVT;
     int64_t len = a.L;
     if (a.lengths) len = a.lengths[b] < 0 ? 0 : a.lengths[b] < a.L ? a.lengths[b] : a.L;
-    float S[kRows];
+    const int64_t begin = seg * p.seg_chunks * C, end = begin + p.seg_chunks * C < a.L ? begin + p.seg_chunks * C : a.L;
+    const int64_t rows = len <= begin ? 0 : (len < end ? len : end) - begin;  // tokens of this segment
+
+    const T *q = static_cast<const T *>(a.q) + (b * a.L + begin) * a.ld_q + h * a.s.qh / a.s.H * dk;
+    const T *k = static_cast<const T *>(a.k) + (b * a.L + begin) * a.ld_k + h * a.s.kh / a.s.H * dk;
+    const T *v = static_cast<const T *>(a.v) + (b * a.L + begin) * a.ld_v + h * a.s.vh / a.s.H * dv + v0;
+    T *y = static_cast<T *>(a.y) + (b * a.L + begin) * a.ld_y + h * dv + v0;
+    const float *decay = a.decay ? a.decay + (a.ld_decay ? (b * a.L + begin) * a.ld_decay : 0) + h : nullptr;
+    const int64_t cells = (int64_t)dk * dv;
+
+    // the state: tile 2P + u, register r = key row 32 P + 8 lg + 4 u + r, value column li of the wave
+    const int col = 16 * wave + li;
+    f32x4 S[2 * PAIRS];
+    {
+        const float *from = nullptr;
+        if (FULL) {
+            if (p.segs > 1)
+                from = reinterpret_cast<const float *>(a.ws) + (bh * p.segs + seg) * cells;
+            else if (a.state_in)
+                from = a.state_in + bh * cells;
+        }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int row = wave * kRows + i;
-        S[i] = a.state_in && row < dk && col < dv ? a.state_in[sbase + (int64_t)row * dv + col] : 0.f;
+        for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
+                S[t][r] = from && row < dk && col < vcols ? from[(int64_t)row * dv + v0 + col] : 0.f;
+            }
     }
-    for (int64_t t0 = 0; t0 < a.L; t0 += kTok) {
-        __syncthreads();
-        for (int i = tid; i < kTok * 256; i += kThreads) {
-            const int t = i / 256, c = i % 256;
-            const bool in = t0 + t < len && c < dk;
-            qs[t][c] = in ? Act<ACT>::ld(q + (t0 + t) * a.ld_q + c) : 0.f;
-            ks[t][c] = in ? Act<ACT>::ld(k + (t0 + t) * a.ld_k + c) : 0.f;
-            if (c < kCols)
-                vs[t][c] = t0 + t < len && v0 + c < dv ? Act<ACT>::ld(v + (t0 + t) * a.ld_v + v0 + c) : 0.f;
-            if (c == 0) {
-                float d = 0.f;
-                if (a.decay && t0 + t < len)
-                    d = a.decay[a.ld_decay ? (b * a.L + t0 + t) * a.ld_decay + h : h];
-                as[t] = expf(bound_decay(d));
+
+    // tokens of the next chunk, on their way
+    const int qr = tid / RP, qc = tid % RP * PER, vr = tid / VP, vc = tid % VP * PER;
+    uint4 rq[NQ], rk[NQ], rv[NV];
+    float ra = 0.f;
+    auto fetch = [&](int64_t t0) {
+        const int64_t n = rows - t0;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const int r = qr + i * RSTEP;
+            rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
+            if (r < n) {
+                if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
+                rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
             }
         }
-        __syncthreads();
-        for (int t = 0; t < kTok; ++t) {
-            float o = 0.f;
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                S[i] = fmaf(as[t], S[i], ks[t][wave * kRows + i] * vs[t][lane]);
-                o = fmaf(qs[t][wave * kRows + i], S[i], o);
-            }
-            part[wave][t][lane] = o;
+        for (int i = 0; i < NV; ++i) {
+            const int r = vr + i * VSTEP;
+            rv[i] = make_uint4(0, 0, 0, 0);
+            if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
         }
+        ra = 0.f;
+        if (wave == 0 && lane < n && lane < C && decay) ra = bound_decay(decay[(t0 + lane) * a.ld_decay]);
+    };
+
+    // tiles above the diagonal that the products read: zero, once
+    if (FULL)
+        for (int i = tid; i < NP * M::PP; i += kThreads) Ps[i] = 0;
+    fetch(0);
+    double total = 0.0;
+    for (int64_t t0 = 0; t0 < rows; t0 += C) {
+        __syncthreads();  // the chunk before is done with the LDS
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            if (FULL) store_piece<ACT, M::QP>(Qs + (qr + i * RSTEP) * M::QS + qc, rq[i]);
+            store_piece<ACT, M::KP>(Ks + (qr + i * RSTEP) * M::KS + qc, rk[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) store_piece<ACT, M::VP>(Vs + (vr + i * VSTEP) * M::VS + vc, rv[i]);
+        if (wave == 0) {
+            double g = ra;
+#pragma unroll
+            for (int d = 1; d < C; d <<= 1) {
+                const double o = __shfl_up(g, d);
+                if (lane >= d) g += o;
+            }
+            const double e = __shfl(g, C - 1);
+            total += e;
+            if (lane < C) {
+                Gs[lane] = g;
+                from_start[lane] = expf((float)g);
+                to_end[lane] = expf((float)(e - g));
+            }
+            if (lane == C - 1) {
+                const double f = exp(e);
+                factor[0] = (float)f;
+                factor[1] = (float)(f - (double)(float)f);
+            }
+        }
+        fetch(t0 + C);
         __syncthreads();
-        for (int i = tid; i < kTok * kCols; i += kThreads) {
-            const int t = i / kCols, c = i % kCols;
-            if (t0 + t < a.L && v0 + c < dv)
-                Act<ACT>::st(y + (t0 + t) * a.ld_y + v0 + c,
-                             a.s.scale * (part[0][t][c] + part[1][t][c] + part[2][t][c] + part[3][t][c]));
+
+        f32x4 acc[TT];
+        if (FULL) {
+            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t: tiles (i, j) of 16 s x 16 t, i <= j
+#pragma unroll
+            for (int n = 0; n < TT * (TT + 1) / 2; ++n) {
+                if ((n & 3) != wave) continue;
+                const int j = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, i = n - j * (j + 1) / 2;
+                f32x4 x4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int pr = 0; pr < PAIRS; ++pr) {
+                    uint4 ka[NP], qb[NP];
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) {
+                        ka[w] = *reinterpret_cast<const uint4 *>(Ks + w * M::KP + (16 * i + li) * M::KS + 32 * pr + 8 * lg);
+                        qb[w] = *reinterpret_cast<const uint4 *>(Qs + w * M::QP + (16 * j + li) * M::QS + 32 * pr + 8 * lg);
+                    }
+                    x4 = mfma(ka, qb, x4);
+                }
+                const int t = 16 * j + li, s = 16 * i + 4 * lg;
+                const double gt = Gs[t];
+                float x[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = s + r <= t ? x4[r] * expf((float)(gt - Gs[s + r])) : 0.f;
+#pragma unroll
+                for (int w = 0; w < NP; ++w) {
+                    const uint32_t lo = take_part(x[0], x[1]);
+                    *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(x[2], x[3]));
+                }
+            }
+            // exp(G_t) S^T q_t
+#pragma unroll
+            for (int j = 0; j < TT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int pr = 0; pr < PAIRS; ++pr) {
+                float x[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) x[r] = S[2 * pr + r / 4][r % 4];
+                uint4 sa[NP];
+                split8(x, sa);
+#pragma unroll
+                for (int j = 0; j < TT; ++j) {
+                    uint4 qb[NP];
+#pragma unroll
+                    for (int w = 0; w < NP; ++w)
+                        qb[w] = *reinterpret_cast<const uint4 *>(Qs + w * M::QP + (16 * j + li) * M::QS + 32 * pr + 8 * lg);
+                    acc[j] = mfma(sa, qb, acc[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < TT; ++j) acc[j] *= from_start[16 * j + li];
+            __syncthreads();
+        }
+        // V of this wave's columns as an operand: value column li, tokens 32 kk + 8 lg + 0..7
+        uint4 va[KK][NP];
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int w = 0; w < NP; ++w) {
+                const uint16_t *at = Vs + w * M::VP + (32 * kk + 8 * lg + (li >> 2)) * M::VS + 16 * wave + 4 * (li & 3);
+                const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::VS);
+                va[kk][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+        if (FULL) {
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+#pragma unroll
+                for (int kk = 0; kk <= j / 2; ++kk) {
+                    uint4 pb[NP];
+#pragma unroll
+                    for (int w = 0; w < NP; ++w)
+                        pb[w] = *reinterpret_cast<const uint4 *>(Ps + w * M::PP + (16 * j + li) * M::PS + 32 * kk + 8 * lg);
+                    acc[j] = mfma(va[kk], pb, acc[j]);
+                }
+                const int64_t t = t0 + 16 * j + li;
+                const int c = 16 * wave + 4 * lg;
+                if (t < end - begin && c < vcols) {
+                    const f32x4 o = acc[j] * a.s.scale;
+                    T *at = y + t * a.ld_y + c;
+                    if (G == 16 || (G == 8 && ACT == kBF16)) {
+                        if constexpr (ACT == kBF16)
+                            *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                        else
+                            *reinterpret_cast<float4 *>(at) = make_float4(o[0], o[1], o[2], o[3]);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (c + r < vcols) Act<ACT>::st(at + r, o[r]);
+                    }
+                }
+            }
+        }
+        // the state
+        const float f0 = factor[0], f1 = factor[1];
+#pragma unroll
+        for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[t][r] = fmaf(S[t][r], f0, S[t][r] * f1);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            float x[8];
+            const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&va[kk][0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = bf16_lo(w0[e]);
+                x[2 * e + 1] = bf16_hi(w0[e]);
+                if constexpr (NP == 3) {
+                    const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
+                    const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
+                    x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
+                    x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= to_end[32 * kk + 8 * lg + e];
+            uint4 vb[3];
+            split8(x, vb);
+#pragma unroll
+            for (int t = 0; t < 2 * PAIRS; ++t) {
+                uint4 ka[NP];
+#pragma unroll
+                for (int w = 0; w < NP; ++w) {
+                    const uint16_t *at = Ks + w * M::KP + (32 * kk + 8 * lg + (li >> 2)) * M::KS + 16 * (t & ~1) +
+                                         8 * (li & 3) + 4 * (t & 1);
+                    const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::KS);
+                    ka[w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+                S[t] = mfma(ka, vb, S[t]);
+            }
         }
     }
+    if (FULL) {  // rows past the tokens
+        const int64_t done = (rows + C - 1) / C * C, n = end - begin - done;
+        for (int64_t i = tid; i < n * vcols; i += kThreads)
+            Act<ACT>::st(y + (done + i / vcols) * a.ld_y + i % vcols, 0.f);
+    }
+    float *to = FULL ? a.state_out + bh * cells : reinterpret_cast<float *>(a.ws) + (bh * p.segs + seg + 1) * cells;
+    if (!FULL || seg == p.segs - 1) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int row = wave * kRows + i;
-        if (row < dk && col < dv) a.state_out[sbase + (int64_t)row * dv + col] = S[i];
+        for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
+                if (row < dk && col < vcols) to[(int64_t)row * dv + v0 + col] = S[t][r];
+            }
+    }
+    if (!FULL && vt == 0 && tid == 0) {
+        const double f = exp(total);
+        reinterpret_cast<float2 *>(a.ws + p.off_decay)[bh * p.segs + seg] =
+            make_float2((float)f, (float)(f - (double)(float)f));
+    }
+}
+
+// States entering the segments: slot 0 the first state, slot s + 1 (which holds
+// segment s's own end state) the state after segment s.
+__global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinAttnArgs a, LinAttnPlan p) {
+    const int64_t cells = (int64_t)a.s.dk * a.s.dv, i = (int64_t)blockIdx.y * kThreads + threadIdx.x;
+    const int64_t bh = blockIdx.x;
+    if (i >= cells) return;
+    float *slot = reinterpret_cast<float *>(a.ws) + bh * p.segs * cells + i;
+    const float2 *factor = reinterpret_cast<const float2 *>(a.ws + p.off_decay) + bh * p.segs;
+    float x = a.state_in ? a.state_in[bh * cells + i] : 0.f;
+    slot[0] = x;
+    for (int64_t s = 1; s < p.segs; ++s) {
+        const float2 f = factor[s - 1];
+        x = fmaf(x, f.x, fmaf(x, f.y, slot[s * cells]));
+        slot[s * cells] = x;
     }
 }
 
@@ -121,17 +488,85 @@ __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a) 
     }
 }
 
+// Padded key width, and the granule of 16, 8 bytes or an element that all rows allow.
+int padded_dk(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+
+LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
+    LinAttnPlan p;
+    p.chunk = s.act == kBF16 && s.dk <= 128 ? 64 : 32;
+    p.vtiles = (s.dv + kVT - 1) / kVT;
+    const int64_t chunks = (L + p.chunk - 1) / p.chunk, groups = s.B * s.H * p.vtiles;
+    int64_t segs = groups >= 512 ? 1 : (512 + groups - 1) / groups;
+    if (segs > chunks / 8) segs = chunks / 8;
+    if (segs < 1) segs = 1;
+    p.seg_chunks = (chunks + segs - 1) / segs;
+    p.segs = p.seg_chunks > 0 ? (chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+    const size_t states = p.segs > 1 ? (size_t)(s.B * s.H * p.segs) * s.dk * s.dv * sizeof(float) : 0;
+    p.off_decay = (states + 255) / 256 * 256;
+    p.bytes = p.segs > 1 ? p.off_decay + (size_t)(s.B * s.H * p.segs) * sizeof(float2) : 0;
+    return p;
+}
+
+int linattn_granule(const LinAttnArgs &a) {
+    const int e = a.s.act == kBF16 ? 2 : 4;
+    uintptr_t bits = 0;
+    for (const void *x : {a.q, a.k, a.v, (const void *)a.y}) bits |= reinterpret_cast<uintptr_t>(x);
+    for (int64_t n : {a.ld_q, a.ld_k, a.ld_v, a.ld_y, (int64_t)a.s.dk, (int64_t)a.s.dv}) bits |= (uintptr_t)(n * e);
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : e;
+}
+
+template <int ACT, int DK, int G, bool FULL>
+hipError_t launch_chunks(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
+    constexpr int bytes = ChunkGeom<ACT, DK>::kBytes;
+    const auto kernel = linattn_chunk_kernel<ACT, DK, G, FULL>;
+    if (bytes > 65536) {
+        const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != hipSuccess) return err;
+    }
+    const int64_t units = a.s.B * a.s.H * p.segs;
+    kernel<<<dim3((unsigned)((units + 7) / 8 * 8 * p.vtiles)), kThreads, bytes, stream>>>(a, p);
+    return hipGetLastError();
+}
+
+template <int ACT, int DK, int G>
+hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
+    if (p.segs > 1) {
+        hipError_t err = launch_chunks<ACT, DK, G, false>(a, p, stream);
+        if (err != hipSuccess) return err;
+        const dim3 grid((unsigned)(a.s.B * a.s.H), (unsigned)((a.s.dk * a.s.dv + kThreads - 1) / kThreads));
+        linattn_join_kernel<<<grid, kThreads, 0, stream>>>(a, p);
+        if ((err = hipGetLastError()) != hipSuccess) return err;
+    }
+    return launch_chunks<ACT, DK, G, true>(a, p, stream);
+}
+
+template <int ACT, int DK>
+hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
+    switch (linattn_granule(a)) {
+        case 16: return launch_prompt<ACT, DK, 16>(a, p, stream);
+        case 8: return launch_prompt<ACT, DK, 8>(a, p, stream);
+        default: return launch_prompt<ACT, DK, Act<ACT>::kBytes>(a, p, stream);
+    }
+}
+
+template <int ACT>
+hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
+    switch (padded_dk(a.s.dk)) {
+        case 32: return launch_prompt<ACT, 32>(a, p, stream);
+        case 64: return launch_prompt<ACT, 64>(a, p, stream);
+        case 128: return launch_prompt<ACT, 128>(a, p, stream);
+        default: return launch_prompt<ACT, 256>(a, p, stream);
+    }
+}
+
 }  // namespace
 
-size_t linattn_workspace(const LinAttnShape &, int64_t) { return 0; }
+size_t linattn_workspace(const LinAttnShape &s, int64_t L) { return linattn_plan(s, L).bytes; }
 
 hipError_t launch_linattn_prefill(const LinAttnArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.s.B * a.s.H), (unsigned)((a.s.dv + kCols - 1) / kCols));
-    if (a.s.act == kBF16)
-        linattn_scan_kernel<kBF16><<<grid, kThreads, 0, stream>>>(a);
-    else
-        linattn_scan_kernel<kF32><<<grid, kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    const LinAttnPlan p = linattn_plan(a.s, a.L);
+    return a.s.act == kBF16 ? launch_prompt<kBF16>(a, p, stream) : launch_prompt<kF32>(a, p, stream);
 }
 
 hipError_t launch_linattn_decode(const LinAttnArgs &a, hipStream_t stream) {
