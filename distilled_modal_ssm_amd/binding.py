@@ -127,6 +127,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library once (raises LibraryMissing if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -556,26 +558,26 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        self.device, self.stream = device, stream
-        if stream is None:
-            self.guard = torch.cuda.device(device)
-        else:
+        self.device, self.torch, self.guard = device, torch, None
+        if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device)
             self.guard = torch.cuda.stream(stream)
-        self.torch = torch
+        elif torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        self.guard.__enter__()
-        return int(self.torch.cuda.current_stream(self.device).cuda_stream)
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        return self.guard.__exit__(*exc) if self.guard is not None else None
 
 
 def _expect(name, t, dtype, shape, device):
     """A contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous {dtype} tensor {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 

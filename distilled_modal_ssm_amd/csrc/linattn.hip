@@ -18,9 +18,10 @@
 //                (bfloat16: each adds a rounding like that of y itself, so y's
 //                error is at most 1.41 of the one its own rounding makes);
 //   products of parts i and j are left out where i + j > 2 (below 2^-24).
-// G is summed in float64 and the state's factor exp(E) has two float32 parts: a
-// head that forgets slowly multiplies by the same factor for thousands of
-// chunks' worth of tokens, so its rounding would add up.
+// G is summed in float64 (and in units of log 2, for the exponential's
+// instruction).  The rounding of the state's factor exp(E) is made good in the
+// next chunk's: a head that forgets slowly multiplies by the same factor over and
+// over, so its rounding would add up.
 //
 // Workgroup: a batch row, a head and 64 value columns, 16 a wave.  The wave's
 // part of the state, [dk][16], stays in the accumulators of the K^T V products
@@ -137,6 +138,10 @@ __device__ __forceinline__ uint2 read_transposed(const uint16_t *at) {
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
 }
 
+__device__ __forceinline__ uint4 load_bounded(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
 constexpr int kVT = 64;  // value columns of a workgroup
 
 struct LinAttnPlan {
@@ -150,13 +155,15 @@ template <int ACT, int DK> struct ChunkGeom {
     static constexpr int C = (ACT == kBF16 && DK <= 128) ? 64 : 32;
     static constexpr int NP = ACT == kBF16 ? 1 : 3;  // parts of q, k, v, and of what y's products round
     static constexpr int EB = Act<ACT>::kBytes;
-    // LDS rows in elements: K's are 20 or 44 words past a multiple of 64, so that
-    // the transposed reads' four rows of four 16-byte steps spread over the banks
-    static constexpr int QS = DK + 8;
-    static constexpr int KS = DK + (DK == 32 ? 8 : DK == 64 ? 24 : 40);
+    // LDS rows in elements, by the counted conflicts of each access (cycles beyond
+    // the first ones of a wave's instruction): Q, read in rows of 16 bytes, has none
+    // where the row is an odd multiple of 16 elements (4 at DK + 8); K is read more
+    // often transposed, with 2 where its row is an odd multiple of 32 (4 to 6 else).
+    static constexpr int QS = DK + 16;
+    static constexpr int KS = DK == 32 ? 32 : DK + 32;
     static constexpr int VS = kVT + 8, PS = C + 8;
     static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
-    static constexpr int kBytes = 2 * NP * (QP + KP + VP + PP) + C * 16 + 16;
+    static constexpr int kBytes = 2 * NP * (QP + KP + VP + PP) + 2 * (C * 16 + 4) + 8;
 };
 
 template <int ACT, int DK, int G, bool FULL>
@@ -170,8 +177,8 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
     extern __shared__ __align__(16) unsigned char smem[];
     uint16_t *Qs = reinterpret_cast<uint16_t *>(smem), *Ks = Qs + NP * M::QP, *Vs = Ks + NP * M::KP,
              *Ps = Vs + NP * M::VP;
-    double *Gs = reinterpret_cast<double *>(Ps + NP * M::PP);
-    float *from_start = reinterpret_cast<float *>(Gs + C), *to_end = from_start + C, *factor = to_end + C;
+    double *Gs = reinterpret_cast<double *>(Ps + NP * M::PP);  // [2][C] by the chunk's parity, as the next three
+    float *from_start = reinterpret_cast<float *>(Gs + 2 * C), *to_end = from_start + 2 * C, *factor = to_end + 2 * C;
 
     // neighbouring value tiles of a head and segment on one XCD (workgroups go
     // round the eight by their index): they read the same q and k
@@ -219,34 +226,82 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
     // tokens of the next chunk, on their way
     const int qr = tid / RP, qc = tid % RP * PER, vr = tid / VP, vc = tid % VP * PER;
     uint4 rq[NQ], rk[NQ], rv[NV];
-    float ra = 0.f;
     auto fetch = [&](int64_t t0) {
         const int64_t n = rows - t0;
+        if constexpr (G == 16) {
+            // rows and columns past the end read as zero by the bounds of the buffer
+            const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
+            const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
+            const auto bq = make_region(q + t0 * a.ld_q, n <= 0 ? 0 : last * sq + dk * M::EB);
+            const auto bk = make_region(k + t0 * a.ld_k, n <= 0 ? 0 : last * sk + dk * M::EB);
+            const auto bv = make_region(v + t0 * a.ld_v, n <= 0 ? 0 : last * sv + vcols * M::EB);
+            const uint32_t oc = qc < dk ? qc * M::EB : 0x80000000u, ov = vc < vcols ? vc * M::EB : 0x80000000u;
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int r = qr + i * RSTEP;
-            rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
-            if (r < n) {
-                if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
-                rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
+            for (int i = 0; i < NQ; ++i) {
+                if (FULL) rq[i] = load_bounded(bq, oc + (qr + i * RSTEP) * sq);
+                rk[i] = load_bounded(bk, oc + (qr + i * RSTEP) * sk);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) rv[i] = load_bounded(bv, ov + (vr + i * VSTEP) * sv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int r = qr + i * RSTEP;
+                rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
+                if (r < n) {
+                    if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
+                    rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int r = vr + i * VSTEP;
+                rv[i] = make_uint4(0, 0, 0, 0);
+                if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int r = vr + i * VSTEP;
-            rv[i] = make_uint4(0, 0, 0, 0);
-            if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
-        }
+    };
+    // The last wave, which has the fewest K Q^T tiles, forms a chunk's decays while
+    // the chunk before is worked on.  `error`: the state's factor as it should be
+    // over what float32 made of it, handed on to the next chunk's factor, so that
+    // the factors' product over many chunks is right to a rounding.
+    float ra = 0.f;
+    double total = 0.0, error = 1.0;
+    auto fetch_decay = [&](int64_t t0) {
         ra = 0.f;
-        if (wave == 0 && lane < n && lane < C && decay) ra = bound_decay(decay[(t0 + lane) * a.ld_decay]);
+        if (decay && lane < C && t0 + lane < rows) ra = bound_decay(decay[(t0 + lane) * a.ld_decay]);
+    };
+    auto form_decays = [&](int at) {
+        constexpr double kLog2e = 1.4426950408889634074;
+        double g = ra * kLog2e;
+#pragma unroll
+        for (int d = 1; d < C; d <<= 1) {
+            const double o = __shfl_up(g, d);
+            if (lane >= d) g += o;
+        }
+        const double e = __shfl(g, C - 1);
+        total += e;
+        if (lane < C) {
+            Gs[at * C + lane] = g;
+            from_start[at * C + lane] = __builtin_amdgcn_exp2f((float)g);
+            to_end[at * C + lane] = __builtin_amdgcn_exp2f((float)(e - g));
+        }
+        const double f = exp2(e) * error;
+        const float ff = (float)f;
+        error = ff > 1e-30f ? f / (double)ff : 1.0;
+        if (lane == 0) factor[at] = ff;
     };
 
     // tiles above the diagonal that the products read: zero, once
     if (FULL)
         for (int i = tid; i < NP * M::PP; i += kThreads) Ps[i] = 0;
     fetch(0);
-    double total = 0.0;
-    for (int64_t t0 = 0; t0 < rows; t0 += C) {
+    if (wave == 3) {
+        fetch_decay(0);
+        form_decays(0);
+        fetch_decay(C);
+    }
+    for (int64_t t0 = 0, odd = 0; t0 < rows; t0 += C, odd ^= 1) {
         __syncthreads();  // the chunk before is done with the LDS
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
@@ -255,36 +310,27 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) store_piece<ACT, M::VP>(Vs + (vr + i * VSTEP) * M::VS + vc, rv[i]);
-        if (wave == 0) {
-            double g = ra;
-#pragma unroll
-            for (int d = 1; d < C; d <<= 1) {
-                const double o = __shfl_up(g, d);
-                if (lane >= d) g += o;
-            }
-            const double e = __shfl(g, C - 1);
-            total += e;
-            if (lane < C) {
-                Gs[lane] = g;
-                from_start[lane] = expf((float)g);
-                to_end[lane] = expf((float)(e - g));
-            }
-            if (lane == C - 1) {
-                const double f = exp(e);
-                factor[0] = (float)f;
-                factor[1] = (float)(f - (double)(float)f);
-            }
-        }
         fetch(t0 + C);
         __syncthreads();
+        if (wave == 3) {
+            form_decays((int)odd ^ 1);
+            fetch_decay(t0 + 2 * C);
+        }
+        const double *gs = Gs + odd * C;
+        const float *fs = from_start + odd * C, *te = to_end + odd * C;
 
         f32x4 acc[TT];
         if (FULL) {
-            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t: tiles (i, j) of 16 s x 16 t, i <= j
+            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t, in tiles (i, j) of 16 s x 16 t, i <= j:
+            // up to three a wave, codes 4 i + j, 15 for none; the last wave has one, or none
+            constexpr uint32_t kTiles4[4] = {0xb73, 0xa62, 0xf51, 0xff0}, kTiles2[4] = {0xff1, 0xff5, 0xff0, 0xfff};
+            const uint32_t tiles = TT == 4 ? kTiles4[wave] : kTiles2[wave];
 #pragma unroll
-            for (int n = 0; n < TT * (TT + 1) / 2; ++n) {
-                if ((n & 3) != wave) continue;
-                const int j = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, i = n - j * (j + 1) / 2;
+            for (int n = 0; n < (TT == 4 ? 3 : 1); ++n) {
+                const uint32_t code = tiles >> (4 * n) & 15;
+                // (3, 3) has the code of none: it is the third tile of wave 2
+                if (code == 15 && !(TT == 4 && wave == 2 && n == 2)) continue;
+                const int i = code >> 2, j = code & 3;
                 f32x4 x4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int pr = 0; pr < PAIRS; ++pr) {
@@ -297,10 +343,10 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
                     x4 = mfma(ka, qb, x4);
                 }
                 const int t = 16 * j + li, s = 16 * i + 4 * lg;
-                const double gt = Gs[t];
+                const double gt = gs[t];
                 float x[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = s + r <= t ? x4[r] * expf((float)(gt - Gs[s + r])) : 0.f;
+                for (int r = 0; r < 4; ++r) x[r] = s + r <= t ? x4[r] * __builtin_amdgcn_exp2f((float)(gt - gs[s + r])) : 0.f;
 #pragma unroll
                 for (int w = 0; w < NP; ++w) {
                     const uint32_t lo = take_part(x[0], x[1]);
@@ -327,7 +373,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
                 }
             }
 #pragma unroll
-            for (int j = 0; j < TT; ++j) acc[j] *= from_start[16 * j + li];
+            for (int j = 0; j < TT; ++j) acc[j] *= fs[16 * j + li];
             __syncthreads();
         }
         // V of this wave's columns as an operand: value column li, tokens 32 kk + 8 lg + 0..7
@@ -370,11 +416,9 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
             }
         }
         // the state
-        const float f0 = factor[0], f1 = factor[1];
+        const float f = factor[odd];
 #pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] = fmaf(S[t][r], f0, S[t][r] * f1);
+        for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             float x[8];
@@ -391,7 +435,7 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= to_end[32 * kk + 8 * lg + e];
+            for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
             uint4 vb[3];
             split8(x, vb);
 #pragma unroll
@@ -423,8 +467,8 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
                 if (row < dk && col < vcols) to[(int64_t)row * dv + v0 + col] = S[t][r];
             }
     }
-    if (!FULL && vt == 0 && tid == 0) {
-        const double f = exp(total);
+    if (!FULL && vt == 0 && wave == 3 && lane == 0) {
+        const double f = exp2(total);
         reinterpret_cast<float2 *>(a.ws + p.off_decay)[bh * p.segs + seg] =
             make_float2((float)f, (float)(f - (double)(float)f));
     }
@@ -512,7 +556,9 @@ int linattn_granule(const LinAttnArgs &a) {
     uintptr_t bits = 0;
     for (const void *x : {a.q, a.k, a.v, (const void *)a.y}) bits |= reinterpret_cast<uintptr_t>(x);
     for (int64_t n : {a.ld_q, a.ld_k, a.ld_v, a.ld_y, (int64_t)a.s.dk, (int64_t)a.s.dv}) bits |= (uintptr_t)(n * e);
-    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : e;
+    // the 16-byte loads go by 32-bit offsets from a chunk's first row
+    const bool near = a.ld_q < 1 << 22 && a.ld_k < 1 << 22 && a.ld_v < 1 << 22;
+    return bits % 16 == 0 && near ? 16 : bits % 8 == 0 ? 8 : e;
 }
 
 template <int ACT, int DK, int G, bool FULL>

@@ -35,6 +35,7 @@ class LinearAttention:
                                          self.scale, self.q_heads, self.k_heads, self.v_heads)
         hb.hyena_linattn_prefill_workspace(self.desc, 0)  # raises for sizes that the library refuses
         self._ws = {}  # scratch memory of each stream
+        self._state_shape = (self.B, self.H, self.dk, self.dv)
 
     def new_state(self):
         return self.torch.zeros((self.B, self.H, self.dk, self.dv), dtype=self.torch.float32, device=self.device)
@@ -48,33 +49,31 @@ class LinearAttention:
             ws = self._ws[stream] = self.torch.empty(n, dtype=self.torch.uint8, device=self.device)
         return ws, n
 
-    def _rows(self, name, t, lead, width):
-        """Row stride of rows [*lead][width] at ((b * L) + t) * stride."""
-        if t.dtype != self.tdtype or t.device != self.device or tuple(t.shape) != (*lead, width):
-            raise ValueError(f"{name}: need {self.tdtype} {(*lead, width)} on {self.device}, got {t.dtype} "
+    def _rows(self, name, t, lead, width, dtype=None):
+        """Row stride of rows [*lead][width] whose row (b, t) lies at (b * L + t) * stride."""
+        shape = (*lead, width)
+        if t.dtype != (dtype or self.tdtype) or t.device != self.device or t.shape != shape:
+            raise ValueError(f"{name}: need {dtype or self.tdtype} {shape} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
-        if t.numel() == 0:
+        if t.is_contiguous():
             return width
-        return hb._row_stride(t if len(lead) == 2 else t[None], ())
+        if len(lead) == 2:
+            return hb._row_stride(t, ())
+        if width > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: rows need unit element stride")
+        return t.stride(0)
 
     def _decay(self, a, lead):
         """Row stride of a log decay: 0 for one a head."""
         if a is None:
             return 0
-        if a.dtype != self.torch.float32 or a.device != self.device:
-            raise ValueError(f"log_decay: need float32 on {self.device}, got {a.dtype} on {a.device}")
-        if tuple(a.shape) == (self.H,):
-            if self.H > 1 and a.stride(0) != 1:
-                raise ValueError("log_decay of the heads must be contiguous")
+        if a.dim() == 1:
+            hb._expect("log_decay", a, self.torch.float32, (self.H,), self.device)
             return 0
-        if tuple(a.shape) != (*lead, self.H):
-            raise ValueError(f"log_decay: need {(self.H,)} or {(*lead, self.H)}, got {tuple(a.shape)}")
-        if a.numel() == 0:
-            return self.H
-        return hb._row_stride(a if len(lead) == 2 else a[None], ())
+        return self._rows("log_decay", a, lead, self.H, self.torch.float32)
 
     def _state(self, name, s):
-        hb._expect(name, s, self.torch.float32, (self.B, self.H, self.dk, self.dv), self.device)
+        hb._expect(name, s, self.torch.float32, self._state_shape, self.device)
 
     def prefill(self, q, k, v, log_decay=None, lengths=None, y=None, state_in=None, state_out=None, stream=None):
         """A prompt of L tokens.  Returns (y, state after each row's last token).
@@ -86,8 +85,9 @@ class LinearAttention:
         """
         L = int(q.shape[1]) if q.dim() == 3 else -1
         lead = (self.B, L)
-        ld = [self._rows(*x) for x in (("q", q, lead, self.q_heads * self.dk), ("k", k, lead, self.k_heads * self.dk),
-                                       ("v", v, lead, self.v_heads * self.dv))]
+        ld_q = self._rows("q", q, lead, self.q_heads * self.dk)
+        ld_k = self._rows("k", k, lead, self.k_heads * self.dk)
+        ld_v = self._rows("v", v, lead, self.v_heads * self.dv)
         ld_a = self._decay(log_decay, lead)
         if lengths is not None:
             hb._expect("lengths", lengths, self.torch.int32, (self.B,), self.device)
@@ -102,7 +102,7 @@ class LinearAttention:
             else:
                 self._state("state_out", state_out)
             ws, n = self._workspace(L, stream)
-            hb.hyena_linattn_prefill(self.desc, L, lengths, q, ld[0], k, ld[1], v, ld[2], log_decay, ld_a, y,
+            hb.hyena_linattn_prefill(self.desc, L, lengths, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
                                      self._rows("y", y, lead, self.H * self.dv), state_in, state_out, ws, n, stream)
         return y, state_out
 
@@ -115,8 +115,9 @@ class LinearAttention:
         rows[b] of ``state``, and ``state_out`` must be another tensor.
         """
         lead = (self.B,)
-        ld = [self._rows(*x) for x in (("q", q, lead, self.q_heads * self.dk), ("k", k, lead, self.k_heads * self.dk),
-                                       ("v", v, lead, self.v_heads * self.dv))]
+        ld_q = self._rows("q", q, lead, self.q_heads * self.dk)
+        ld_k = self._rows("k", k, lead, self.k_heads * self.dk)
+        ld_v = self._rows("v", v, lead, self.v_heads * self.dv)
         ld_a = self._decay(log_decay, lead)
         self._state("state", state)
         if state_out is not None:
@@ -128,7 +129,7 @@ class LinearAttention:
         with hb._On(self.device, stream) as stream:
             if y is None:
                 y = self.torch.empty((self.B, self.H * self.dv), dtype=self.tdtype, device=self.device)
-            hb.hyena_linattn_decode_step(self.desc, q, ld[0], k, ld[1], v, ld[2], log_decay, ld_a, y,
+            hb.hyena_linattn_decode_step(self.desc, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
                                          self._rows("y", y, lead, self.H * self.dv), state, rows,
                                          state if state_out is None else state_out, stream)
         return y
