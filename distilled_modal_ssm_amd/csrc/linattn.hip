@@ -37,6 +37,8 @@
 // starts every segment from its own.
 #include "hm_internal.hpp"
 
+#include <type_traits>
+
 namespace hm {
 namespace {
 
@@ -51,20 +53,23 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Sum of the products of parts i of a and j of b, the smallest first.
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mfma(const uint4 (&a)[NA], const uint4 (&b)[NB], f32x4 c) {
-    constexpr int N = NA > NB ? NA : NB;
+// c[n] += a[n] b[n] for N tiles: the products of their parts i and j, i + j
+// decreasing so that the smallest come first, tile after tile in between (a
+// product that waits for the one before of its own tile leaves a gap).
+template <int N, int NA, int NB, int MA, int MB>
+__device__ __forceinline__ void mfma_tiles(const uint4 (&a)[MA][NA], const uint4 (&b)[MB][NB], f32x4 *c) {
+    constexpr int P = NA > NB ? NA : NB;
 #pragma unroll
-    for (int sum = N - 1; sum >= 0; --sum)
+    for (int sum = P - 1; sum >= 0; --sum)
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             const int j = sum - i;
-            if (j >= 0 && j < NB)
-                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
-                                                            __builtin_bit_cast(bf16x8, b[j]), c, 0, 0, 0);
+            if (j < 0 || j >= NB) continue;
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                c[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[n][i]),
+                                                               __builtin_bit_cast(bf16x8, b[n][j]), c[n], 0, 0, 0);
         }
-    return c;
 }
 
 // x, y -> their leading bfloat16 parts packed; x, y become what is left.
@@ -164,10 +169,11 @@ template <int ACT, int DK> struct ChunkGeom {
     static constexpr int VS = kVT + 8, PS = C + 8;
     static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
     static constexpr int kBytes = 2 * NP * (QP + KP + VP + PP) + 2 * (C * 16 + 4) + 8;
+    static constexpr int kPerCU = kBytes <= 80 * 1024 ? 2 : 1;
 };
 
 template <int ACT, int DK, int G, bool FULL>
-__global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
+__global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
     using T = typename Act<ACT>::T;
     using M = ChunkGeom<ACT, DK>;
     constexpr int C = M::C, NP = M::NP, PER = 16 / M::EB;
@@ -320,57 +326,91 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
         const float *fs = from_start + odd * C, *te = to_end + odd * C;
 
         f32x4 acc[TT];
-        if (FULL) {
-            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t, in tiles (i, j) of 16 s x 16 t, i <= j:
-            // up to three a wave, codes 4 i + j, 15 for none; the last wave has one, or none
-            constexpr uint32_t kTiles4[4] = {0xb73, 0xa62, 0xf51, 0xff0}, kTiles2[4] = {0xff1, 0xff5, 0xff0, 0xfff};
-            const uint32_t tiles = TT == 4 ? kTiles4[wave] : kTiles2[wave];
+        if constexpr (FULL) {
+            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t, in tiles (i, j) of 16 s x 16 t, i <= j,
+            // N of them at once
+            auto weigh = [&](auto count, uint32_t tiles) {
+                constexpr int N = decltype(count)::value;
+                const uint16_t *kat[N], *qat[N];
+                f32x4 x[N];
 #pragma unroll
-            for (int n = 0; n < (TT == 4 ? 3 : 1); ++n) {
-                const uint32_t code = tiles >> (4 * n) & 15;
-                // (3, 3) has the code of none: it is the third tile of wave 2
-                if (code == 15 && !(TT == 4 && wave == 2 && n == 2)) continue;
-                const int i = code >> 2, j = code & 3;
-                f32x4 x4 = {0.f, 0.f, 0.f, 0.f};
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t code = tiles >> (4 * n) & 15;
+                    kat[n] = Ks + (16 * (code >> 2) + li) * M::KS + 8 * lg;
+                    qat[n] = Qs + (16 * (code & 3) + li) * M::QS + 8 * lg;
+                    x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+                uint4 ka[2][N][NP], qb[2][N][NP];
+                auto load = [&](int pr) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+#pragma unroll
+                        for (int w = 0; w < NP; ++w) {
+                            ka[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(kat[n] + w * M::KP + 32 * pr);
+                            qb[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(qat[n] + w * M::QP + 32 * pr);
+                        }
+                };
+                load(0);
 #pragma unroll
                 for (int pr = 0; pr < PAIRS; ++pr) {
-                    uint4 ka[NP], qb[NP];
+                    if (pr + 1 < PAIRS) load(pr + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    mfma_tiles<N>(ka[pr & 1], qb[pr & 1], x);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const uint32_t code = tiles >> (4 * n) & 15;
+                    const int t = 16 * (code & 3) + li, s = 16 * (code >> 2) + 4 * lg;
+                    const double gt = gs[t];
+                    float o[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float d = (float)(gt - gs[s + r]);
+                        o[r] = x[n][r] * __builtin_amdgcn_exp2f(s + r <= t ? d : -__builtin_inff());
+                    }
 #pragma unroll
                     for (int w = 0; w < NP; ++w) {
-                        ka[w] = *reinterpret_cast<const uint4 *>(Ks + w * M::KP + (16 * i + li) * M::KS + 32 * pr + 8 * lg);
-                        qb[w] = *reinterpret_cast<const uint4 *>(Qs + w * M::QP + (16 * j + li) * M::QS + 32 * pr + 8 * lg);
+                        const uint32_t lo = take_part(o[0], o[1]);
+                        *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(o[2], o[3]));
                     }
-                    x4 = mfma(ka, qb, x4);
                 }
-                const int t = 16 * j + li, s = 16 * i + 4 * lg;
-                const double gt = gs[t];
-                float x[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = s + r <= t ? x4[r] * __builtin_amdgcn_exp2f((float)(gt - gs[s + r])) : 0.f;
-#pragma unroll
-                for (int w = 0; w < NP; ++w) {
-                    const uint32_t lo = take_part(x[0], x[1]);
-                    *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(x[2], x[3]));
-                }
-            }
+            };
+            // codes 4 i + j of each wave's tiles; the last wave, which forms the decays, has the fewest
+            constexpr uint32_t kTiles4[4] = {0xb73, 0xa62, 0xf51, 0x0}, kTiles2[4] = {0x1, 0x5, 0x0, 0x0};
+            if (wave < 3)
+                weigh(std::integral_constant<int, TT == 4 ? 3 : 1>{}, TT == 4 ? kTiles4[wave] : kTiles2[wave]);
+            else if constexpr (TT == 4)
+                weigh(std::integral_constant<int, 1>{}, kTiles4[3]);
+
             // exp(G_t) S^T q_t
+            const uint16_t *qat = Qs + li * M::QS + 8 * lg;
+            uint4 qb[2][TT][NP];
+            auto load = [&](int pr) {
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+#pragma unroll
+                    for (int w = 0; w < NP; ++w)
+                        qb[pr & 1][j][w] = *reinterpret_cast<const uint4 *>(qat + w * M::QP + 16 * j * M::QS + 32 * pr);
+            };
+            load(0);
 #pragma unroll
             for (int j = 0; j < TT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int pr = 0; pr < PAIRS; ++pr) {
+                if (pr + 1 < PAIRS) load(pr + 1);
+                __builtin_amdgcn_sched_barrier(0);
                 float x[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) x[r] = S[2 * pr + r / 4][r % 4];
-                uint4 sa[NP];
-                split8(x, sa);
+                uint4 sa[TT][NP];
+                split8(x, sa[0]);
 #pragma unroll
-                for (int j = 0; j < TT; ++j) {
-                    uint4 qb[NP];
+                for (int j = 1; j < TT; ++j)
 #pragma unroll
-                    for (int w = 0; w < NP; ++w)
-                        qb[w] = *reinterpret_cast<const uint4 *>(Qs + w * M::QP + (16 * j + li) * M::QS + 32 * pr + 8 * lg);
-                    acc[j] = mfma(sa, qb, acc[j]);
-                }
+                    for (int w = 0; w < NP; ++w) sa[j][w] = sa[0][w];
+                mfma_tiles<TT>(sa, qb[pr & 1], acc);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int j = 0; j < TT; ++j) acc[j] *= fs[16 * j + li];
@@ -386,69 +426,99 @@ __global__ __launch_bounds__(kThreads, 2) void linattn_chunk_kernel(LinAttnArgs 
                 const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::VS);
                 va[kk][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
-        if (FULL) {
+        // K transposed, KG tiles of key rows at a time, loaded one time ahead
+        constexpr int KG = NP == 3 || DK == 32 || DK == 256 ? 2 : 4, KN = KK * 2 * PAIRS / KG;
+        uint4 ka[2][KG][NP];
+        auto load_keys = [&](int n) {
+            const int kk = n / (2 * PAIRS / KG);
 #pragma unroll
-            for (int j = 0; j < TT; ++j) {
-#pragma unroll
-                for (int kk = 0; kk <= j / 2; ++kk) {
-                    uint4 pb[NP];
-#pragma unroll
-                    for (int w = 0; w < NP; ++w)
-                        pb[w] = *reinterpret_cast<const uint4 *>(Ps + w * M::PP + (16 * j + li) * M::PS + 32 * kk + 8 * lg);
-                    acc[j] = mfma(va[kk], pb, acc[j]);
-                }
-                const int64_t t = t0 + 16 * j + li;
-                const int c = 16 * wave + 4 * lg;
-                if (t < end - begin && c < vcols) {
-                    const f32x4 o = acc[j] * a.s.scale;
-                    T *at = y + t * a.ld_y + c;
-                    if (G == 16 || (G == 8 && ACT == kBF16)) {
-                        if constexpr (ACT == kBF16)
-                            *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-                        else
-                            *reinterpret_cast<float4 *>(at) = make_float4(o[0], o[1], o[2], o[3]);
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (c + r < vcols) Act<ACT>::st(at + r, o[r]);
-                    }
-                }
-            }
-        }
-        // the state
-        const float f = factor[odd];
-#pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            float x[8];
-            const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&va[kk][0]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = bf16_lo(w0[e]);
-                x[2 * e + 1] = bf16_hi(w0[e]);
-                if constexpr (NP == 3) {
-                    const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
-                    const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
-                    x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
-                    x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
-            uint4 vb[3];
-            split8(x, vb);
-#pragma unroll
-            for (int t = 0; t < 2 * PAIRS; ++t) {
-                uint4 ka[NP];
+            for (int g = 0; g < KG; ++g) {
+                const int t = n % (2 * PAIRS / KG) * KG + g;
 #pragma unroll
                 for (int w = 0; w < NP; ++w) {
                     const uint16_t *at = Ks + w * M::KP + (32 * kk + 8 * lg + (li >> 2)) * M::KS + 16 * (t & ~1) +
                                          8 * (li & 3) + 4 * (t & 1);
                     const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::KS);
-                    ka[w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    ka[n & 1][g][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
-                S[t] = mfma(ka, vb, S[t]);
+            }
+        };
+        if constexpr (FULL) {
+            const uint16_t *pat = Ps + li * M::PS + 8 * lg;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                uint4 pb[TT][NP], vv[TT][NP];  // tiles j from 2 kk on
+#pragma unroll
+                for (int j = 2 * kk; j < TT; ++j)
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) {
+                        pb[j - 2 * kk][w] = *reinterpret_cast<const uint4 *>(pat + w * M::PP + 16 * j * M::PS + 32 * kk);
+                        vv[j - 2 * kk][w] = va[kk][w];
+                    }
+                if (kk == KK - 1) load_keys(0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (kk == 0)
+                    mfma_tiles<TT>(vv, pb, acc);
+                else
+                    mfma_tiles<2>(vv, pb, acc + 2 * kk);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            load_keys(0);
+        }
+        // the state
+        const float f = factor[odd];
+#pragma unroll
+        for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
+        uint4 vb[KG][3];
+#pragma unroll
+        for (int n = 0; n < KN; ++n) {
+            const int kk = n / (2 * PAIRS / KG), first = n % (2 * PAIRS / KG) * KG;
+            if (n + 1 < KN) load_keys(n + 1);
+            if (first == 0) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w0 = reinterpret_cast<const uint32_t *>(&va[kk][0])[e];
+                    x[2 * e] = bf16_lo(w0);
+                    x[2 * e + 1] = bf16_hi(w0);
+                    if constexpr (NP == 3) {
+                        const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
+                        const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
+                        x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
+                        x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
+                split8(x, vb[0]);
+#pragma unroll
+                for (int g = 1; g < KG; ++g)
+#pragma unroll
+                    for (int w = 0; w < 3; ++w) vb[g][w] = vb[0][w];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            mfma_tiles<KG>(ka[n & 1], vb, S + first);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (FULL) {
+            const int c = 16 * wave + 4 * lg;
+            T *at = y + (t0 + li) * a.ld_y + c;
+            const bool whole = t0 + C <= end - begin;
+#pragma unroll
+            for (int j = 0; j < TT; ++j, at += 16 * a.ld_y) {
+                if (c >= vcols || !(whole || t0 + 16 * j + li < end - begin)) continue;
+                const f32x4 o = acc[j] * a.s.scale;
+                if constexpr (G == 16 || (G == 8 && ACT == kBF16)) {
+                    if constexpr (ACT == kBF16)
+                        *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+                    else
+                        *reinterpret_cast<float4 *>(at) = make_float4(o[0], o[1], o[2], o[3]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (c + r < vcols) Act<ACT>::st(at + r, o[r]);
+                }
             }
         }
     }
