@@ -23,13 +23,13 @@
 // next chunk's: a head that forgets slowly multiplies by the same factor over and
 // over, so its rounding would add up.
 //
-// Workgroup: a batch row, a head and 64 value columns, 16 a wave.  The wave's
-// part of the state, [dk][16], stays in the accumulators of the K^T V products
-// from chunk to chunk (lane = value column, registers = key rows).  The key rows
-// of an MFMA tile are chosen so that two tiles' registers are, converted in
-// place, the S^T operand of the next chunk (lane group g: key rows 8g .. 8g+7 of
-// each 32): the state never passes through the LDS.  K and V come out of the LDS
-// transposed (ds_read_b64_tr_b16).
+// Workgroup: a batch row, a head and 64 or 128 value columns, 16 a wave.  The
+// wave's part of the state, [dk][16], stays in the accumulators of the K^T V
+// products from chunk to chunk (lane = value column, registers = key rows).  The
+// key rows of an MFMA tile are chosen so that two tiles' registers are, converted
+// in place, the S^T operand of the next chunk (lane group g: key rows 8g .. 8g+7
+// of each 32): the state never passes through the LDS.  K and V come out of the
+// LDS transposed (ds_read_b64_tr_b16).  Four more waves bring the next chunk.
 //
 // A prompt of too few rows and heads to fill the GPU is cut into segments of
 // chunks: the state-only form of the kernel runs over every segment but the last
@@ -147,16 +147,45 @@ __device__ __forceinline__ uint4 load_bounded(__amdgpu_buffer_rsrc_t r, uint32_t
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
-constexpr int kVT = 64;  // value columns of a workgroup
+// x of the lane that a DPP control names, 0 where there is none (rows not in the mask keep 0)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the lanes up to and with this one: within rows of 16 lanes, then the
+// rows' last lanes into the rows after them.
+__device__ __forceinline__ double scan_sum(double x) {
+    x += dpp<0x111, 0xf>(x);  // the lane 1, 2, 4, 8 before
+    x += dpp<0x112, 0xf>(x);
+    x += dpp<0x114, 0xf>(x);
+    x += dpp<0x118, 0xf>(x);
+    x += dpp<0x142, 0xa>(x);  // lane 15 to row 1, lane 47 to row 3
+    x += dpp<0x143, 0xc>(x);  // lane 31 to rows 2 and 3
+    return x;
+}
+
+__device__ __forceinline__ double read_lane(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 
 struct LinAttnPlan {
     int64_t segs, seg_chunks;   // segments of the prompt, and chunks of each
     int chunk;                  // tokens of a chunk
-    int vtiles;                 // workgroups of a row and head
+    int vt, vtiles;             // value columns of a workgroup, and workgroups of a row and head
     size_t off_decay, bytes;    // float [B H][segs][dk][dv] states; float2 [B H][segs] segment factors
 };
 
-template <int ACT, int DK> struct ChunkGeom {
+constexpr int kLds = 160 * 1024;
+constexpr int kMakers = 4;  // waves that fetch, form decays and weigh K Q^T
+
+template <int ACT, int DK, int VT> struct ChunkGeom {
     static constexpr int C = (ACT == kBF16 && DK <= 128) ? 64 : 32;
     static constexpr int NP = ACT == kBF16 ? 1 : 3;  // parts of q, k, v, and of what y's products round
     static constexpr int EB = Act<ACT>::kBytes;
@@ -166,25 +195,44 @@ template <int ACT, int DK> struct ChunkGeom {
     // often transposed, with 2 where its row is an odd multiple of 32 (4 to 6 else).
     static constexpr int QS = DK + 16;
     static constexpr int KS = DK == 32 ? 32 : DK + 32;
-    static constexpr int VS = kVT + 8, PS = C + 8;
+    static constexpr int VS = VT + 8, PS = C + 8;
     static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
-    static constexpr int kBytes = 2 * NP * (QP + KP + VP + PP) + 2 * (C * 16 + 4) + 8;
-    static constexpr int kPerCU = kBytes <= 80 * 1024 ? 2 : 1;
+    static constexpr int buffers(int depth) {
+        return 2 * NP * (depth * (QP + KP + VP) + PP) + 2 * (C * 16 + 4) + 8;
+    }
+    // chunks in the LDS: two, or one where two do not fit
+    static constexpr int kDepth = buffers(2) <= kLds ? 2 : 1;
+    static constexpr int kBytes = buffers(kDepth);
+    static constexpr int kTakers = VT / 16;  // waves that own value columns
+    static constexpr int kThreads = 64 * (kTakers + kMakers);
+    static constexpr int kWavesPerSimd = kThreads == 512 && 2 * kBytes <= kLds ? 4 : kThreads / 256;
+    static_assert(kBytes <= kLds, "LDS");
 };
 
-template <int ACT, int DK, int G, bool FULL>
-__global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
+// The workgroup's waves have two roles.  Takers own 16 value columns each and
+// hold their part of the state: they form y and the next state from what is in
+// the LDS.  Makers put it there a chunk ahead: tokens (fetched a further chunk
+// ahead into registers), decays, and P.  A chunk takes two steps, each ended by
+// the workgroup's barrier:
+//              makers                              takers
+//   step 1     tokens of chunk c + 1 to the LDS    y of chunk c
+//   step 2     P of chunk c + 1                    state after chunk c
+template <int ACT, int DK, int VT, int G, bool FULL>
+__global__ __launch_bounds__((ChunkGeom<ACT, DK, VT>::kThreads), (ChunkGeom<ACT, DK, VT>::kWavesPerSimd))
+void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
     using T = typename Act<ACT>::T;
-    using M = ChunkGeom<ACT, DK>;
-    constexpr int C = M::C, NP = M::NP, PER = 16 / M::EB;
-    constexpr int RP = DK / PER, NQ = C * RP / kThreads, RSTEP = kThreads / RP;     // q, k pieces of a row, a thread
-    constexpr int VP = kVT / PER, NV = C * VP / kThreads, VSTEP = kThreads / VP;    // v pieces
+    using M = ChunkGeom<ACT, DK, VT>;
+    constexpr int C = M::C, NP = M::NP, PER = 16 / M::EB, MT = 64 * kMakers;
+    constexpr int RP = DK / PER, NQ = C * RP / MT, RSTEP = MT / RP;     // q, k pieces of a row, of a maker's thread
+    constexpr int VR = VT / PER, NV = C * VR / MT, VSTEP = MT / VR;     // v pieces
     constexpr int TT = C / 16, KK = C / 32, PAIRS = DK / 32;
+    constexpr bool TWO = M::kDepth == 2;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint16_t *Qs = reinterpret_cast<uint16_t *>(smem), *Ks = Qs + NP * M::QP, *Vs = Ks + NP * M::KP,
-             *Ps = Vs + NP * M::VP;
-    double *Gs = reinterpret_cast<double *>(Ps + NP * M::PP);  // [2][C] by the chunk's parity, as the next three
-    float *from_start = reinterpret_cast<float *>(Gs + 2 * C), *to_end = from_start + 2 * C, *factor = to_end + 2 * C;
+    // by the chunk's parity where two chunks fit
+    uint16_t *const Q0 = reinterpret_cast<uint16_t *>(smem), *const K0 = Q0 + M::kDepth * NP * M::QP,
+             *const V0 = K0 + M::kDepth * NP * M::KP, *const Ps = V0 + M::kDepth * NP * M::VP;
+    double *const G0 = reinterpret_cast<double *>(Ps + NP * M::PP);  // [2][C] by parity, as the next three
+    float *const F0 = reinterpret_cast<float *>(G0 + 2 * C), *const E0 = F0 + 2 * C, *const factor = E0 + 2 * C;
 
     // neighbouring value tiles of a head and segment on one XCD (workgroups go
     // round the eight by their index): they read the same q and k
@@ -196,195 +244,237 @@ __global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linatt
     if (!FULL && seg == p.segs - 1) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15,
               lg = lane >> 4;
-    const int dk = a.s.dk, dv = a.s.dv, v0 = vt * kVT, vcols = dv - v0 < kVT ? dv - v0 : kVT;
+    const int dk = a.s.dk, dv = a.s.dv, v0 = vt * VT, vcols = dv - v0 < VT ? dv - v0 : VT;
     int64_t len = a.L;
     if (a.lengths) len = a.lengths[b] < 0 ? 0 : a.lengths[b] < a.L ? a.lengths[b] : a.L;
     const int64_t begin = seg * p.seg_chunks * C, end = begin + p.seg_chunks * C < a.L ? begin + p.seg_chunks * C : a.L;
     const int64_t rows = len <= begin ? 0 : (len < end ? len : end) - begin;  // tokens of this segment
+    const int chunks = (int)((rows + C - 1) / C);
+    T *const y = static_cast<T *>(a.y) + (b * a.L + begin) * a.ld_y + h * dv + v0;
 
-    const T *q = static_cast<const T *>(a.q) + (b * a.L + begin) * a.ld_q + h * a.s.qh / a.s.H * dk;
-    const T *k = static_cast<const T *>(a.k) + (b * a.L + begin) * a.ld_k + h * a.s.kh / a.s.H * dk;
-    const T *v = static_cast<const T *>(a.v) + (b * a.L + begin) * a.ld_v + h * a.s.vh / a.s.H * dv + v0;
-    T *y = static_cast<T *>(a.y) + (b * a.L + begin) * a.ld_y + h * dv + v0;
-    const float *decay = a.decay ? a.decay + (a.ld_decay ? (b * a.L + begin) * a.ld_decay : 0) + h : nullptr;
-    const int64_t cells = (int64_t)dk * dv;
+    if (wave >= M::kTakers) {
+        // ---------------------------------------------------------------- makers
+        const int mt = tid - 64 * M::kTakers, maker = wave - M::kTakers;
+        const T *const q = static_cast<const T *>(a.q) + (b * a.L + begin) * a.ld_q + h * a.s.qh / a.s.H * dk;
+        const T *const k = static_cast<const T *>(a.k) + (b * a.L + begin) * a.ld_k + h * a.s.kh / a.s.H * dk;
+        const T *const v = static_cast<const T *>(a.v) + (b * a.L + begin) * a.ld_v + h * a.s.vh / a.s.H * dv + v0;
+        const float *const decay = a.decay ? a.decay + (a.ld_decay ? (b * a.L + begin) * a.ld_decay : 0) + h : nullptr;
 
-    // the state: tile 2P + u, register r = key row 32 P + 8 lg + 4 u + r, value column li of the wave
-    const int col = 16 * wave + li;
-    f32x4 S[2 * PAIRS];
-    {
-        const float *from = nullptr;
-        if (FULL) {
-            if (p.segs > 1)
-                from = reinterpret_cast<const float *>(a.ws) + (bh * p.segs + seg) * cells;
-            else if (a.state_in)
-                from = a.state_in + bh * cells;
-        }
+        // tokens of a chunk, on their way
+        const int qr = mt / RP, qc = mt % RP * PER, vr = mt / VR, vc = mt % VR * PER;
+        uint4 rq[NQ], rk[NQ], rv[NV];
+        auto fetch = [&](int c) {
+            const int64_t t0 = (int64_t)c * C, n = rows - t0;
+            if constexpr (G == 16) {
+                // rows and columns past the end read as zero by the bounds of the buffer
+                const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
+                const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
+                const auto bq = make_region(q + t0 * a.ld_q, n <= 0 ? 0 : last * sq + dk * M::EB);
+                const auto bk = make_region(k + t0 * a.ld_k, n <= 0 ? 0 : last * sk + dk * M::EB);
+                const auto bv = make_region(v + t0 * a.ld_v, n <= 0 ? 0 : last * sv + vcols * M::EB);
+                const uint32_t oc = qc < dk ? qc * M::EB : 0x80000000u, ov = vc < vcols ? vc * M::EB : 0x80000000u;
 #pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
-                S[t][r] = from && row < dk && col < vcols ? from[(int64_t)row * dv + v0 + col] : 0.f;
-            }
-    }
-
-    // tokens of the next chunk, on their way
-    const int qr = tid / RP, qc = tid % RP * PER, vr = tid / VP, vc = tid % VP * PER;
-    uint4 rq[NQ], rk[NQ], rv[NV];
-    auto fetch = [&](int64_t t0) {
-        const int64_t n = rows - t0;
-        if constexpr (G == 16) {
-            // rows and columns past the end read as zero by the bounds of the buffer
-            const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
-            const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
-            const auto bq = make_region(q + t0 * a.ld_q, n <= 0 ? 0 : last * sq + dk * M::EB);
-            const auto bk = make_region(k + t0 * a.ld_k, n <= 0 ? 0 : last * sk + dk * M::EB);
-            const auto bv = make_region(v + t0 * a.ld_v, n <= 0 ? 0 : last * sv + vcols * M::EB);
-            const uint32_t oc = qc < dk ? qc * M::EB : 0x80000000u, ov = vc < vcols ? vc * M::EB : 0x80000000u;
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-                if (FULL) rq[i] = load_bounded(bq, oc + (qr + i * RSTEP) * sq);
-                rk[i] = load_bounded(bk, oc + (qr + i * RSTEP) * sk);
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) rv[i] = load_bounded(bv, ov + (vr + i * VSTEP) * sv);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-                const int r = qr + i * RSTEP;
-                rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
-                if (r < n) {
-                    if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
-                    rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int r = vr + i * VSTEP;
-                rv[i] = make_uint4(0, 0, 0, 0);
-                if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
-            }
-        }
-    };
-    // The last wave, which has the fewest K Q^T tiles, forms a chunk's decays while
-    // the chunk before is worked on.  `error`: the state's factor as it should be
-    // over what float32 made of it, handed on to the next chunk's factor, so that
-    // the factors' product over many chunks is right to a rounding.
-    float ra = 0.f;
-    double total = 0.0, error = 1.0;
-    auto fetch_decay = [&](int64_t t0) {
-        ra = 0.f;
-        if (decay && lane < C && t0 + lane < rows) ra = bound_decay(decay[(t0 + lane) * a.ld_decay]);
-    };
-    auto form_decays = [&](int at) {
-        constexpr double kLog2e = 1.4426950408889634074;
-        double g = ra * kLog2e;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double o = __shfl_up(g, d);
-            if (lane >= d) g += o;
-        }
-        const double e = __shfl(g, C - 1);
-        total += e;
-        if (lane < C) {
-            Gs[at * C + lane] = g;
-            from_start[at * C + lane] = __builtin_amdgcn_exp2f((float)g);
-            to_end[at * C + lane] = __builtin_amdgcn_exp2f((float)(e - g));
-        }
-        const double f = exp2(e) * error;
-        const float ff = (float)f;
-        error = ff > 1e-30f ? f / (double)ff : 1.0;
-        if (lane == 0) factor[at] = ff;
-    };
-
-    // tiles above the diagonal that the products read: zero, once
-    if (FULL)
-        for (int i = tid; i < NP * M::PP; i += kThreads) Ps[i] = 0;
-    fetch(0);
-    if (wave == 3) {
-        fetch_decay(0);
-        form_decays(0);
-        fetch_decay(C);
-    }
-    for (int64_t t0 = 0, odd = 0; t0 < rows; t0 += C, odd ^= 1) {
-        __syncthreads();  // the chunk before is done with the LDS
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            if (FULL) store_piece<ACT, M::QP>(Qs + (qr + i * RSTEP) * M::QS + qc, rq[i]);
-            store_piece<ACT, M::KP>(Ks + (qr + i * RSTEP) * M::KS + qc, rk[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) store_piece<ACT, M::VP>(Vs + (vr + i * VSTEP) * M::VS + vc, rv[i]);
-        fetch(t0 + C);
-        __syncthreads();
-        if (wave == 3) {
-            form_decays((int)odd ^ 1);
-            fetch_decay(t0 + 2 * C);
-        }
-        const double *gs = Gs + odd * C;
-        const float *fs = from_start + odd * C, *te = to_end + odd * C;
-
-        f32x4 acc[TT];
-        if constexpr (FULL) {
-            // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t, in tiles (i, j) of 16 s x 16 t, i <= j,
-            // N of them at once
-            auto weigh = [&](auto count, uint32_t tiles) {
-                constexpr int N = decltype(count)::value;
-                const uint16_t *kat[N], *qat[N];
-                f32x4 x[N];
-#pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const uint32_t code = tiles >> (4 * n) & 15;
-                    kat[n] = Ks + (16 * (code >> 2) + li) * M::KS + 8 * lg;
-                    qat[n] = Qs + (16 * (code & 3) + li) * M::QS + 8 * lg;
-                    x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-                uint4 ka[2][N][NP], qb[2][N][NP];
-                auto load = [&](int pr) {
-#pragma unroll
-                    for (int n = 0; n < N; ++n)
-#pragma unroll
-                        for (int w = 0; w < NP; ++w) {
-                            ka[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(kat[n] + w * M::KP + 32 * pr);
-                            qb[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(qat[n] + w * M::QP + 32 * pr);
-                        }
-                };
-                load(0);
-#pragma unroll
-                for (int pr = 0; pr < PAIRS; ++pr) {
-                    if (pr + 1 < PAIRS) load(pr + 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    mfma_tiles<N>(ka[pr & 1], qb[pr & 1], x);
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int i = 0; i < NQ; ++i) {
+                    if (FULL) rq[i] = load_bounded(bq, oc + (qr + i * RSTEP) * sq);
+                    rk[i] = load_bounded(bk, oc + (qr + i * RSTEP) * sk);
                 }
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const uint32_t code = tiles >> (4 * n) & 15;
-                    const int t = 16 * (code & 3) + li, s = 16 * (code >> 2) + 4 * lg;
-                    const double gt = gs[t];
-                    float o[4];
+                for (int i = 0; i < NV; ++i) rv[i] = load_bounded(bv, ov + (vr + i * VSTEP) * sv);
+            } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float d = (float)(gt - gs[s + r]);
-                        o[r] = x[n][r] * __builtin_amdgcn_exp2f(s + r <= t ? d : -__builtin_inff());
+                for (int i = 0; i < NQ; ++i) {
+                    const int r = qr + i * RSTEP;
+                    rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
+                    if (r < n) {
+                        if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
+                        rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
                     }
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int r = vr + i * VSTEP;
+                    rv[i] = make_uint4(0, 0, 0, 0);
+                    if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
+                }
+            }
+        };
+        auto store = [&](int c) {
+            const int at = TWO ? c & 1 : 0;
+            uint16_t *const Qs = Q0 + at * NP * M::QP, *const Ks = K0 + at * NP * M::KP, *const Vs = V0 + at * NP * M::VP;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                if (FULL) store_piece<ACT, M::QP>(Qs + (qr + i * RSTEP) * M::QS + qc, rq[i]);
+                store_piece<ACT, M::KP>(Ks + (qr + i * RSTEP) * M::KS + qc, rk[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) store_piece<ACT, M::VP>(Vs + (vr + i * VSTEP) * M::VS + vc, rv[i]);
+        };
+
+        // The last maker, which has the fewest tiles of P, forms a chunk's decays.
+        // `error`: the state's factor as it should be over what float32 made of it,
+        // handed on to the next chunk's factor, so that the factors' product over
+        // many chunks is right to a rounding.
+        float ra = 0.f;
+        double total = 0.0, error = 1.0;
+        auto fetch_decay = [&](int c) {
+            const int64_t t = (int64_t)c * C + lane;
+            ra = 0.f;
+            if (decay && lane < C && t < rows) ra = bound_decay(decay[t * a.ld_decay]);
+        };
+        auto form_decays = [&](int c) {
+            constexpr double kLog2e = 1.4426950408889634074;
+            const int at = c & 1;
+            const double g = scan_sum(ra * kLog2e);
+            const double e = read_lane(g, C - 1);
+            total += e;
+            if (lane < C) {
+                G0[at * C + lane] = g;
+                F0[at * C + lane] = __builtin_amdgcn_exp2f((float)g);
+                E0[at * C + lane] = __builtin_amdgcn_exp2f((float)(e - g));
+            }
+            const double f = exp2(e) * error;
+            const float ff = (float)f;
+            error = ff > 1e-30f ? 1.0 + (double)((float)(f - (double)ff) * __builtin_amdgcn_rcpf(ff)) : 1.0;
+            if (lane == 0) factor[at] = ff;
+        };
+
+        // P[t][s] = exp(G_t - G_s) q_t . k_s for s <= t, in tiles (i, j) of 16 s x 16 t,
+        // i <= j, N of them at once
+        auto weigh_tiles = [&](int c, auto count, uint32_t tiles) {
+            constexpr int N = decltype(count)::value;
+            const int at = TWO ? c & 1 : 0;
+            const uint16_t *kat[N], *qat[N];
+            f32x4 x[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint32_t code = tiles >> (4 * n) & 15;
+                kat[n] = K0 + at * NP * M::KP + (16 * (code >> 2) + li) * M::KS + 8 * lg;
+                qat[n] = Q0 + at * NP * M::QP + (16 * (code & 3) + li) * M::QS + 8 * lg;
+                x[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            uint4 ka[2][N][NP], qb[2][N][NP];
+            auto load = [&](int pr) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int w = 0; w < NP; ++w) {
-                        const uint32_t lo = take_part(o[0], o[1]);
-                        *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(o[2], o[3]));
+                        ka[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(kat[n] + w * M::KP + 32 * pr);
+                        qb[pr & 1][n][w] = *reinterpret_cast<const uint4 *>(qat[n] + w * M::QP + 32 * pr);
                     }
-                }
             };
-            // codes 4 i + j of each wave's tiles; the last wave, which forms the decays, has the fewest
-            constexpr uint32_t kTiles4[4] = {0xb73, 0xa62, 0xf51, 0x0}, kTiles2[4] = {0x1, 0x5, 0x0, 0x0};
-            if (wave < 3)
-                weigh(std::integral_constant<int, TT == 4 ? 3 : 1>{}, TT == 4 ? kTiles4[wave] : kTiles2[wave]);
+            load(0);
+#pragma unroll
+            for (int pr = 0; pr < PAIRS; ++pr) {
+                if (pr + 1 < PAIRS) load(pr + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                mfma_tiles<N>(ka[pr & 1], qb[pr & 1], x);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const double *const gs = G0 + (c & 1) * C;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const uint32_t code = tiles >> (4 * n) & 15;
+                const int t = 16 * (code & 3) + li, s = 16 * (code >> 2) + 4 * lg;
+                const double gt = gs[t];
+                float o[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float d = (float)(gt - gs[s + r]);
+                    o[r] = x[n][r] * __builtin_amdgcn_exp2f(s + r <= t ? d : -__builtin_inff());
+                }
+#pragma unroll
+                for (int w = 0; w < NP; ++w) {
+                    const uint32_t lo = take_part(o[0], o[1]);
+                    *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(o[2], o[3]));
+                }
+            }
+        };
+        auto weigh = [&](int c) {
+            // codes 4 i + j of each maker's tiles
+            constexpr uint32_t kTiles4[kMakers] = {0xb73, 0xa62, 0xf51, 0x0}, kTiles2[kMakers] = {0x1, 0x5, 0x0, 0x0};
+            if (maker < 3)
+                weigh_tiles(c, std::integral_constant<int, TT == 4 ? 3 : 1>{}, TT == 4 ? kTiles4[maker] : kTiles2[maker]);
             else if constexpr (TT == 4)
-                weigh(std::integral_constant<int, 1>{}, kTiles4[3]);
+                weigh_tiles(c, std::integral_constant<int, 1>{}, kTiles4[3]);
+        };
 
-            // exp(G_t) S^T q_t
-            const uint16_t *qat = Qs + li * M::QS + 8 * lg;
+        // tiles above the diagonal that the products read: zero, once
+        if (FULL)
+            for (int i = mt; i < NP * M::PP; i += MT) Ps[i] = 0;
+        if (chunks > 0) {
+            fetch(0);
+            if (maker == kMakers - 1) {
+                fetch_decay(0);
+                form_decays(0);
+                fetch_decay(1);
+            }
+            store(0);
+            fetch(1);
+            __syncthreads();
+            if (FULL) {
+                weigh(0);
+                __syncthreads();
+            }
+            for (int c = 0; c < chunks; ++c) {
+                if (maker == kMakers - 1) {
+                    form_decays(c + 1);
+                    fetch_decay(c + 2);
+                }
+                if constexpr (!TWO) __syncthreads();
+                if (c + 1 < chunks) store(c + 1);
+                fetch(c + 2);
+                __syncthreads();
+                if (FULL) {
+                    if (c + 1 < chunks) weigh(c + 1);
+                    __syncthreads();
+                }
+            }
+        }
+        if (!FULL && vt == 0 && maker == kMakers - 1 && lane == 0) {
+            const double f = exp2(total);
+            reinterpret_cast<float2 *>(a.ws + p.off_decay)[bh * p.segs + seg] =
+                make_float2((float)f, (float)(f - (double)(float)f));
+        }
+    } else {
+        // ---------------------------------------------------------------- takers
+        // the state: tile 2P + u, register r = key row 32 P + 8 lg + 4 u + r, value column li of the wave
+        const int64_t cells = (int64_t)dk * dv;
+        const int col = 16 * wave + li;
+        f32x4 S[2 * PAIRS];
+        {
+            const float *from = nullptr;
+            if (FULL) {
+                if (p.segs > 1)
+                    from = reinterpret_cast<const float *>(a.ws) + (bh * p.segs + seg) * cells;
+                else if (a.state_in)
+                    from = a.state_in + bh * cells;
+            }
+#pragma unroll
+            for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
+                    S[t][r] = from && row < dk && col < vcols ? from[(int64_t)row * dv + v0 + col] : 0.f;
+                }
+        }
+        f32x4 acc[TT];
+        uint4 va[KK][NP];
+        // V of this wave's columns as an operand: value column li, tokens 32 kk + 8 lg + 0..7
+        auto load_values = [&](int c) {
+            const uint16_t *const Vs = V0 + (TWO ? c & 1 : 0) * NP * M::VP;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                for (int w = 0; w < NP; ++w) {
+                    const uint16_t *at = Vs + w * M::VP + (32 * kk + 8 * lg + (li >> 2)) * M::VS + 16 * wave + 4 * (li & 3);
+                    const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::VS);
+                    va[kk][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+        };
+        // acc = y / scale: exp(G_t) S^T q_t, then P V
+        auto form_y = [&](int c) {
+            const int buf = TWO ? c & 1 : 0;
+            const uint16_t *const qat = Q0 + buf * NP * M::QP + li * M::QS + 8 * lg;
             uint4 qb[2][TT][NP];
             auto load = [&](int pr) {
 #pragma unroll
@@ -399,6 +489,7 @@ __global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linatt
 #pragma unroll
             for (int pr = 0; pr < PAIRS; ++pr) {
                 if (pr + 1 < PAIRS) load(pr + 1);
+                if (pr == PAIRS - 1) load_values(c);
                 __builtin_amdgcn_sched_barrier(0);
                 float x[8];
 #pragma unroll
@@ -412,39 +503,12 @@ __global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linatt
                 mfma_tiles<TT>(sa, qb[pr & 1], acc);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            const float *const fs = F0 + (c & 1) * C;
 #pragma unroll
             for (int j = 0; j < TT; ++j) acc[j] *= fs[16 * j + li];
-            __syncthreads();
-        }
-        // V of this wave's columns as an operand: value column li, tokens 32 kk + 8 lg + 0..7
-        uint4 va[KK][NP];
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-            for (int w = 0; w < NP; ++w) {
-                const uint16_t *at = Vs + w * M::VP + (32 * kk + 8 * lg + (li >> 2)) * M::VS + 16 * wave + 4 * (li & 3);
-                const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::VS);
-                va[kk][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            }
-        // K transposed, KG tiles of key rows at a time, loaded one time ahead
-        constexpr int KG = NP == 3 || DK == 32 || DK == 256 ? 2 : 4, KN = KK * 2 * PAIRS / KG;
-        uint4 ka[2][KG][NP];
-        auto load_keys = [&](int n) {
-            const int kk = n / (2 * PAIRS / KG);
-#pragma unroll
-            for (int g = 0; g < KG; ++g) {
-                const int t = n % (2 * PAIRS / KG) * KG + g;
-#pragma unroll
-                for (int w = 0; w < NP; ++w) {
-                    const uint16_t *at = Ks + w * M::KP + (32 * kk + 8 * lg + (li >> 2)) * M::KS + 16 * (t & ~1) +
-                                         8 * (li & 3) + 4 * (t & 1);
-                    const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::KS);
-                    ka[n & 1][g][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                }
-            }
         };
-        if constexpr (FULL) {
-            const uint16_t *pat = Ps + li * M::PS + 8 * lg;
+        auto add_near = [&](int c) {
+            const uint16_t *const pat = Ps + li * M::PS + 8 * lg;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 uint4 pb[TT][NP], vv[TT][NP];  // tiles j from 2 kk on
@@ -455,59 +519,20 @@ __global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linatt
                         pb[j - 2 * kk][w] = *reinterpret_cast<const uint4 *>(pat + w * M::PP + 16 * j * M::PS + 32 * kk);
                         vv[j - 2 * kk][w] = va[kk][w];
                     }
-                if (kk == KK - 1) load_keys(0);
-                __builtin_amdgcn_sched_barrier(0);
                 if (kk == 0)
                     mfma_tiles<TT>(vv, pb, acc);
                 else
                     mfma_tiles<2>(vv, pb, acc + 2 * kk);
-                __builtin_amdgcn_sched_barrier(0);
             }
-        } else {
-            load_keys(0);
-        }
-        // the state
-        const float f = factor[odd];
-#pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
-        uint4 vb[KG][3];
-#pragma unroll
-        for (int n = 0; n < KN; ++n) {
-            const int kk = n / (2 * PAIRS / KG), first = n % (2 * PAIRS / KG) * KG;
-            if (n + 1 < KN) load_keys(n + 1);
-            if (first == 0) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w0 = reinterpret_cast<const uint32_t *>(&va[kk][0])[e];
-                    x[2 * e] = bf16_lo(w0);
-                    x[2 * e + 1] = bf16_hi(w0);
-                    if constexpr (NP == 3) {
-                        const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
-                        const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
-                        x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
-                        x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
-                split8(x, vb[0]);
-#pragma unroll
-                for (int g = 1; g < KG; ++g)
-#pragma unroll
-                    for (int w = 0; w < 3; ++w) vb[g][w] = vb[0][w];
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            mfma_tiles<KG>(ka[n & 1], vb, S + first);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (FULL) {
-            const int c = 16 * wave + 4 * lg;
-            T *at = y + (t0 + li) * a.ld_y + c;
-            const bool whole = t0 + C <= end - begin;
+        };
+        auto store_y = [&](int c) {
+            const int64_t t0 = (int64_t)c * C, n = end - begin - t0;
+            const int vc = 16 * wave + 4 * lg;
+            T *at = y + (t0 + li) * a.ld_y + vc;
+            const bool whole = n >= C;
 #pragma unroll
             for (int j = 0; j < TT; ++j, at += 16 * a.ld_y) {
-                if (c >= vcols || !(whole || t0 + 16 * j + li < end - begin)) continue;
+                if (vc >= vcols || !(whole || 16 * j + li < n)) continue;
                 const f32x4 o = acc[j] * a.s.scale;
                 if constexpr (G == 16 || (G == 8 && ACT == kBF16)) {
                     if constexpr (ACT == kBF16)
@@ -517,30 +542,102 @@ __global__ __launch_bounds__(kThreads, (ChunkGeom<ACT, DK>::kPerCU)) void linatt
                 } else {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (c + r < vcols) Act<ACT>::st(at + r, o[r]);
+                        if (vc + r < vcols) Act<ACT>::st(at + r, o[r]);
+                }
+            }
+        };
+        auto advance = [&](int c) {
+            const int buf = TWO ? c & 1 : 0;
+            const uint16_t *const kat = K0 + buf * NP * M::KP + (8 * lg + (li >> 2)) * M::KS + 8 * (li & 3);
+            // K transposed, KG tiles of key rows at a time, loaded one time ahead
+            constexpr int KG = NP == 3 || DK == 32 ? 2 : 4, KPK = 2 * PAIRS / KG, KN = KK * KPK;
+            uint4 ka[2][KG][NP], vb[KG][3];
+            auto load = [&](int n) {
+#pragma unroll
+                for (int g = 0; g < KG; ++g) {
+                    const int t = n % KPK * KG + g;
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) {
+                        const uint16_t *at = kat + w * M::KP + 32 * (n / KPK) * M::KS + 16 * (t & ~1) + 4 * (t & 1);
+                        const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::KS);
+                        ka[n & 1][g][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    }
+                }
+            };
+            load(0);
+            const float f = factor[c & 1];
+            const float *const te = E0 + (c & 1) * C;
+#pragma unroll
+            for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
+#pragma unroll
+            for (int n = 0; n < KN; ++n) {
+                const int kk = n / KPK, first = n % KPK * KG;
+                if (n + 1 < KN) load(n + 1);
+                if (first == 0) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t w0 = reinterpret_cast<const uint32_t *>(&va[kk][0])[e];
+                        x[2 * e] = bf16_lo(w0);
+                        x[2 * e + 1] = bf16_hi(w0);
+                        if constexpr (NP == 3) {
+                            const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
+                            const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
+                            x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
+                            x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
+                    split8(x, vb[0]);
+#pragma unroll
+                    for (int g = 1; g < KG; ++g)
+#pragma unroll
+                        for (int w = 0; w < 3; ++w) vb[g][w] = vb[0][w];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                mfma_tiles<KG>(ka[n & 1], vb, S + first);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+
+        if (chunks > 0) {
+            __syncthreads();
+            if (FULL) __syncthreads();
+            for (int c = 0; c < chunks; ++c) {
+                if constexpr (FULL) {
+                    form_y(c);
+                    add_near(c);
+                    if constexpr (TWO) __syncthreads();
+                    advance(c);
+                    store_y(c);
+                } else {
+                    load_values(c);
+                    advance(c);
+                }
+                __syncthreads();
+                if constexpr (!TWO) {
+                    __syncthreads();
+                    if (FULL) __syncthreads();
                 }
             }
         }
+        float *const to = FULL ? a.state_out + bh * cells
+                               : reinterpret_cast<float *>(a.ws) + (bh * p.segs + seg + 1) * cells;
+        if (!FULL || seg == p.segs - 1) {
+#pragma unroll
+            for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
+                    if (row < dk && col < vcols) to[(int64_t)row * dv + v0 + col] = S[t][r];
+                }
+        }
     }
     if (FULL) {  // rows past the tokens
-        const int64_t done = (rows + C - 1) / C * C, n = end - begin - done;
-        for (int64_t i = tid; i < n * vcols; i += kThreads)
+        const int64_t done = (int64_t)chunks * C, n = end - begin - done;
+        for (int64_t i = tid; i < n * vcols; i += M::kThreads)
             Act<ACT>::st(y + (done + i / vcols) * a.ld_y + i % vcols, 0.f);
-    }
-    float *to = FULL ? a.state_out + bh * cells : reinterpret_cast<float *>(a.ws) + (bh * p.segs + seg + 1) * cells;
-    if (!FULL || seg == p.segs - 1) {
-#pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
-                if (row < dk && col < vcols) to[(int64_t)row * dv + v0 + col] = S[t][r];
-            }
-    }
-    if (!FULL && vt == 0 && wave == 3 && lane == 0) {
-        const double f = exp2(total);
-        reinterpret_cast<float2 *>(a.ws + p.off_decay)[bh * p.segs + seg] =
-            make_float2((float)f, (float)(f - (double)(float)f));
     }
 }
 
@@ -608,9 +705,12 @@ int padded_dk(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 :
 LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     LinAttnPlan p;
     p.chunk = s.act == kBF16 && s.dk <= 128 ? 64 : 32;
-    p.vtiles = (s.dv + kVT - 1) / kVT;
+    // 128 value columns a workgroup where there are more than 64, the LDS holds two
+    // chunks of them and the registers of three waves a SIMD the state
+    p.vt = s.dv > 64 && s.dk <= (s.act == kBF16 ? 128 : 64) ? 128 : 64;
+    p.vtiles = (s.dv + p.vt - 1) / p.vt;
     const int64_t chunks = (L + p.chunk - 1) / p.chunk, groups = s.B * s.H * p.vtiles;
-    int64_t segs = groups >= 512 ? 1 : (512 + groups - 1) / groups;
+    int64_t segs = groups >= 256 ? 1 : (256 + groups - 1) / groups;
     if (segs > chunks / 8) segs = chunks / 8;
     if (segs < 1) segs = 1;
     p.seg_chunks = (chunks + segs - 1) / segs;
@@ -631,30 +731,37 @@ int linattn_granule(const LinAttnArgs &a) {
     return bits % 16 == 0 && near ? 16 : bits % 8 == 0 ? 8 : e;
 }
 
-template <int ACT, int DK, int G, bool FULL>
+template <int ACT, int DK, int VT, int G, bool FULL>
 hipError_t launch_chunks(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
-    constexpr int bytes = ChunkGeom<ACT, DK>::kBytes;
-    const auto kernel = linattn_chunk_kernel<ACT, DK, G, FULL>;
-    if (bytes > 65536) {
+    using M = ChunkGeom<ACT, DK, VT>;
+    const auto kernel = linattn_chunk_kernel<ACT, DK, VT, G, FULL>;
+    if (M::kBytes > 65536) {
         const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, M::kBytes);
         if (err != hipSuccess) return err;
     }
     const int64_t units = a.s.B * a.s.H * p.segs;
-    kernel<<<dim3((unsigned)((units + 7) / 8 * 8 * p.vtiles)), kThreads, bytes, stream>>>(a, p);
+    kernel<<<dim3((unsigned)((units + 7) / 8 * 8 * p.vtiles)), M::kThreads, M::kBytes, stream>>>(a, p);
     return hipGetLastError();
 }
 
-template <int ACT, int DK, int G>
+template <int ACT, int DK, int VT, int G>
 hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
     if (p.segs > 1) {
-        hipError_t err = launch_chunks<ACT, DK, G, false>(a, p, stream);
+        hipError_t err = launch_chunks<ACT, DK, VT, G, false>(a, p, stream);
         if (err != hipSuccess) return err;
         const dim3 grid((unsigned)(a.s.B * a.s.H), (unsigned)((a.s.dk * a.s.dv + kThreads - 1) / kThreads));
         linattn_join_kernel<<<grid, kThreads, 0, stream>>>(a, p);
         if ((err = hipGetLastError()) != hipSuccess) return err;
     }
-    return launch_chunks<ACT, DK, G, true>(a, p, stream);
+    return launch_chunks<ACT, DK, VT, G, true>(a, p, stream);
+}
+
+template <int ACT, int DK, int G>
+hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
+    if constexpr (DK <= (ACT == kBF16 ? 128 : 64))
+        if (p.vt == 128) return launch_prompt<ACT, DK, 128, G>(a, p, stream);
+    return launch_prompt<ACT, DK, 64, G>(a, p, stream);
 }
 
 template <int ACT, int DK>
