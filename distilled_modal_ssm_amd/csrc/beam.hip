@@ -48,6 +48,11 @@ __device__ __forceinline__ float wave_sort(float x) {
     return x;
 }
 
+__device__ __forceinline__ uint64_t uniform(uint64_t x) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x);
+}
+
 struct BestShared {
     Best list[kList];
     float bound[kWaves];
@@ -289,36 +294,54 @@ struct ReorderArgs {
     int64_t bytes[kBuffers];
 };
 
-// One workgroup for a group, a buffer and 256 pieces of its rows.  A thread
-// moves its piece in every row of the group, all reads before the first write,
-// so the rows need no other order and no second buffer.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kMoves = 4;  // pieces of a row that a thread moves, one after the other
+
+// One workgroup for a group, a buffer and kMoves * 256 pieces of its rows.  A
+// thread moves its piece in every row of the group, all reads before the first
+// write, so the rows need no other order and no second buffer.  A parent is read
+// once however many beams continue it; a row that stays is not touched, but as
+// some other's parent.
 template <typename T, int K>
 __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(ReorderArgs a) {
+    __shared__ uint64_t kids[kMaxSelect];  // beams, but itself, that continue each beam
+    const int tid = threadIdx.x;
+    const int32_t *parent = a.parents + (int64_t)blockIdx.y * a.beams;
+    if (tid < a.beams) {
+        uint64_t m = 0;
+        for (int k = 0; k < a.beams; ++k)
+            if (k != tid && parent[k] == tid) m |= uint64_t(1) << k;
+        kids[tid] = m;
+    }
     int i = 0;
     while (i + 1 < a.n && (int)blockIdx.x >= a.first[i + 1]) ++i;
     const int64_t pieces = a.bytes[i] / (int64_t)sizeof(T);
-    const int64_t at = ((int64_t)blockIdx.x - a.first[i]) * kThreads + threadIdx.x;
-    if (at >= pieces) return;
-    const int32_t *parent = a.parents + (int64_t)blockIdx.y * a.beams;
-    T *rows = reinterpret_cast<T *>(a.buf[i]) + (int64_t)blockIdx.y * a.beams * pieces + at;
-    T x[K];
+    const int64_t first = ((int64_t)blockIdx.x - a.first[i]) * (kMoves * kThreads) + tid;
+    T *rows = reinterpret_cast<T *>(a.buf[i]) + (int64_t)blockIdx.y * a.beams * pieces;
+    __syncthreads();
+    for (int64_t at = first; at < pieces && at < first + kMoves * kThreads; at += kThreads) {
+        T x[K];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int p = k < a.beams ? parent[k] : k;
-        if (p != k && p >= 0 && p < a.beams) x[k] = rows[p * pieces];
-    }
+        for (int p = 0; p < K; ++p)
+            if (p < a.beams && uniform(kids[p]) != 0) x[p] = rows[p * pieces + at];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int p = k < a.beams ? parent[k] : k;
-        if (p != k && p >= 0 && p < a.beams) rows[k * pieces] = x[k];
+        for (int p = 0; p < K; ++p) {
+            for (uint64_t m = p < a.beams ? uniform(kids[p]) : 0; m != 0; m &= m - 1)
+                rows[__builtin_ctzll(m) * pieces + at] = x[p];
+        }
     }
 }
 
 template <typename T>
 void launch_reorder(const ReorderArgs &a, int64_t groups, hipStream_t stream) {
     const dim3 grid((unsigned)a.first[a.n], (unsigned)groups);
+    // registers for a piece of every beam
     if (a.beams <= 8)
         beam_reorder_kernel<T, 8><<<grid, kThreads, 0, stream>>>(a);
+    else if (a.beams <= 16)
+        beam_reorder_kernel<T, 16><<<grid, kThreads, 0, stream>>>(a);
     else
         beam_reorder_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
 }
@@ -343,8 +366,10 @@ hipError_t launch_beam_select(const BeamSelectArgs &a, hipStream_t stream) {
 hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n, void *const *buffers,
                                const int64_t *row_bytes, hipStream_t stream) {
     if (beams == 1) return hipSuccess;
-    // buffers of one piece size share a launch: 16 bytes where all rows allow it, else 4, else 1
-    for (int size : {16, 4, 1}) {
+    // buffers of one piece size share a launch: 16 bytes where all rows allow it (8
+    // for more than 16 beams: a thread holds a piece of each), else 4, else 1
+    const int widest = beams <= 16 ? 16 : 8;
+    for (int size : {widest, 4, 1}) {
         ReorderArgs a;
         a.parents = parents;
         a.beams = (int)beams;
@@ -353,17 +378,19 @@ hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *par
         for (int64_t i = 0; i <= n; ++i) {
             if (i < n && row_bytes[i] > 0) {
                 const uintptr_t bits = reinterpret_cast<uintptr_t>(buffers[i]) | (uintptr_t)row_bytes[i];
-                const int fits = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+                const int fits = bits % widest == 0 ? widest : bits % 4 == 0 ? 4 : 1;
                 if (fits == size) {
+                    const int64_t block = (int64_t)size * kMoves * kThreads;
                     a.buf[a.n] = static_cast<unsigned char *>(buffers[i]);
                     a.bytes[a.n] = row_bytes[i];
-                    a.first[a.n + 1] = a.first[a.n] + (int)((row_bytes[i] / size + kThreads - 1) / kThreads);
+                    a.first[a.n + 1] = a.first[a.n] + (int)((row_bytes[i] + block - 1) / block);
                     ++a.n;
                 }
             }
-            // (a buffer has at most 2^28 workgroups)
+            // (a buffer has at most 2^26 workgroups)
             if (a.n == kBuffers || a.first[a.n] >= 1 << 29 || (i == n && a.n > 0)) {
-                if (size == 16) launch_reorder<uint4>(a, groups, stream);
+                if (size == 16) launch_reorder<u32x4>(a, groups, stream);
+                if (size == 8) launch_reorder<u32x2>(a, groups, stream);
                 if (size == 4) launch_reorder<uint32_t>(a, groups, stream);
                 if (size == 1) launch_reorder<uint8_t>(a, groups, stream);
                 const hipError_t err = hipGetLastError();

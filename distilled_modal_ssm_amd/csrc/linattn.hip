@@ -43,6 +43,7 @@ namespace hm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxDk = 256;
 
 // exp(a) of a log decay; a is bounded below so that sums of it stay finite
 __device__ __forceinline__ float bound_decay(float a) { return a < -1000.f ? -1000.f : a; }
@@ -660,43 +661,96 @@ __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinAttnArgs a, L
 
 // ------------------------------------------------------------------ one token
 
-// One workgroup for a batch row and head: lane = value column, the four waves
-// take every fourth key row.
-template <int ACT>
-__global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a) {
+// One workgroup for a batch row, a head and a tile of LANES * V value columns:
+// LANES threads of V columns a key row, 256 / LANES rows at a time, every row's
+// load of a thread in flight before the first is used (in turns of 16).
+// Bound by the state's way in and out.
+template <int ACT, int LANES, int V>
+__global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, int vtiles) {
     using T = typename Act<ACT>::T;
-    __shared__ float qs[256], ks[256], part[4][64];
-    const int64_t b = blockIdx.x / a.s.H, h = blockIdx.x - b * a.s.H;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, dk = a.s.dk, dv = a.s.dv;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    constexpr int ROWS = kThreads / LANES, TILE = LANES * V, FLY = LANES == 8 ? 8 : 16;
+    __shared__ float2 qk[kMaxDk];  // q scale, k
+    __shared__ vec part[kThreads / kWave][LANES];
+    const int64_t unit = blockIdx.x / vtiles, b = unit / a.s.H, h = unit - b * a.s.H;
+    const int tid = threadIdx.x, lane = tid % LANES, row0 = tid / LANES, dk = a.s.dk, dv = a.s.dv;
+    const int col = (int)(blockIdx.x - unit * vtiles) * TILE + lane * V;
     int64_t src = b;
-    if (a.src_rows && a.src_rows[b] >= 0 && a.src_rows[b] < a.s.B) src = a.src_rows[b];
-    const float *in = a.state_in + (src * a.s.H + h) * (int64_t)dk * dv;
-    float *out = a.state_out + (b * a.s.H + h) * (int64_t)dk * dv;
-    const T *v = static_cast<const T *>(a.v) + b * a.ld_v + h * a.s.vh / a.s.H * dv;
-    T *y = static_cast<T *>(a.y) + b * a.ld_y + h * dv;
-    if (tid < dk) {
-        qs[tid] = Act<ACT>::ld(static_cast<const T *>(a.q) + b * a.ld_q + h * a.s.qh / a.s.H * dk + tid);
-        ks[tid] = Act<ACT>::ld(static_cast<const T *>(a.k) + b * a.ld_k + h * a.s.kh / a.s.H * dk + tid);
+    if (a.src_rows) {
+        const int s = a.src_rows[b];
+        if (s >= 0 && s < a.s.B) src = s;
     }
+    const float *in = a.state_in + (src * a.s.H + h) * (int64_t)dk * dv + col;
+    float *out = a.state_out + unit * (int64_t)dk * dv + col;
+    const bool own = col < dv;  // V divides dv
+    vec s[FLY];
+#pragma unroll
+    for (int n = 0; n < FLY; ++n) {
+        const int i = row0 + n * ROWS;
+        if (own && i < dk) s[n] = __builtin_nontemporal_load(reinterpret_cast<const vec *>(in + (int64_t)i * dv));
+    }
+    for (int i = tid; i < dk; i += kThreads)
+        qk[i] = make_float2(
+            a.s.scale * Act<ACT>::ld(static_cast<const T *>(a.q) + b * a.ld_q + h * a.s.qh / a.s.H * dk + i),
+            Act<ACT>::ld(static_cast<const T *>(a.k) + b * a.ld_k + h * a.s.kh / a.s.H * dk + i));
     const float g = a.decay ? expf(bound_decay(a.decay[a.ld_decay ? b * a.ld_decay + h : h])) : 1.f;
+    vec v = {}, y = {};
+    if (own) {
+        const T *at = static_cast<const T *>(a.v) + b * a.ld_v + h * a.s.vh / a.s.H * dv + col;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = Act<ACT>::ld(at + e);
+    }
     __syncthreads();
-    for (int c0 = 0; c0 < dv; c0 += 64) {
-        const int c = c0 + lane;
-        float o = 0.f;
-        if (c < dv) {
-            const float x = Act<ACT>::ld(v + c);
-            for (int i = wave; i < dk; i += 4) {
-                const float s = fmaf(g, in[(int64_t)i * dv + c], ks[i] * x);
-                out[(int64_t)i * dv + c] = s;
-                o = fmaf(qs[i], s, o);
+    for (int n0 = 0; n0 * ROWS < dk; n0 += FLY) {
+        if (n0 > 0)
+#pragma unroll
+            for (int n = 0; n < FLY; ++n) {
+                const int i = row0 + (n0 + n) * ROWS;
+                if (own && i < dk) s[n] = __builtin_nontemporal_load(reinterpret_cast<const vec *>(in + (int64_t)i * dv));
+            }
+#pragma unroll
+        for (int n = 0; n < FLY; ++n) {
+            const int i = row0 + (n0 + n) * ROWS;
+            if (own && i < dk) {
+                const float2 w = qk[i];
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    s[n][e] = fmaf(g, s[n][e], w.y * v[e]);
+                    y[e] = fmaf(w.x, s[n][e], y[e]);
+                }
+                __builtin_nontemporal_store(s[n], reinterpret_cast<vec *>(out + (int64_t)i * dv));
             }
         }
-        part[wave][lane] = o;
-        __syncthreads();
-        if (tid < 64 && c < dv)
-            Act<ACT>::st(y + c, a.s.scale * (part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]));
-        __syncthreads();
     }
+    // the rows' parts of y: within a wave, then over the waves
+#pragma unroll
+    for (int m = LANES; m < kWave; m <<= 1)
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] += __shfl_xor(y[e], m);
+    if ((tid & (kWave - 1)) < LANES) part[tid / kWave][lane] = y;
+    __syncthreads();
+    if (tid < LANES && own) {
+        const vec o = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+        T *at = static_cast<T *>(a.y) + b * a.ld_y + h * dv + col;
+#pragma unroll
+        for (int e = 0; e < V; ++e) Act<ACT>::st(at + e, o[e]);
+    }
+}
+
+template <int ACT, int LANES, int V>
+hipError_t launch_token(const LinAttnArgs &a, hipStream_t stream) {
+    const int vtiles = (a.s.dv + LANES * V - 1) / (LANES * V);
+    linattn_token_kernel<ACT, LANES, V><<<dim3((unsigned)(a.s.B * a.s.H * vtiles)), kThreads, 0, stream>>>(a, vtiles);
+    return hipGetLastError();
+}
+
+template <int ACT>
+hipError_t launch_token(const LinAttnArgs &a, hipStream_t stream) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.state_in) | reinterpret_cast<uintptr_t>(a.state_out);
+    if (bits % 16 != 0 || a.s.dv % 4 != 0) return launch_token<ACT, 64, 1>(a, stream);
+    const int64_t units = a.s.B * a.s.H;
+    if (units * ((a.s.dv + 127) / 128) >= 512) return launch_token<ACT, 32, 4>(a, stream);
+    return launch_token<ACT, 8, 4>(a, stream);
 }
 
 // Padded key width, and the granule of 16, 8 bytes or an element that all rows allow.
@@ -793,12 +847,7 @@ hipError_t launch_linattn_prefill(const LinAttnArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_linattn_decode(const LinAttnArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.s.B * a.s.H));
-    if (a.s.act == kBF16)
-        linattn_token_kernel<kBF16><<<grid, kThreads, 0, stream>>>(a);
-    else
-        linattn_token_kernel<kF32><<<grid, kThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    return a.s.act == kBF16 ? launch_token<kBF16>(a, stream) : launch_token<kF32>(a, stream);
 }
 
 }  // namespace hm
