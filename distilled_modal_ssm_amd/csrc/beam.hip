@@ -28,25 +28,60 @@ struct Best {
 
 __device__ __forceinline__ bool before(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor(x, m));
+// x of the lane whose number differs in bit J.
+template <int J>
+__device__ __forceinline__ float across(float x) {
+    const int b = __float_as_int(x);
+    if constexpr (J == 1) return __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0xb1, 0xf, 0xf, false));  // quad 1 0 3 2
+    if constexpr (J == 2) return __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x4e, 0xf, 0xf, false));  // quad 2 3 0 1
+    if constexpr (J == 4) {  // banks 0 and 2 of a row from 4 lanes on, 1 and 3 from 4 lanes before
+        const int up = __builtin_amdgcn_update_dpp(0, b, 0x104, 0xf, 0x5, false);
+        return __int_as_float(__builtin_amdgcn_update_dpp(up, b, 0x114, 0xf, 0xa, false));
+    }
+    if constexpr (J == 8) return __int_as_float(__builtin_amdgcn_update_dpp(0, b, 0x128, 0xf, 0xf, false));  // row turned by 8
+    return __shfl_xor(x, J);
+}
+
+template <int K, int J>
+__device__ __forceinline__ void sort_steps(float &x, int lane) {
+    const float y = across<J>(x);
+    const bool large = ((lane & J) == 0) == ((lane & K) == 0);
+    x = large ? fmaxf(x, y) : fminf(x, y);
+    if constexpr (J > 1) sort_steps<K, J / 2>(x, lane);
+}
+
+// The 64 lanes' values in decreasing order (a bitonic network).
+__device__ __forceinline__ float wave_sort(float x) {
+    const int lane = threadIdx.x & 63;
+    sort_steps<2, 1>(x, lane);
+    sort_steps<4, 2>(x, lane);
+    sort_steps<8, 4>(x, lane);
+    sort_steps<16, 8>(x, lane);
+    sort_steps<32, 16>(x, lane);
+    sort_steps<64, 32>(x, lane);
     return x;
 }
 
-// The 64 lanes' values in decreasing order.
-__device__ __forceinline__ float wave_sort(float x) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            const float y = __shfl_xor(x, j);
-            const bool up = (lane & k) != 0, low = (lane & j) == 0;
-            x = (low != up) ? fmaxf(x, y) : fminf(x, y);
-        }
-    return x;
+__device__ __forceinline__ float wave_sum(float x) {
+    x += across<1>(x);
+    x += across<2>(x);
+    x += across<4>(x);
+    x += across<8>(x);
+    x += across<16>(x);
+    return x + across<32>(x);
 }
+
+__device__ __forceinline__ float wave_max(float x) {
+    x = fmaxf(x, across<1>(x));
+    x = fmaxf(x, across<2>(x));
+    x = fmaxf(x, across<4>(x));
+    x = fmaxf(x, across<8>(x));
+    x = fmaxf(x, across<16>(x));
+    return fmaxf(x, across<32>(x));
+}
+
+// exp(d) for d <= 0, to 2^-22 of it and the rounding of d's product
+__device__ __forceinline__ float exp_below(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); }
 
 __device__ __forceinline__ uint64_t uniform(uint64_t x) {
     return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 |
@@ -62,24 +97,22 @@ struct BestShared {
 
 // The best n (<= 64) of the workgroup's values, kThreads x E in registers, by
 // (value, lowest index), into out[0 .. n) in that order; values of -infinity are
-// absent, and missing places get {-infinity, kNone}.  Indices differ.
+// absent, and missing places get {-infinity, kNone}.  index(e): the index of x[e];
+// no two are alike.  sorted: wave_sort of the threads' largest, top the thread's.
 //
 // The n-th largest of a wave's 64 lane maxima bounds the n-th best value from
 // below, and so does the largest of the waves' bounds: what is below it is out.
 // The rest, n and a few more, is listed and each entry put at its rank.  Values
 // that are equal many times over can overrun the list; then the best are taken
 // out one by one instead.
-template <int E>
-__device__ __forceinline__ void block_best(const float (&x)[E], const int (&idx)[E], int n, BestShared &sh, Best *out) {
+template <int E, typename Index>
+__device__ __forceinline__ void block_best(const float (&x)[E], Index index, float top, float sorted, int n,
+                                           BestShared &sh, Best *out) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    float top = kNever;
-#pragma unroll
-    for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
-    const float sorted = wave_sort(top);
-    const float nth = __shfl(sorted, n - 1);
+    const float nth = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sorted), n - 1));
     if (lane == 0) sh.bound[wave] = nth;
     if (tid == 0) sh.count = 0;
-    for (int i = tid; i < n; i += kThreads) out[i] = {kNever, kNone};
+    if (tid < n) out[tid] = {kNever, kNone};
     __syncthreads();
     float bound = sh.bound[0];
 #pragma unroll
@@ -89,7 +122,7 @@ __device__ __forceinline__ void block_best(const float (&x)[E], const int (&idx)
         for (int e = 0; e < E; ++e)
             if (x[e] >= bound && x[e] > kNever) {
                 const int at = atomicAdd(&sh.count, 1);
-                if (at < kList) sh.list[at] = {x[e], idx[e]};
+                if (at < kList) sh.list[at] = {x[e], index(e)};
             }
     }
     __syncthreads();
@@ -108,11 +141,13 @@ __device__ __forceinline__ void block_best(const float (&x)[E], const int (&idx)
             float bx = kNever;
             int bi = kNone;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (before(lx, li, x[e], idx[e]) && x[e] > kNever && before(x[e], idx[e], bx, bi)) {
+            for (int e = 0; e < E; ++e) {
+                const int i = index(e);
+                if (before(lx, li, x[e], i) && x[e] > kNever && before(x[e], i, bx, bi)) {
                     bx = x[e];
-                    bi = idx[e];
+                    bi = i;
                 }
+            }
 #pragma unroll
             for (int m = 32; m > 0; m >>= 1) {
                 const float ox = __shfl_xor(bx, m);
@@ -140,137 +175,174 @@ __device__ __forceinline__ void block_best(const float (&x)[E], const int (&idx)
 
 // ------------------------------------------------------------------ segments
 
-constexpr int kSegE = 32;                       // logits of a thread
-constexpr int kSegment = kThreads * kSegE;
-
 struct SelectPlan {
-    int64_t segs;
-    size_t off_stat, off_best, bytes;  // float2 [rows][segs] (max, sum); Best [rows][segs][select]
+    int each;                          // logits of a thread: a segment has 256 times as many
+    int segs;                          // segments of a row
+    size_t off_stat, off_best, bytes;  // float2 [rows][segs] (max, sum); Best [groups][select][beams][segs]
 };
 
+// Segments of 8192 logits where that gives two workgroups a CU, else of 2048.
+// (A row starts up to 7 elements into its first 16 bytes.)
 SelectPlan select_plan(int64_t groups, int64_t beams, int64_t vocab, int64_t select) {
     SelectPlan p;
-    p.segs = (vocab + kSegment - 1) / kSegment;
+    p.each = groups * beams * ((vocab + 8191) / 8192) >= 512 ? 32 : 8;
+    p.segs = (int)((vocab + 7 + kThreads * p.each - 1) / (kThreads * p.each));
     p.off_stat = 0;
     p.off_best = ((size_t)(groups * beams * p.segs) * sizeof(float2) + 255) / 256 * 256;
     p.bytes = p.off_best + (size_t)(groups * beams * p.segs * select) * sizeof(Best);
     return p;
 }
 
-template <int ACT>
+// One workgroup a segment of a row: 16 bytes a thread and load, E logits in
+// registers, read once.  Bound by that read.
+template <int ACT, int E>
 __global__ __launch_bounds__(kThreads) void beam_segment_kernel(BeamSelectArgs a, SelectPlan p) {
     using T = typename Act<ACT>::T;
+    constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
     __shared__ BestShared sh;
     __shared__ Best best[kMaxSelect];
-    __shared__ float red[kWaves];
-    const int64_t row = blockIdx.x / p.segs, seg = blockIdx.x - row * p.segs;
-    const int tid = threadIdx.x, n = (int)a.select;
+    __shared__ float2 stat[kWaves];
+    const int row = (int)(blockIdx.x / (unsigned)p.segs), seg = (int)blockIdx.x - row * p.segs;
+    const int tid = threadIdx.x, n = (int)a.select, V = (int)a.vocab;
     // a beam that has ended or is not alive has no continuation of its own here
     if (a.scores[row] == kNever || (a.finished && a.finished[row])) return;
-    const T *x = static_cast<const T *>(a.logits) + row * a.ld;
-    float val[kSegE];
-    int idx[kSegE];
+    const T *x = static_cast<const T *>(a.logits) + (int64_t)row * a.ld;
+    // from the 16 bytes that the row starts in
+    const int base = seg * (kThreads * E) - (int)(reinterpret_cast<uintptr_t>(x) % 16) / EB;
+    const auto index = [&](int e) { return base + (e / PER * kThreads + tid) * PER + e % PER; };
+    float val[E];
+#pragma unroll
+    for (int e = 0; e < E; e += PER) {
+        const int i = index(e);
+        if (i >= 0 && i + PER <= V) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(x + i);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                val[e + j] = ACT == kBF16 ? (j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2])) : __uint_as_float(u[j % 4]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) val[e + j] = i + j >= 0 && i + j < V ? Act<ACT>::ld(x + i + j) : kNever;
+        }
+    }
     float top = kNever;
 #pragma unroll
-    for (int e = 0; e < kSegE; ++e) {
-        idx[e] = (int)(seg * kSegment) + e * kThreads + tid;
-        const float f = idx[e] < a.vocab ? Act<ACT>::ld(x + idx[e]) : kNever;
-        val[e] = f == f ? f : kNever;
+    for (int e = 0; e < E; ++e) {
+        val[e] = val[e] == val[e] ? val[e] : kNever;
         top = fmaxf(top, val[e]);
     }
-    top = wave_max(top);
-    if ((tid & 63) == 0) red[tid >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red[w]);
-    __syncthreads();
+    const float sorted = wave_sort(top);
+    const float high = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(sorted)));
     float sum = 0.f;
-    if (top > kNever) {
+    if (high > kNever) {
 #pragma unroll
-        for (int e = 0; e < kSegE; ++e) sum += val[e] == top ? 1.f : __expf(val[e] - top);
+        for (int e = 0; e < E; ++e) sum += val[e] == high ? 1.f : exp_below(val[e] - high);
     }
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) stat[tid >> 6] = make_float2(high, sum);
+    block_best<E>(val, index, top, sorted, n, sh, best);
+    if (tid == 0) {
+        float m = kNever, s = 0.f;
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    if ((tid & 63) == 0) red[tid >> 6] = sum;
-    block_best<kSegE>(val, idx, n, sh, best);
-    const int64_t at = row * p.segs + seg;
-    if (tid == 0)
-        reinterpret_cast<float2 *>(a.ws + p.off_stat)[at] = make_float2(top, (red[0] + red[1]) + (red[2] + red[3]));
-    if (tid < n) reinterpret_cast<Best *>(a.ws + p.off_best)[at * n + tid] = best[tid];
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, stat[w].x);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+            if (stat[w].x > kNever) s += stat[w].x == m ? stat[w].y : stat[w].y * exp_below(stat[w].x - m);
+        reinterpret_cast<float2 *>(a.ws + p.off_stat)[(int64_t)row * p.segs + seg] = make_float2(m, s);
+    }
+    const int K = (int)a.beams, g = row / K;
+    if (tid < n)
+        reinterpret_cast<Best *>(a.ws + p.off_best)[((int64_t)(g * n + tid) * K + (row - g * K)) * p.segs + seg] = best[tid];
 }
 
 // ------------------------------------------------------------------ groups
 
 constexpr int kPickE = 8;
 
+// One workgroup a group.  What the segments handed on is taken rank by rank, all
+// segments' first ones first, so that the leads spread over the lanes and
+// block_best's bound is a tight one.
 __global__ __launch_bounds__(kThreads) void beam_pick_kernel(BeamSelectArgs a, SelectPlan p) {
     __shared__ BestShared sh;
     __shared__ Best best[kMaxSelect];
     __shared__ float score0[kMaxSelect], top[kMaxSelect], lse[kMaxSelect];  // lse: log of the sum, after the maximum
     __shared__ bool ended[kMaxSelect];
     const int64_t g = blockIdx.x;
-    const int tid = threadIdx.x, K = (int)a.beams, n = (int)a.select, V = (int)a.vocab;
-    const float2 *stat = reinterpret_cast<const float2 *>(a.ws + p.off_stat) + g * K * p.segs;
-    const Best *cand = reinterpret_cast<const Best *>(a.ws + p.off_best) + g * K * p.segs * n;
-    if (tid < K) {
-        const float s = a.scores[g * K + tid];
-        const bool f = a.finished && a.finished[g * K + tid];
+    const int tid = threadIdx.x, lane = tid & 63, K = (int)a.beams, n = (int)a.select, V = (int)a.vocab;
+    const unsigned lists = (unsigned)(K * p.segs), total = lists * n;
+    const float2 *stat = reinterpret_cast<const float2 *>(a.ws + p.off_stat) + g * lists;
+    const Best *cand = reinterpret_cast<const Best *>(a.ws + p.off_best) + g * total;
+    Best have[kPickE];
+    auto fetch = [&](unsigned c0) {
+#pragma unroll
+        for (int e = 0; e < kPickE; ++e) {
+            const unsigned c = c0 + e * kThreads + tid;
+            if (c < total) have[e] = cand[c];
+        }
+    };
+    fetch(0);
+    for (int k = tid >> 6; k < K; k += kWaves) {
+        const float s = a.scores[g * K + k];
+        const bool f = a.finished && a.finished[g * K + k];
         float m = kNever, sum = 0.f;
         if (!f && s > kNever) {
-            for (int64_t i = 0; i < p.segs; ++i) m = fmaxf(m, stat[tid * p.segs + i].x);
-            for (int64_t i = 0; i < p.segs; ++i) {
-                const float2 st = stat[tid * p.segs + i];
-                if (st.x > kNever) sum += st.x == m ? st.y : st.y * expf(st.x - m);
+            for (int i = lane; i < p.segs; i += 64) m = fmaxf(m, stat[k * p.segs + i].x);
+            m = wave_max(m);
+            for (int i = lane; i < p.segs; i += 64) {
+                const float2 st = stat[k * p.segs + i];
+                if (st.x > kNever) sum += st.x == m ? st.y : st.y * exp_below(st.x - m);
             }
+            sum = wave_sum(sum);
         }
-        score0[tid] = s;
-        ended[tid] = f;
-        top[tid] = m;
-        lse[tid] = logf(sum);
+        if (lane == 0) {
+            score0[k] = s;
+            ended[k] = f;
+            top[k] = m;
+            lse[k] = logf(sum);
+        }
     }
     if (tid < kMaxSelect) best[tid] = {kNever, kNone};
     __syncthreads();
-    const int64_t per = p.segs * n, total = K * per;
     float val[kPickE + 1];
     int idx[kPickE + 1];
-    for (int64_t c0 = 0; c0 < total; c0 += kThreads * kPickE) {
+    for (unsigned c0 = 0; c0 < total; c0 += kThreads * kPickE) {
+        if (c0 > 0) fetch(c0);
+        float high = kNever;
 #pragma unroll
         for (int e = 0; e < kPickE; ++e) {
-            const int64_t c = c0 + e * kThreads + tid;
+            const unsigned c = c0 + e * kThreads + tid;
             val[e] = kNever;
             idx[e] = kNone;
             if (c < total) {
-                const int k = (int)(c / per);
+                const unsigned list = c % lists, k = list / (unsigned)p.segs;
                 if (ended[k]) {  // one continuation, in the place of the beam's first
-                    if (c == k * per) {
+                    if (c == k * p.segs) {
                         val[e] = score0[k];
-                        idx[e] = k * V + (int)a.end_token;
+                        idx[e] = (int)k * V + (int)a.end_token;
                     }
-                } else if (score0[k] > kNever) {
-                    const Best x = cand[c];
-                    if (x.i != kNone) {
-                        const float d = x.x == top[k] ? 0.f : x.x - top[k];
-                        val[e] = score0[k] + (d - lse[k]);
-                        idx[e] = k * V + x.i;
-                    }
+                } else if (score0[k] > kNever && have[e].i != kNone) {
+                    const float d = have[e].x == top[k] ? 0.f : have[e].x - top[k];
+                    val[e] = score0[k] + (d - lse[k]);
+                    idx[e] = (int)k * V + have[e].i;
                 }
             }
+            high = fmaxf(high, val[e]);
         }
         // the best so far stay in
         val[kPickE] = tid < n ? best[tid].x : kNever;
         idx[kPickE] = tid < n ? best[tid].i : kNone;
+        high = fmaxf(high, val[kPickE]);
         __syncthreads();
-        block_best<kPickE + 1>(val, idx, n, sh, best);
+        block_best<kPickE + 1>(val, [&](int e) { return idx[e]; }, high, wave_sort(high), n, sh, best);
     }
     // fewer than n continuations: the first others, all of score -infinity
     if (tid == 0 && best[n - 1].i == kNone) {
-        int have = 0;
-        while (have < n && best[have].i != kNone) ++have;
-        const int found = have;
-        for (int f = 0; have < n; ++f) {
+        int found = 0;
+        while (found < n && best[found].i != kNone) ++found;
+        for (int at = found, f = 0; at < n; ++f) {
             bool taken = false;
             for (int j = 0; j < found; ++j) taken |= best[j].i == f;
-            if (!taken) best[have++].i = f;
+            if (!taken) best[at++].i = f;
         }
     }
     __syncthreads();
@@ -355,10 +427,16 @@ size_t beam_select_workspace(int64_t groups, int64_t beams, int64_t vocab, int64
 hipError_t launch_beam_select(const BeamSelectArgs &a, hipStream_t stream) {
     const SelectPlan p = select_plan(a.groups, a.beams, a.vocab, a.select);
     const dim3 grid((unsigned)(a.groups * a.beams * p.segs));
-    if (a.act == kBF16)
-        beam_segment_kernel<kBF16><<<grid, kThreads, 0, stream>>>(a, p);
-    else
-        beam_segment_kernel<kF32><<<grid, kThreads, 0, stream>>>(a, p);
+    if (p.each == 8) {
+        if (a.act == kBF16)
+            beam_segment_kernel<kBF16, 8><<<grid, kThreads, 0, stream>>>(a, p);
+        else
+            beam_segment_kernel<kF32, 8><<<grid, kThreads, 0, stream>>>(a, p);
+    } else if (a.act == kBF16) {
+        beam_segment_kernel<kBF16, 32><<<grid, kThreads, 0, stream>>>(a, p);
+    } else {
+        beam_segment_kernel<kF32, 32><<<grid, kThreads, 0, stream>>>(a, p);
+    }
     beam_pick_kernel<<<dim3((unsigned)a.groups), kThreads, 0, stream>>>(a, p);
     return hipGetLastError();
 }
