@@ -234,9 +234,12 @@ __global__ __launch_bounds__(kThreads) void beam_segment_kernel(BeamSelectArgs a
     const float sorted = wave_sort(top);
     const float high = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(sorted)));
     float sum = 0.f;
-    if (high > kNever) {
+    if (high == __builtin_inff()) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum += val[e] == high ? 1.f : exp_below(val[e] - high);
+        for (int e = 0; e < E; ++e) sum += val[e] == high ? 1.f : 0.f;
+    } else if (high > kNever) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += exp_below(val[e] - high);
     }
     sum = wave_sum(sum);
     if ((tid & 63) == 0) stat[tid >> 6] = make_float2(high, sum);

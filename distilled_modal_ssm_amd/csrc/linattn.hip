@@ -764,9 +764,19 @@ LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     p.vt = s.dv > 64 && s.dk <= (s.act == kBF16 ? 128 : 64) ? 128 : 64;
     p.vtiles = (s.dv + p.vt - 1) / p.vt;
     const int64_t chunks = (L + p.chunk - 1) / p.chunk, groups = s.B * s.H * p.vtiles;
-    int64_t segs = groups >= 256 ? 1 : (256 + groups - 1) / groups;
-    if (segs > chunks / 8) segs = chunks / 8;
-    if (segs < 1) segs = 1;
+    // Segments cost a second pass over k and v (kAgain of the full pass, measured)
+    // and pay by filling the GPU, one workgroup a CU: the least of rounds x chunks.
+    constexpr double kAgain = 0.6;
+    constexpr int64_t kCUs = 256, kFew = 4;  // kFew: chunks of a segment, at least
+    int64_t segs = 1;
+    double best = (double)((groups + kCUs - 1) / kCUs * chunks);
+    for (int64_t n = 2; n * kFew <= chunks && groups * n < 2 * kCUs; ++n) {
+        const double cost = (double)((groups * n + kCUs - 1) / kCUs * ((chunks + n - 1) / n)) * (1 + kAgain);
+        if (cost < best) {
+            best = cost;
+            segs = n;
+        }
+    }
     p.seg_chunks = (chunks + segs - 1) / segs;
     p.segs = p.seg_chunks > 0 ? (chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
     const size_t states = p.segs > 1 ? (size_t)(s.B * s.H * p.segs) * s.dk * s.dv * sizeof(float) : 0;
