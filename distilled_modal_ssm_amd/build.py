@@ -34,7 +34,14 @@ FLAGS = [
 # preloaded into SGPRs at wave launch instead of being fetched from the
 # argument segment (gfx950 kernarg preloading; the code keeps a prologue that
 # loads them for firmware without it).
-SOURCE_FLAGS = {"decode.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=9"]}
+#
+# No kernel of linear attention or beam search may use stack memory: the compiler
+# has been seen to save a vector register there where only some lanes were active
+# and to reload it where all were (a wrong address in a final store).  A kernel
+# that needs more registers than it has is an error, not a slow kernel.
+NO_STACK = ["-Xarch_device", "-Wframe-larger-than=0", "-Xarch_device", "-Werror=frame-larger-than"]
+SOURCE_FLAGS = {"decode.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=9"],
+                "linattn.hip": NO_STACK, "beam.hip": NO_STACK}
 
 
 def _compile(src: str) -> str:

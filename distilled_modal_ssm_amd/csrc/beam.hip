@@ -409,7 +409,8 @@ __global__ __launch_bounds__(kThreads) void beam_reorder_kernel(ReorderArgs a) {
     }
 }
 
-template <typename T>
+// MOST: beams that pieces of this size are used for
+template <typename T, int MOST>
 void launch_reorder(const ReorderArgs &a, int64_t groups, hipStream_t stream) {
     const dim3 grid((unsigned)a.first[a.n], (unsigned)groups);
     // registers for a piece of every beam
@@ -417,8 +418,12 @@ void launch_reorder(const ReorderArgs &a, int64_t groups, hipStream_t stream) {
         beam_reorder_kernel<T, 8><<<grid, kThreads, 0, stream>>>(a);
     else if (a.beams <= 16)
         beam_reorder_kernel<T, 16><<<grid, kThreads, 0, stream>>>(a);
-    else
-        beam_reorder_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
+    else if constexpr (MOST > 16) {
+        if (a.beams <= 32)
+            beam_reorder_kernel<T, 32><<<grid, kThreads, 0, stream>>>(a);
+        else if constexpr (MOST > 32)
+            beam_reorder_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
+    }
 }
 
 }  // namespace
@@ -448,9 +453,11 @@ hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *par
                                const int64_t *row_bytes, hipStream_t stream) {
     if (beams == 1) return hipSuccess;
     // buffers of one piece size share a launch: 16 bytes where all rows allow it (8
-    // for more than 16 beams: a thread holds a piece of each), else 4, else 1
-    const int widest = beams <= 16 ? 16 : 8;
-    for (int size : {widest, 4, 1}) {
+    // for more than 16 beams, 4 for more than 32: a thread holds a piece of each),
+    // else 4, else 1
+    const int widest = beams <= 16 ? 16 : beams <= 32 ? 8 : 4;
+    for (int size : {16, 8, 4, 1}) {
+        if (size > widest || (size == 8 && widest == 16)) continue;
         ReorderArgs a;
         a.parents = parents;
         a.beams = (int)beams;
@@ -470,10 +477,12 @@ hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *par
             }
             // (a buffer has at most 2^26 workgroups)
             if (a.n == kBuffers || a.first[a.n] >= 1 << 29 || (i == n && a.n > 0)) {
-                if (size == 16) launch_reorder<u32x4>(a, groups, stream);
-                if (size == 8) launch_reorder<u32x2>(a, groups, stream);
-                if (size == 4) launch_reorder<uint32_t>(a, groups, stream);
-                if (size == 1) launch_reorder<uint8_t>(a, groups, stream);
+                switch (size) {
+                    case 16: launch_reorder<u32x4, 16>(a, groups, stream); break;
+                    case 8: launch_reorder<u32x2, 32>(a, groups, stream); break;
+                    case 4: launch_reorder<uint32_t, 64>(a, groups, stream); break;
+                    default: launch_reorder<uint8_t, 64>(a, groups, stream);
+                }
                 const hipError_t err = hipGetLastError();
                 if (err != hipSuccess) return err;
                 a.n = 0;

@@ -859,6 +859,9 @@ hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const in
         if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;
     }
     if (desc->batch * desc->heads > INT32_MAX / 64) return HM_ERR_UNSUPPORTED;  // grid limit
+    // a chunk of 64 rows is addressed by 32-bit byte offsets
+    for (int64_t ld : {ld_q, ld_k, ld_v})
+        if (L > 0 && ld >= int64_t(1) << 22) return HM_ERR_UNSUPPORTED;
     a.lengths = lengths;
     a.ws = static_cast<unsigned char *>(workspace);
     return hm::launch_linattn_prefill(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;

@@ -88,38 +88,34 @@ __device__ __forceinline__ void split8(float (&x)[8], uint4 (&out)[N]) {
         out[n] = make_uint4(take_part(x[0], x[1]), take_part(x[2], x[3]), take_part(x[4], x[5]), take_part(x[6], x[7]));
 }
 
-// 16 bytes of a row from column c on, of n columns (zero past them).  G: bytes
-// that every address and the row's width are a multiple of (16, 8 or an element).
+// 16 bytes at `off` of a bounded region, from column c of a row of n on: zero past
+// the row's columns, and past the region's end.  G: bytes that every row and its
+// width are a multiple of (16, 8 or an element).
 template <int ACT, int G>
-__device__ __forceinline__ uint4 load_piece(const typename Act<ACT>::T *row, int c, int n) {
+__device__ __forceinline__ uint4 load_piece(__amdgpu_buffer_rsrc_t region, uint32_t off, int c, int n) {
     constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
-    uint4 w = make_uint4(0, 0, 0, 0);
+    constexpr uint32_t kNowhere = 0x80000000u;
     if constexpr (G == 16) {
-        if (c < n) w = *reinterpret_cast<const uint4 *>(row + c);
+        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(region, c < n ? off : kNowhere, 0, 0));
     } else if constexpr (G == 8) {
-        if (c < n) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(row + c);
-            w.x = x.x;
-            w.y = x.y;
-        }
-        if (c + PER / 2 < n) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(row + c + PER / 2);
-            w.z = x.x;
-            w.w = x.y;
-        }
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(region, c < n ? off : kNowhere, 0, 0);
+        const auto y = __builtin_amdgcn_raw_buffer_load_b64(region, c + PER / 2 < n ? off + 8 : kNowhere, 0, 0);
+        return make_uint4(x[0], x[1], y[0], y[1]);
     } else {
-        uint32_t x[4] = {0, 0, 0, 0};
+        uint32_t w[PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-            if (c + e < n) {
-                if constexpr (EB == 2)
-                    x[e / 2] |= (uint32_t)row[c + e] << (16 * (e & 1));
-                else
-                    x[e] = __float_as_uint(row[c + e]);
-            }
-        w = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int e = 0; e < PER; ++e) {
+            const uint32_t at = c + e < n ? off + e * EB : kNowhere;
+            if constexpr (EB == 2)
+                w[e] = __builtin_amdgcn_raw_buffer_load_b16(region, at, 0, 0);
+            else
+                w[e] = __builtin_amdgcn_raw_buffer_load_b32(region, at, 0, 0);
+        }
+        if constexpr (EB == 2)
+            return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        else
+            return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return w;
 }
 
 // A piece into its place in the parts' LDS planes.
@@ -142,10 +138,6 @@ __device__ __forceinline__ void store_piece(uint16_t *at, const uint4 w) {
 __device__ __forceinline__ uint2 read_transposed(const uint16_t *at) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
-}
-
-__device__ __forceinline__ uint4 load_bounded(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
 // x of the lane that a DPP control names, 0 where there is none (rows not in the mask keep 0)
@@ -206,7 +198,7 @@ template <int ACT, int DK, int VT> struct ChunkGeom {
     static constexpr int kBytes = buffers(kDepth);
     static constexpr int kTakers = VT / 16;  // waves that own value columns
     static constexpr int kThreads = 64 * (kTakers + kMakers);
-    static constexpr int kWavesPerSimd = kThreads == 512 && 2 * kBytes <= kLds ? 4 : kThreads / 256;
+    static constexpr int kWavesPerSimd = kThreads / 256;  // registers for one workgroup a CU
     static_assert(kBytes <= kLds, "LDS");
 };
 
@@ -255,6 +247,9 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
 
     if (wave >= M::kTakers) {
         // ---------------------------------------------------------------- makers
+        // ahead of the takers where both can issue: their two steps are the shorter
+        // ones of work but wait on memory (float32, 2.6 -> 2.3 us a chunk)
+        __builtin_amdgcn_s_setprio(1);
         const int mt = tid - 64 * M::kTakers, maker = wave - M::kTakers;
         const T *const q = static_cast<const T *>(a.q) + (b * a.L + begin) * a.ld_q + h * a.s.qh / a.s.H * dk;
         const T *const k = static_cast<const T *>(a.k) + (b * a.L + begin) * a.ld_k + h * a.s.kh / a.s.H * dk;
@@ -266,37 +261,26 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         uint4 rq[NQ], rk[NQ], rv[NV];
         auto fetch = [&](int c) {
             const int64_t t0 = (int64_t)c * C, n = rows - t0;
-            if constexpr (G == 16) {
-                // rows and columns past the end read as zero by the bounds of the buffer
-                const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
-                const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
-                const auto bq = make_region(q + t0 * a.ld_q, n <= 0 ? 0 : last * sq + dk * M::EB);
-                const auto bk = make_region(k + t0 * a.ld_k, n <= 0 ? 0 : last * sk + dk * M::EB);
-                const auto bv = make_region(v + t0 * a.ld_v, n <= 0 ? 0 : last * sv + vcols * M::EB);
-                const uint32_t oc = qc < dk ? qc * M::EB : 0x80000000u, ov = vc < vcols ? vc * M::EB : 0x80000000u;
+            // rows past the last token read as zero by the bounds of the buffer
+            const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
+            const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
+            const auto bq = make_region(q + t0 * a.ld_q, n <= 0 ? 0 : last * sq + dk * M::EB);
+            const auto bk = make_region(k + t0 * a.ld_k, n <= 0 ? 0 : last * sk + dk * M::EB);
+            const auto bv = make_region(v + t0 * a.ld_v, n <= 0 ? 0 : last * sv + vcols * M::EB);
+            // of the thread's first pieces; the others' are formed here each time, not kept
+            uint32_t oq = qc * M::EB + qr * sq, ok = qc * M::EB + qr * sk, ov = vc * M::EB + vr * sv;
+            asm volatile("" : "+v"(oq), "+v"(ok), "+v"(ov));
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    if (FULL) rq[i] = load_bounded(bq, oc + (qr + i * RSTEP) * sq);
-                    rk[i] = load_bounded(bk, oc + (qr + i * RSTEP) * sk);
-                }
+            for (int i = 0; i < NQ; ++i) {
+                if (FULL) rq[i] = load_piece<ACT, G>(bq, oq + i * RSTEP * sq, qc, dk);
+                if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);  // elements are packed as they come
+                rk[i] = load_piece<ACT, G>(bk, ok + i * RSTEP * sk, qc, dk);
+                if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-                for (int i = 0; i < NV; ++i) rv[i] = load_bounded(bv, ov + (vr + i * VSTEP) * sv);
-            } else {
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                    const int r = qr + i * RSTEP;
-                    rq[i] = rk[i] = make_uint4(0, 0, 0, 0);
-                    if (r < n) {
-                        if (FULL) rq[i] = load_piece<ACT, G>(q + (t0 + r) * a.ld_q, qc, dk);
-                        rk[i] = load_piece<ACT, G>(k + (t0 + r) * a.ld_k, qc, dk);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int r = vr + i * VSTEP;
-                    rv[i] = make_uint4(0, 0, 0, 0);
-                    if (r < n) rv[i] = load_piece<ACT, G>(v + (t0 + r) * a.ld_v, vc, vcols);
-                }
+            for (int i = 0; i < NV; ++i) {
+                rv[i] = load_piece<ACT, G>(bv, ov + i * VSTEP * sv, vc, vcols);
+                if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);
             }
         };
         auto store = [&](int c) {
@@ -441,6 +425,13 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         // the state: tile 2P + u, register r = key row 32 P + 8 lg + 4 u + r, value column li of the wave
         const int64_t cells = (int64_t)dk * dv;
         const int col = 16 * wave + li;
+        // of the lane's first cell; rows 16 (t & ~1) + 4 (t & 1) + r further on.  The
+        // compiler is kept from holding the cells' places from the first use to the last
+        auto cell0 = [&](const float *x) {
+            int g = lg;
+            asm volatile("" : "+v"(g));
+            return x + (int64_t)(8 * g) * dv + v0 + col;
+        };
         f32x4 S[2 * PAIRS];
         {
             const float *from = nullptr;
@@ -451,15 +442,21 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                     from = a.state_in + bh * cells;
             }
 #pragma unroll
-            for (int t = 0; t < 2 * PAIRS; ++t)
+            for (int t = 0; t < 2 * PAIRS; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (from && col < vcols) {
+                const float *at = cell0(from);
+                const int left = dk - 8 * lg;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
-                    S[t][r] = from && row < dk && col < vcols ? from[(int64_t)row * dv + v0 + col] : 0.f;
-                }
+                for (int t = 0; t < 2 * PAIRS; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * (t & ~1) + 4 * (t & 1) + r;
+                        if (row < left) S[t][r] = at[row * dv];
+                    }
+            }
         }
         f32x4 acc[TT];
-        uint4 va[KK][NP];
+        uint4 va[KK][NP], vb[KK][3];
         // V of this wave's columns as an operand: value column li, tokens 32 kk + 8 lg + 0..7
         auto load_values = [&](int c) {
             const uint16_t *const Vs = V0 + (TWO ? c & 1 : 0) * NP * M::VP;
@@ -471,6 +468,29 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                     const uint2 lo = read_transposed(at), hi = read_transposed(at + 4 * M::VS);
                     va[kk][w] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
+        };
+        // V weighted to the chunk's end, in parts
+        auto weigh_values = [&](int c) {
+            const float *const te = E0 + (c & 1) * C;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w0 = reinterpret_cast<const uint32_t *>(&va[kk][0])[e];
+                    x[2 * e] = bf16_lo(w0);
+                    x[2 * e + 1] = bf16_hi(w0);
+                    if constexpr (NP == 3) {
+                        const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
+                        const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
+                        x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
+                        x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
+                split8(x, vb[kk]);
+            }
         };
         // acc = y / scale: exp(G_t) S^T q_t, then P V
         auto form_y = [&](int c) {
@@ -551,8 +571,8 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             const int buf = TWO ? c & 1 : 0;
             const uint16_t *const kat = K0 + buf * NP * M::KP + (8 * lg + (li >> 2)) * M::KS + 8 * (li & 3);
             // K transposed, KG tiles of key rows at a time, loaded one time ahead
-            constexpr int KG = NP == 3 || DK == 32 ? 2 : 4, KPK = 2 * PAIRS / KG, KN = KK * KPK;
-            uint4 ka[2][KG][NP], vb[KG][3];
+            constexpr int KG = NP == 3 || DK == 32 || G != 16 ? 2 : 4, KPK = 2 * PAIRS / KG, KN = KK * KPK;
+            uint4 ka[2][KG][NP];
             auto load = [&](int n) {
 #pragma unroll
                 for (int g = 0; g < KG; ++g) {
@@ -567,37 +587,19 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             };
             load(0);
             const float f = factor[c & 1];
-            const float *const te = E0 + (c & 1) * C;
 #pragma unroll
             for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
 #pragma unroll
             for (int n = 0; n < KN; ++n) {
                 const int kk = n / KPK, first = n % KPK * KG;
                 if (n + 1 < KN) load(n + 1);
-                if (first == 0) {
-                    float x[8];
+                uint4 vv[KG][3];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t w0 = reinterpret_cast<const uint32_t *>(&va[kk][0])[e];
-                        x[2 * e] = bf16_lo(w0);
-                        x[2 * e + 1] = bf16_hi(w0);
-                        if constexpr (NP == 3) {
-                            const uint32_t w1 = reinterpret_cast<const uint32_t *>(&va[kk][1])[e];
-                            const uint32_t w2 = reinterpret_cast<const uint32_t *>(&va[kk][2])[e];
-                            x[2 * e] += bf16_lo(w1) + bf16_lo(w2);
-                            x[2 * e + 1] += bf16_hi(w1) + bf16_hi(w2);
-                        }
-                    }
+                for (int g = 0; g < KG; ++g)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= te[32 * kk + 8 * lg + e];
-                    split8(x, vb[0]);
-#pragma unroll
-                    for (int g = 1; g < KG; ++g)
-#pragma unroll
-                        for (int w = 0; w < 3; ++w) vb[g][w] = vb[0][w];
-                }
+                    for (int w = 0; w < 3; ++w) vv[g][w] = vb[kk][w];
                 __builtin_amdgcn_sched_barrier(0);
-                mfma_tiles<KG>(ka[n & 1], vb, S + first);
+                mfma_tiles<KG>(ka[n & 1], vv, S + first);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -608,12 +610,14 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             for (int c = 0; c < chunks; ++c) {
                 if constexpr (FULL) {
                     form_y(c);
+                    weigh_values(c);
                     add_near(c);
                     if constexpr (TWO) __syncthreads();
                     advance(c);
                     store_y(c);
                 } else {
                     load_values(c);
+                    weigh_values(c);
                     advance(c);
                 }
                 __syncthreads();
@@ -625,20 +629,23 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         }
         float *const to = FULL ? a.state_out + bh * cells
                                : reinterpret_cast<float *>(a.ws) + (bh * p.segs + seg + 1) * cells;
-        if (!FULL || seg == p.segs - 1) {
+        if ((!FULL || seg == p.segs - 1) && col < vcols) {
+            float *at = const_cast<float *>(cell0(to));
+            const int left = dk - 8 * lg;
 #pragma unroll
             for (int t = 0; t < 2 * PAIRS; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * (t & ~1) + 8 * lg + 4 * (t & 1) + r;
-                    if (row < dk && col < vcols) to[(int64_t)row * dv + v0 + col] = S[t][r];
+                    const int row = 16 * (t & ~1) + 4 * (t & 1) + r;
+                    if (row < left) at[row * dv] = S[t][r];
                 }
         }
     }
     if (FULL) {  // rows past the tokens
-        const int64_t done = (int64_t)chunks * C, n = end - begin - done;
-        for (int64_t i = tid; i < n * vcols; i += M::kThreads)
-            Act<ACT>::st(y + (done + i / vcols) * a.ld_y + i % vcols, 0.f);
+        const int col = tid % VT;
+        if (col < vcols)
+            for (int64_t t = (int64_t)chunks * C + tid / VT; t < end - begin; t += M::kThreads / VT)
+                Act<ACT>::st(y + t * a.ld_y + col, 0.f);
     }
 }
 
@@ -766,6 +773,8 @@ LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     const int64_t chunks = (L + p.chunk - 1) / p.chunk, groups = s.B * s.H * p.vtiles;
     // Segments cost a second pass over k and v (kAgain of the full pass, measured)
     // and pay by filling the GPU, one workgroup a CU: the least of rounds x chunks.
+    // (Cutting rows of their own lengths finer, for balance, did not pay: six rows of
+    // up to 1501 float32 tokens, 32 heads: 152 us in four segments, 124 us whole.)
     constexpr double kAgain = 0.6;
     constexpr int64_t kCUs = 256, kFew = 4;  // kFew: chunks of a segment, at least
     int64_t segs = 1;
@@ -790,9 +799,7 @@ int linattn_granule(const LinAttnArgs &a) {
     uintptr_t bits = 0;
     for (const void *x : {a.q, a.k, a.v, (const void *)a.y}) bits |= reinterpret_cast<uintptr_t>(x);
     for (int64_t n : {a.ld_q, a.ld_k, a.ld_v, a.ld_y, (int64_t)a.s.dk, (int64_t)a.s.dv}) bits |= (uintptr_t)(n * e);
-    // the 16-byte loads go by 32-bit offsets from a chunk's first row
-    const bool near = a.ld_q < 1 << 22 && a.ld_k < 1 << 22 && a.ld_v < 1 << 22;
-    return bits % 16 == 0 && near ? 16 : bits % 8 == 0 ? 8 : e;
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : e;
 }
 
 template <int ACT, int DK, int VT, int G, bool FULL>
@@ -823,9 +830,13 @@ hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t
 
 template <int ACT, int DK, int G>
 hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t stream) {
-    if constexpr (DK <= (ACT == kBF16 ? 128 : 64))
+    // (element loads take more registers than a workgroup of 128 columns has)
+    if constexpr (DK <= (ACT == kBF16 ? 128 : 64) && G >= 8)
         if (p.vt == 128) return launch_prompt<ACT, DK, 128, G>(a, p, stream);
-    return launch_prompt<ACT, DK, 64, G>(a, p, stream);
+    LinAttnPlan narrow = p;
+    narrow.vt = 64;
+    narrow.vtiles = (a.s.dv + 63) / 64;
+    return launch_prompt<ACT, DK, 64, G>(a, narrow, stream);
 }
 
 template <int ACT, int DK>

@@ -572,6 +572,7 @@ hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L
  *   state_in  [batch][heads][key_dim][value_dim] float32, or NULL for zero.
  *   state_out the state after each row's last token (may equal state_in).
  *   workspace 256-byte aligned scratch, hyena_linattn_prefill_workspace bytes.
+ * ld_q, ld_k, ld_v < 2^22 and L < 2^30 (else HM_ERR_UNSUPPORTED).
  * Sums and the state are float32.  The prompt runs in chunks on the matrix
  * cores: decays inside a chunk are formed from float64 sums of a, float32
  * operands keep about 24 significant bits, and of bfloat16 ones only what the

@@ -82,6 +82,7 @@ def test_linattn_own_arguments():
     _refused(BAD, _prefill, _desc(), L=-1)
     _refused(NO, _prefill, _desc(), L=1 << 40, ld_decay=0)
     _refused(NO, _prefill, _desc(), lengths=FAKE + 2)
+    _refused(NO, _prefill, _desc(), ld_k=1 << 22)
     _refused(BAD, hb.hyena_linattn_prefill_workspace, _desc(), -1)
     _refused(BAD, _token, _desc(), state_in=None)
     _refused(BAD, _token, _desc(), src_rows=FAKE)  # in place
