@@ -55,12 +55,14 @@ class BeamSearch:
         hb._expect("scores", scores, torch.float32, (G, K), self.device)
         if finished is not None:
             hb._expect("finished", finished, torch.uint8, (G, K), self.device)
-        types = (torch.float32, torch.int32, torch.int32, torch.uint8)
         with hb._On(self.device, stream) as stream:
             if out is None:
-                out = tuple(torch.empty((G, n), dtype=t, device=self.device) for t in types)
+                # (three of them from one allocation)
+                s, tokens, parents = torch.empty((3, G, n), dtype=torch.int32, device=self.device).unbind(0)
+                out = (s.view(torch.float32), tokens, parents, torch.empty((G, n), dtype=torch.uint8, device=self.device))
             else:
-                for name, x, t in zip(("scores", "tokens", "parents", "finished"), out, types):
+                for name, x, t in zip(("scores", "tokens", "parents", "finished"), out,
+                                      (torch.float32, torch.int32, torch.int32, torch.uint8)):
                     hb._expect("out " + name, x, t, (G, n), self.device)
             ws = self._ws.get(stream)
             if ws is None:

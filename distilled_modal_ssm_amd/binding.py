@@ -551,6 +551,14 @@ def hyena_beam_reorder(groups, beams, parents, buffers, row_bytes, stream=None) 
 # ----------------------------------------------------------------- tensor helpers
 
 
+def _current_stream(device):
+    """The hipStream_t of torch's current stream on a device (torch's own lookup of the handle costs
+    2 us less than its Stream object, which stays where the lookup is missing)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 class _On:
     """``with _On(device, stream) as s``: makes the device current, with the given
     stream (a hipStream_t, a torch stream) or else its current one as torch's, so
@@ -558,7 +566,7 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        self.device, self.torch, self.guard = device, torch, None
+        self.device, self.guard = device, None
         if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=device)
@@ -569,7 +577,7 @@ class _On:
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return self.torch.cuda.current_stream(self.device).cuda_stream
+        return _current_stream(self.device)
 
     def __exit__(self, *exc):
         return self.guard.__exit__(*exc) if self.guard is not None else None

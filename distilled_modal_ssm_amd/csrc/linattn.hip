@@ -659,10 +659,19 @@ __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinAttnArgs a, L
     const float2 *factor = reinterpret_cast<const float2 *>(a.ws + p.off_decay) + bh * p.segs;
     float x = a.state_in ? a.state_in[bh * cells + i] : 0.f;
     slot[0] = x;
-    for (int64_t s = 1; s < p.segs; ++s) {
-        const float2 f = factor[s - 1];
-        x = fmaf(x, f.x, fmaf(x, f.y, slot[s * cells]));
-        slot[s * cells] = x;
+    constexpr int AHEAD = 8;  // own states read before the first of them is overwritten
+    for (int64_t s = 1; s < p.segs; s += AHEAD) {
+        float own[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (s + j < p.segs) own[j] = slot[(s + j) * cells];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (s + j < p.segs) {
+                const float2 f = factor[s + j - 1];
+                x = fmaf(x, f.x, fmaf(x, f.y, own[j]));
+                slot[(s + j) * cells] = x;
+            }
     }
 }
 

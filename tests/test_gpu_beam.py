@@ -93,6 +93,8 @@ CASES = [
     (1, 16, 40001, 64, "f32", 0.0),
     (40, 4, 511, 8, "bf16", 0.3),
     (1, 2, 160000, 3, "bf16", 0.0),
+    (30, 8, 70003, 16, "bf16", 0.2),
+    (16, 16, 66000, 64, "f32", 0.1),
 ]
 
 
@@ -114,6 +116,40 @@ def test_select(G, K, V, n, act, share):
     got = op.select(x.cuda(), scores.cuda(), None if fin is None else fin.cuda())
     torch.cuda.synchronize()
     _check(got, x, scores, fin, end)
+
+
+@pytest.mark.parametrize("act", ["float32", "bfloat16"])
+@pytest.mark.parametrize("kind", ["rising", "falling", "late ties", "constant", "few"])
+def test_rows_in_many_batches(kind, act):
+    """Rows long and many enough that a workgroup goes through them in batches: better
+    and better ones to the end, ties across batches, nearly all taken out."""
+    torch = require_gpu()
+    G, K, V, n = 32, 8, 70001, 24
+    at = torch.arange(V, device="cuda", dtype=torch.float32)
+    if kind == "rising":
+        x = at / 4096
+    elif kind == "falling":
+        x = -at / 4096
+    elif kind == "late ties":
+        x = torch.where(at >= 40000, 3.0, (at % 5) / 8)
+    elif kind == "constant":
+        x = torch.zeros_like(at)
+    else:
+        x = torch.full_like(at, NEVER)
+        x[[5, 8191, 8192, 8193, 30000, 69999, 70000]] = torch.tensor([1., 2, 2, 2, -4, 0, 3], device="cuda")
+    logits = x.to(getattr(torch, act))[None].repeat(G * K, 1)
+    scores = (torch.arange(K, device="cuda", dtype=torch.float32) / 64).repeat(G, 1).contiguous()
+    log(f"select batches {kind} {act}")
+    got = BeamSearch(G, K, V, select=n).select(logits, scores)
+    torch.cuda.synchronize()
+    for t in got[:3]:  # every group is alike
+        assert bool((t == t[:1]).all())
+    _check([t[:1] for t in got], logits[:K].cpu(), scores[:1], None, None)
+    out, tok, par, _ = (t[0].cpu() for t in got)
+    if kind == "constant":  # the best beam's first tokens
+        assert par.tolist() == [K - 1] * n and tok.tolist() == list(range(n))
+    if kind == "late ties":
+        assert par.tolist() == [K - 1] * n and tok.tolist() == list(range(40000, 40000 + n))
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
