@@ -775,24 +775,31 @@ int padded_dk(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 :
 LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     LinAttnPlan p;
     p.chunk = s.act == kBF16 && s.dk <= 128 ? 64 : 32;
-    // 128 value columns a workgroup where there are more than 64, the LDS holds two
-    // chunks of them and the registers of three waves a SIMD the state
-    p.vt = s.dv > 64 && s.dk <= (s.act == kBF16 ? 128 : 64) ? 128 : 64;
-    p.vtiles = (s.dv + p.vt - 1) / p.vt;
-    const int64_t chunks = (L + p.chunk - 1) / p.chunk, groups = s.B * s.H * p.vtiles;
-    // Segments cost a second pass over k and v (kAgain of the full pass, measured)
-    // and pay by filling the GPU, one workgroup a CU: the least of rounds x chunks.
-    // (Cutting rows of their own lengths finer, for balance, did not pay: six rows of
-    // up to 1501 float32 tokens, 32 heads: 152 us in four segments, 124 us whole.)
-    constexpr double kAgain = 0.6;
+    // Value columns of a workgroup and segments of the prompt: the least of rounds of
+    // workgroups, one a CU, x chunks of one.  64 columns take kNarrow of the time of 128
+    // a chunk (77 tokens of 16 heads: 12.3 us against 14.3), which are for more than 64
+    // where the LDS holds two chunks of them and the registers of three waves a SIMD the
+    // state.  Segments cost a second pass over k and v, kAgain of the full one.  (Cutting
+    // rows of their own lengths finer, for balance, did not pay: six rows of up to 1501
+    // float32 tokens, 32 heads: 152 us in four segments, 124 us whole.)
+    constexpr double kNarrow = 0.75, kAgain = 0.6;
     constexpr int64_t kCUs = 256, kFew = 4;  // kFew: chunks of a segment, at least
+    const int64_t chunks = (L + p.chunk - 1) / p.chunk;
     int64_t segs = 1;
-    double best = (double)((groups + kCUs - 1) / kCUs * chunks);
-    for (int64_t n = 2; n * kFew <= chunks && groups * n < 2 * kCUs; ++n) {
-        const double cost = (double)((groups * n + kCUs - 1) / kCUs * ((chunks + n - 1) / n)) * (1 + kAgain);
-        if (cost < best) {
-            best = cost;
-            segs = n;
+    double best = -1.0;
+    for (int vt : {64, 128}) {
+        if (vt == 128 && (s.dv <= 64 || s.dk > (s.act == kBF16 ? 128 : 64))) continue;
+        const int vtiles = (s.dv + vt - 1) / vt;
+        const int64_t groups = s.B * s.H * vtiles;
+        for (int64_t n = 1; n == 1 || (n * kFew <= chunks && groups * n < 2 * kCUs); ++n) {
+            const double cost = (double)((groups * n + kCUs - 1) / kCUs * ((chunks + n - 1) / n)) *
+                                (n > 1 ? 1 + kAgain : 1) * (vt == 64 ? kNarrow : 1);
+            if (best < 0 || cost < best) {
+                best = cost;
+                segs = n;
+                p.vt = vt;
+                p.vtiles = vtiles;
+            }
         }
     }
     p.seg_chunks = (chunks + segs - 1) / segs;
