@@ -31,6 +31,11 @@ class BeamSearch:
         self.end_token = -1 if end_token is None else int(end_token)
         self.ws_bytes = hb.hyena_beam_select_workspace(self.groups, self.beams, self.vocab, self.n)
         self._ws = {}  # scratch memory of each stream
+        self._select = hb.load().hyena_beam_select
+        # outputs are made like these: scores, tokens and parents in one allocation
+        self._like = (torch.empty((3, self.groups, self.n), dtype=torch.int32, device=self.device),
+                      torch.empty((self.groups, self.n), dtype=torch.uint8, device=self.device))
+        self._logits_shape, self._beams_shape = (self.groups * self.beams, self.vocab), (self.groups, self.beams)
 
     def first_scores(self):
         """Scores of a search's start: one live beam in each group."""
@@ -46,30 +51,33 @@ class BeamSearch:
         scores: float32 [groups][beams]; finished: uint8 [groups][beams] or None.
         out: the four tensors to write, instead of new ones.
         """
-        torch = self.torch
-        G, K, n = self.groups, self.beams, self.n
-        if logits.dtype not in (torch.float32, torch.bfloat16) or logits.device != self.device \
-                or tuple(logits.shape) != (G * K, self.vocab) or (self.vocab > 1 and logits.stride(1) != 1):
-            raise ValueError(f"logits: need float32 or bfloat16 {(G * K, self.vocab)} rows on {self.device}, got "
-                             f"{logits.dtype} {tuple(logits.shape)} on {logits.device}")
-        hb._expect("scores", scores, torch.float32, (G, K), self.device)
+        torch, (rows, V) = self.torch, self._logits_shape
+        dtype = logits.dtype
+        if dtype not in (torch.float32, torch.bfloat16) or logits.shape != self._logits_shape \
+                or logits.device != self.device or (V > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits: need float32 or bfloat16 {self._logits_shape} rows on {self.device}, got {dtype} "
+                             f"{tuple(logits.shape)} on {logits.device}")
+        hb._expect("scores", scores, torch.float32, self._beams_shape, self.device)
         if finished is not None:
-            hb._expect("finished", finished, torch.uint8, (G, K), self.device)
+            hb._expect("finished", finished, torch.uint8, self._beams_shape, self.device)
         with hb._On(self.device, stream) as stream:
             if out is None:
-                # (three of them from one allocation)
-                s, tokens, parents = torch.empty((3, G, n), dtype=torch.int32, device=self.device).unbind(0)
-                out = (s.view(torch.float32), tokens, parents, torch.empty((G, n), dtype=torch.uint8, device=self.device))
+                s, tokens, parents = torch.empty_like(self._like[0]).unbind(0)
+                out = (s.view(torch.float32), tokens, parents, torch.empty_like(self._like[1]))
             else:
                 for name, x, t in zip(("scores", "tokens", "parents", "finished"), out,
                                       (torch.float32, torch.int32, torch.int32, torch.uint8)):
-                    hb._expect("out " + name, x, t, (G, n), self.device)
+                    hb._expect("out " + name, x, t, (self.groups, self.n), self.device)
             ws = self._ws.get(stream)
             if ws is None:
                 ws = self._ws[stream] = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=self.device)
-            hb.hyena_beam_select(G, K, self.vocab, n, hb.HM_BF16 if logits.dtype == torch.bfloat16 else hb.HM_F32,
-                                 logits, logits.stride(0) if G * K > 1 else self.vocab, scores, finished,
-                                 self.end_token, *out, ws, self.ws_bytes, stream)
+            # (straight to the C entry point: a step's call counts in microseconds)
+            hb._check(self._select(self.groups, self.beams, V, self.n,
+                                   hb.HM_BF16 if dtype == torch.bfloat16 else hb.HM_F32, logits.data_ptr(),
+                                   logits.stride(0) if rows > 1 else V, scores.data_ptr(),
+                                   None if finished is None else finished.data_ptr(), self.end_token,
+                                   out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                                   ws.data_ptr(), self.ws_bytes, stream), "hyena_beam_select")
         return out
 
     def rows(self, parents):

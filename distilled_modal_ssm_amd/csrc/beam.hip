@@ -9,6 +9,15 @@
 // sum of exponentials (one pass over the logits); a second kernel, one workgroup
 // a group, joins the segments' statistics and takes the best of what they
 // handed on.  Both find their best through the same block_best below.
+//
+// What bounds it (MI355X): a segment's fixed steps (the lane sort, the listing, the
+// ranks) and its exponentials, some 24 vector instructions a logit, of which 7 are
+// the softmax's; 32 x 8 rows of 131072 float32 logits take 42 us of segments (3.2
+// TB/s) and 12 us of picks.  Segments of 2048 logits took 110 us in all, of 4096 83,
+// of 8192 59, of 16384 58.  Small calls: two launches and the calling program.
+//
+// The reorder is bound by memory (64 beams over 24 layers: 1.49 GB in 320 us, 4.7
+// TB/s); each thread moves one piece of every row of its group.
 #include "hm_internal.hpp"
 
 namespace hm {
@@ -373,7 +382,7 @@ struct ReorderArgs {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kMoves = 4;  // pieces of a row that a thread moves, one after the other
+constexpr int kMoves = 4;  // pieces of a row that a thread moves, one after the other (1: 489 us for 312, 2: 323, 8: 311)
 
 // One workgroup for a group, a buffer and kMoves * 256 pieces of its rows.  A
 // thread moves its piece in every row of the group, all reads before the first

@@ -9,6 +9,8 @@ same two modes, a prompt with its end state and one step a token.
 
 from __future__ import annotations
 
+import ctypes
+
 from . import binding as hb
 
 
@@ -36,6 +38,9 @@ class LinearAttention:
         hb.hyena_linattn_prefill_workspace(self.desc, 0)  # raises for sizes that the library refuses
         self._ws = {}  # scratch memory of each stream
         self._state_shape = (self.B, self.H, self.dk, self.dv)
+        self._token_shapes = ((self.B, self.q_heads * self.dk), (self.B, self.k_heads * self.dk),
+                              (self.B, self.v_heads * self.dv), (self.B, self.H * self.dv))
+        self._token, self._desc_ref = hb.load().hyena_linattn_decode_step, ctypes.byref(self.desc)
 
     def new_state(self):
         return self.torch.zeros((self.B, self.H, self.dk, self.dv), dtype=self.torch.float32, device=self.device)
@@ -49,17 +54,16 @@ class LinearAttention:
             ws = self._ws[stream] = self.torch.empty(n, dtype=self.torch.uint8, device=self.device)
         return ws, n
 
-    def _rows(self, name, t, lead, width, dtype=None):
-        """Row stride of rows [*lead][width] whose row (b, t) lies at (b * L + t) * stride."""
-        shape = (*lead, width)
-        if t.dtype != (dtype or self.tdtype) or t.device != self.device or t.shape != shape:
-            raise ValueError(f"{name}: need {dtype or self.tdtype} {shape} on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
+    def _rows(self, name, t, shape, dtype):
+        """Row stride of rows [..][width] of this shape, row (b, t) at (b * L + t) * stride."""
+        if t.dtype != dtype or t.shape != shape or t.device != self.device:
+            raise ValueError(f"{name}: need {dtype} {shape} on {self.device}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
         if t.is_contiguous():
-            return width
-        if len(lead) == 2:
+            return shape[-1]
+        if len(shape) == 3:
             return hb._row_stride(t, ())
-        if width > 1 and t.stride(1) != 1:
+        if shape[1] > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: rows need unit element stride")
         return t.stride(0)
 
@@ -70,7 +74,7 @@ class LinearAttention:
         if a.dim() == 1:
             hb._expect("log_decay", a, self.torch.float32, (self.H,), self.device)
             return 0
-        return self._rows("log_decay", a, lead, self.H, self.torch.float32)
+        return self._rows("log_decay", a, (*lead, self.H), self.torch.float32)
 
     def _state(self, name, s):
         hb._expect(name, s, self.torch.float32, self._state_shape, self.device)
@@ -84,10 +88,10 @@ class LinearAttention:
         (later ones are not read, their y is 0).  state_out may be state_in.
         """
         L = int(q.shape[1]) if q.dim() == 3 else -1
-        lead = (self.B, L)
-        ld_q = self._rows("q", q, lead, self.q_heads * self.dk)
-        ld_k = self._rows("k", k, lead, self.k_heads * self.dk)
-        ld_v = self._rows("v", v, lead, self.v_heads * self.dv)
+        lead, dt = (self.B, L), self.tdtype
+        ld_q = self._rows("q", q, (*lead, self.q_heads * self.dk), dt)
+        ld_k = self._rows("k", k, (*lead, self.k_heads * self.dk), dt)
+        ld_v = self._rows("v", v, (*lead, self.v_heads * self.dv), dt)
         ld_a = self._decay(log_decay, lead)
         if lengths is not None:
             hb._expect("lengths", lengths, self.torch.int32, (self.B,), self.device)
@@ -95,15 +99,15 @@ class LinearAttention:
             self._state("state_in", state_in)
         with hb._On(self.device, stream) as stream:
             if y is None:
-                y = self.torch.empty((self.B, L, self.H * self.dv), dtype=self.tdtype, device=self.device)
+                y = self.torch.empty((*lead, self.H * self.dv), dtype=dt, device=self.device)
             if state_out is None:
-                state_out = self.torch.empty((self.B, self.H, self.dk, self.dv), dtype=self.torch.float32,
-                                             device=self.device)
+                state_out = self.torch.empty(self._state_shape, dtype=self.torch.float32, device=self.device)
             else:
                 self._state("state_out", state_out)
             ws, n = self._workspace(L, stream)
             hb.hyena_linattn_prefill(self.desc, L, lengths, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
-                                     self._rows("y", y, lead, self.H * self.dv), state_in, state_out, ws, n, stream)
+                                     self._rows("y", y, (*lead, self.H * self.dv), dt), state_in, state_out, ws, n,
+                                     stream)
         return y, state_out
 
     def decode_step(self, q, k, v, state, log_decay=None, y=None, rows=None, state_out=None, stream=None):
@@ -114,22 +118,27 @@ class LinearAttention:
         to ``state_out``; with ``rows`` (int32 [B]) batch row b continues row
         rows[b] of ``state``, and ``state_out`` must be another tensor.
         """
-        lead = (self.B,)
-        ld_q = self._rows("q", q, lead, self.q_heads * self.dk)
-        ld_k = self._rows("k", k, lead, self.k_heads * self.dk)
-        ld_v = self._rows("v", v, lead, self.v_heads * self.dv)
-        ld_a = self._decay(log_decay, lead)
+        dt = self.tdtype
+        ld_q = self._rows("q", q, self._token_shapes[0], dt)
+        ld_k = self._rows("k", k, self._token_shapes[1], dt)
+        ld_v = self._rows("v", v, self._token_shapes[2], dt)
+        ld_a = self._decay(log_decay, (self.B,))
         self._state("state", state)
-        if state_out is not None:
-            self._state("state_out", state_out)
         if rows is not None:
             hb._expect("rows", rows, self.torch.int32, (self.B,), self.device)
             if state_out is None:
                 raise ValueError("rows need a state_out beside the state")
+        if state_out is None:
+            state_out = state
+        else:
+            self._state("state_out", state_out)
         with hb._On(self.device, stream) as stream:
             if y is None:
-                y = self.torch.empty((self.B, self.H * self.dv), dtype=self.tdtype, device=self.device)
-            hb.hyena_linattn_decode_step(self.desc, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
-                                         self._rows("y", y, lead, self.H * self.dv), state, rows,
-                                         state if state_out is None else state_out, stream)
+                y = self.torch.empty(self._token_shapes[3], dtype=dt, device=self.device)
+            # (straight to the C entry point: a token's call counts in microseconds)
+            hb._check(self._token(self._desc_ref, q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v,
+                                  None if log_decay is None else log_decay.data_ptr(), ld_a, y.data_ptr(),
+                                  self._rows("y", y, self._token_shapes[3], dt), state.data_ptr(),
+                                  None if rows is None else rows.data_ptr(), state_out.data_ptr(), stream),
+                      "hyena_linattn_decode_step")
         return y
