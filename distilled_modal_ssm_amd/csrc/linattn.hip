@@ -688,6 +688,105 @@ __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinAttnArgs a, L
     }
 }
 
+// ------------------------------------------------------------------ a few tokens
+
+// Tokens of a prompt that the chunks are too long for.  (40 x 16 heads of 128 x 128:
+// 12 float32 tokens 28 us, 54 in chunks; 16 bfloat16 ones 62, 40 in chunks.)
+constexpr int short_prompt_tokens(int act) { return act == kF32 ? 16 : 8; }
+
+// LDS of linattn_short_kernel: a token's q, k, decay, values, and y of four waves
+constexpr int short_bytes(int tokens, int dk, int tile) {
+    return tokens * (8 * dk + 4 + 4 * tile + 4 * tile * (kThreads / kWave));
+}
+
+// A prompt of at most so many tokens, all float32: the layout of one token's kernel
+// (LANES threads of V value columns a key row), the state read once, taken through
+// the tokens in registers and written once.  Bound by the state's way out, and past
+// some 8 tokens by the vector ALUs.  (37 x 4 heads of 256 x 256, 3 float32 tokens:
+// 12.7 us, 50.8 in chunks; 44 x 24 of 16 x 16, 8 bfloat16 ones: 14.3, 17.7 in chunks.)
+template <int ACT, int LANES, int V>
+__global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, int vtiles) {
+    using T = typename Act<ACT>::T;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    constexpr int ROWS = kThreads / LANES, TILE = LANES * V, FLY = LANES == 8 ? 8 : 16;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int64_t unit = blockIdx.x / vtiles, b = unit / a.s.H, h = unit - b * a.s.H;
+    const int tid = threadIdx.x, lane = tid % LANES, row0 = tid / LANES, dk = a.s.dk, dv = a.s.dv;
+    const int L = (int)a.L, col0 = (int)(blockIdx.x - unit * vtiles) * TILE, col = col0 + lane * V;
+    int len = L;
+    if (a.lengths) len = a.lengths[b] < 0 ? 0 : a.lengths[b] < L ? a.lengths[b] : L;
+    vec *const part = reinterpret_cast<vec *>(smem);                    // [waves][L][LANES]
+    float *const vs = reinterpret_cast<float *>(part + kThreads / kWave * L * LANES);  // [L][TILE]
+    float2 *const qk = reinterpret_cast<float2 *>(vs + L * TILE);       // [L][dk]: q scale, k
+    float *const g = reinterpret_cast<float *>(qk + L * dk);            // [L]
+    const T *const q = static_cast<const T *>(a.q) + b * L * a.ld_q + h * a.s.qh / a.s.H * dk;
+    const T *const k = static_cast<const T *>(a.k) + b * L * a.ld_k + h * a.s.kh / a.s.H * dk;
+    const T *const v = static_cast<const T *>(a.v) + b * L * a.ld_v + h * a.s.vh / a.s.H * dv + col0;
+    for (int i = tid; i < len * dk; i += kThreads) {
+        const int t = i / dk, c = i - t * dk;
+        qk[i] = make_float2(a.s.scale * Act<ACT>::ld(q + t * a.ld_q + c), Act<ACT>::ld(k + t * a.ld_k + c));
+    }
+    for (int i = tid; i < len * TILE; i += kThreads) {
+        const int t = i / TILE, c = i % TILE;
+        vs[i] = col0 + c < dv ? Act<ACT>::ld(v + t * a.ld_v + c) : 0.f;
+    }
+    if (tid < len)
+        g[tid] = a.decay ? expf(bound_decay(a.decay[a.ld_decay ? (b * L + tid) * a.ld_decay + h : h])) : 1.f;
+    __syncthreads();
+    const int64_t base = unit * (int64_t)dk * dv + col;
+    const bool own = col < dv;  // V divides dv
+    const int wave = tid / kWave;
+    for (int n0 = 0; n0 * ROWS < dk; n0 += FLY) {
+        vec s[FLY];
+#pragma unroll
+        for (int n = 0; n < FLY; ++n) {
+            const int i = row0 + (n0 + n) * ROWS;
+            s[n] = vec{};
+            if (a.state_in && own && i < dk) s[n] = *reinterpret_cast<const vec *>(a.state_in + base + (int64_t)i * dv);
+        }
+        for (int t = 0; t < len; ++t) {
+            const vec x = reinterpret_cast<const vec *>(vs + t * TILE)[lane];
+            const float f = g[t];
+            vec y = {};
+#pragma unroll
+            for (int n = 0; n < FLY; ++n) {
+                const int i = row0 + (n0 + n) * ROWS;
+                if (i < dk) {
+                    const float2 w = qk[t * dk + i];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        s[n][e] = fmaf(f, s[n][e], w.y * x[e]);
+                        y[e] = fmaf(w.x, s[n][e], y[e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int m = LANES; m < kWave; m <<= 1)
+#pragma unroll
+                for (int e = 0; e < V; ++e) y[e] += __shfl_xor(y[e], m);
+            if ((tid & (kWave - 1)) < LANES) {
+                vec *const at = part + (wave * L + t) * LANES + lane;
+                *at = n0 == 0 ? y : *at + y;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < FLY; ++n) {
+            const int i = row0 + (n0 + n) * ROWS;
+            if (own && i < dk) *reinterpret_cast<vec *>(a.state_out + base + (int64_t)i * dv) = s[n];
+        }
+    }
+    __syncthreads();
+    T *const y = static_cast<T *>(a.y) + b * L * a.ld_y + h * dv + col0;
+    const float *const sums = reinterpret_cast<const float *>(part);
+    for (int i = tid; i < L * TILE; i += kThreads) {
+        const int t = i / TILE, c = i % TILE;
+        if (col0 + c >= dv) continue;
+        float o = 0.f;
+        if (t < len) o = (sums[i] + sums[L * TILE + i]) + (sums[2 * L * TILE + i] + sums[3 * L * TILE + i]);
+        Act<ACT>::st(y + t * a.ld_y + c, o);
+    }
+}
+
 // ------------------------------------------------------------------ one token
 
 // One workgroup for a batch row, a head and a tile of LANES * V value columns:
@@ -766,20 +865,36 @@ __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, 
     }
 }
 
+// One token (short_prompt false) or a short prompt.
 template <int ACT, int LANES, int V>
-hipError_t launch_token(const LinAttnArgs &a, hipStream_t stream) {
+hipError_t launch_token(const LinAttnArgs &a, bool short_prompt, hipStream_t stream) {
     const int vtiles = (a.s.dv + LANES * V - 1) / (LANES * V);
-    linattn_token_kernel<ACT, LANES, V><<<dim3((unsigned)(a.s.B * a.s.H * vtiles)), kThreads, 0, stream>>>(a, vtiles);
+    const dim3 grid((unsigned)(a.s.B * a.s.H * vtiles));
+    if (!short_prompt) {
+        linattn_token_kernel<ACT, LANES, V><<<grid, kThreads, 0, stream>>>(a, vtiles);
+        return hipGetLastError();
+    }
+    const int bytes = short_bytes((int)a.L, a.s.dk, LANES * V);
+    const auto kernel = linattn_short_kernel<ACT, LANES, V>;
+    if (bytes > 65536) {
+        const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                   hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (err != hipSuccess) return err;
+    }
+    kernel<<<grid, kThreads, bytes, stream>>>(a, vtiles);
     return hipGetLastError();
 }
 
+// 16-byte pieces of the state where its rows allow them.  128 value columns a
+// workgroup where that gives two a CU, else 32 (batch 1, 16 heads of 128 x 128:
+// 4.6 us, 11.5 with whole heads).
 template <int ACT>
-hipError_t launch_token(const LinAttnArgs &a, hipStream_t stream) {
+hipError_t launch_token(const LinAttnArgs &a, bool short_prompt, hipStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.state_in) | reinterpret_cast<uintptr_t>(a.state_out);
-    if (bits % 16 != 0 || a.s.dv % 4 != 0) return launch_token<ACT, 64, 1>(a, stream);
+    if (bits % 16 != 0 || a.s.dv % 4 != 0) return launch_token<ACT, 64, 1>(a, short_prompt, stream);
     const int64_t units = a.s.B * a.s.H;
-    if (units * ((a.s.dv + 127) / 128) >= 512) return launch_token<ACT, 32, 4>(a, stream);
-    return launch_token<ACT, 8, 4>(a, stream);
+    if (units * ((a.s.dv + 127) / 128) >= 512) return launch_token<ACT, 32, 4>(a, short_prompt, stream);
+    return launch_token<ACT, 8, 4>(a, short_prompt, stream);
 }
 
 // Padded key width, and the granule of 16, 8 bytes or an element that all rows allow.
@@ -789,12 +904,15 @@ LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     LinAttnPlan p;
     p.chunk = s.act == kBF16 && s.dk <= 128 ? 64 : 32;
     // Value columns of a workgroup and segments of the prompt: the least of rounds of
-    // workgroups, one a CU, x chunks of one.  64 columns take kNarrow of the time of 128
-    // a chunk (77 tokens of 16 heads: 12.3 us against 14.3), which are for more than 64
-    // where the LDS holds two chunks of them and the registers of three waves a SIMD the
-    // state.  Segments cost a second pass over k and v, kAgain of the full one.  (Cutting
-    // rows of their own lengths finer, for balance, did not pay: six rows of up to 1501
-    // float32 tokens, 32 heads: 152 us in four segments, 124 us whole.)
+    // workgroups x chunks of one.
+    //   One workgroup a CU; two of 64 columns and up to 32 bfloat16 keys, which leave room
+    //     (8 rows of 2000 tokens, 16 heads of 32 x 32: 49 us against 62).
+    //   64 columns take kNarrow of the time of 128 a chunk (77 tokens of 16 heads: 12.3 us
+    //     against 14.3).  128 are for more than 64 where the LDS holds two chunks of them
+    //     and the registers of three waves a SIMD the state.
+    //   Segments cost a second pass over k and v, kAgain of the full one.  (Cutting rows of
+    //     their own lengths finer, for balance, did not pay: six rows of up to 1501 float32
+    //     tokens, 32 heads: 152 us in four segments, 124 us whole.)
     constexpr double kNarrow = 0.75, kAgain = 0.6;
     constexpr int64_t kCUs = 256, kFew = 4;  // kFew: chunks of a segment, at least
     const int64_t chunks = (L + p.chunk - 1) / p.chunk;
@@ -803,9 +921,9 @@ LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     for (int vt : {64, 128}) {
         if (vt == 128 && (s.dv <= 64 || s.dk > (s.act == kBF16 ? 128 : 64))) continue;
         const int vtiles = (s.dv + vt - 1) / vt;
-        const int64_t groups = s.B * s.H * vtiles;
-        for (int64_t n = 1; n == 1 || (n * kFew <= chunks && groups * n < 2 * kCUs); ++n) {
-            const double cost = (double)((groups * n + kCUs - 1) / kCUs * ((chunks + n - 1) / n)) *
+        const int64_t groups = s.B * s.H * vtiles, kSlots = vt == 64 && s.dk <= 32 && s.act == kBF16 ? 2 * kCUs : kCUs;
+        for (int64_t n = 1; n == 1 || (n * kFew <= chunks && groups * n < 2 * kSlots); ++n) {
+            const double cost = (double)((groups * n + kSlots - 1) / kSlots * ((chunks + n - 1) / n)) *
                                 (n > 1 ? 1 + kAgain : 1) * (vt == 64 ? kNarrow : 1);
             if (best < 0 || cost < best) {
                 best = cost;
@@ -892,12 +1010,14 @@ hipError_t launch_prompt(const LinAttnArgs &a, const LinAttnPlan &p, hipStream_t
 size_t linattn_workspace(const LinAttnShape &s, int64_t L) { return linattn_plan(s, L).bytes; }
 
 hipError_t launch_linattn_prefill(const LinAttnArgs &a, hipStream_t stream) {
+    if (a.L > 0 && a.L <= short_prompt_tokens(a.s.act))
+        return a.s.act == kBF16 ? launch_token<kBF16>(a, true, stream) : launch_token<kF32>(a, true, stream);
     const LinAttnPlan p = linattn_plan(a.s, a.L);
     return a.s.act == kBF16 ? launch_prompt<kBF16>(a, p, stream) : launch_prompt<kF32>(a, p, stream);
 }
 
 hipError_t launch_linattn_decode(const LinAttnArgs &a, hipStream_t stream) {
-    return a.s.act == kBF16 ? launch_token<kBF16>(a, stream) : launch_token<kF32>(a, stream);
+    return a.s.act == kBF16 ? launch_token<kBF16>(a, false, stream) : launch_token<kF32>(a, false, stream);
 }
 
 }  // namespace hm

@@ -368,3 +368,33 @@ def test_refusals():
             LinearAttention(**{**dict(batch=2, heads=4, key_dim=32, value_dim=16, act="f32"), **bad})
     with pytest.raises(ValueError):
         LinearAttention(1, 1, 8, 8, "f16")
+
+
+SHORT = [
+    dict(B=3, L=2, H=2, dk=256, dv=256, resume=True),
+    dict(B=2, L=16, H=3, dk=128, dv=96, lengths=[16, 5]),
+    dict(B=2, L=17, H=3, dk=128, dv=96, lengths=[17, 5]),
+    dict(B=2, L=9, H=2, dk=64, dv=64),
+    dict(B=4, L=9, H=2, dk=200, dv=33, pad=1, lengths=[0, 9, 12, -1], resume=True),
+    dict(B=70, L=8, H=8, dk=16, dv=16),
+    dict(B=80, L=16, H=8, dk=64, dv=128, kh=2, vh=2, qh=8, resume=True),
+    dict(B=2, L=15, H=2, dk=256, dv=130, special="reset", resume=True),
+    dict(B=1, L=3, H=1, dk=5, dv=3, decay="none"),
+]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kw", SHORT, ids=lambda d: "-".join(f"{k}{v}" for k, v in d.items()).replace(" ", ""))
+def test_short_prompt(kw, act):
+    """Prompts that the state goes through in registers, and the first that goes in chunks."""
+    torch = require_gpu()
+    p = Problem(torch, act=act, **kw)
+    log(f"linattn short {act} {kw}")
+    y, S = _prefill(p)
+    torch.cuda.synchronize()
+    p.check(y, S)
+    if p.state is not None:  # the state in place
+        S = p.state.clone()
+        y, _ = p.op.prefill(p.q, p.k, p.v, p.a, lengths=p.lengths, state_in=S, state_out=S)
+        torch.cuda.synchronize()
+        p.check(y, S)
