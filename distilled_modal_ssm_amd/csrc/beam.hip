@@ -80,15 +80,6 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x + across<32>(x);
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-    x = fmaxf(x, across<1>(x));
-    x = fmaxf(x, across<2>(x));
-    x = fmaxf(x, across<4>(x));
-    x = fmaxf(x, across<8>(x));
-    x = fmaxf(x, across<16>(x));
-    return fmaxf(x, across<32>(x));
-}
-
 // exp(d) for d <= 0, to 2^-22 of it and the rounding of d's product
 __device__ __forceinline__ float exp_below(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504f); }
 
@@ -281,7 +272,7 @@ __global__ __launch_bounds__(kThreads) void beam_pick_kernel(BeamSelectArgs a, S
     __shared__ float score0[kMaxSelect], top[kMaxSelect], lse[kMaxSelect];  // lse: log of the sum, after the maximum
     __shared__ bool ended[kMaxSelect];
     const int64_t g = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 63, K = (int)a.beams, n = (int)a.select, V = (int)a.vocab;
+    const int tid = threadIdx.x, K = (int)a.beams, n = (int)a.select, V = (int)a.vocab;
     const unsigned lists = (unsigned)(K * p.segs), total = lists * n;
     const float2 *stat = reinterpret_cast<const float2 *>(a.ws + p.off_stat) + g * lists;
     const Best *cand = reinterpret_cast<const Best *>(a.ws + p.off_best) + g * total;
@@ -294,23 +285,30 @@ __global__ __launch_bounds__(kThreads) void beam_pick_kernel(BeamSelectArgs a, S
         }
     };
     fetch(0);
-    for (int k = tid >> 6; k < K; k += kWaves) {
+    // four lanes a beam, each over every fourth segment, all beams at once
+    if (const int k = tid >> 2; k < K) {
         const float s = a.scores[g * K + k];
         const bool f = a.finished && a.finished[g * K + k];
         float m = kNever, sum = 0.f;
-        if (!f && s > kNever) {
-            for (int i = lane; i < p.segs; i += 64) m = fmaxf(m, stat[k * p.segs + i].x);
-            m = wave_max(m);
-            for (int i = lane; i < p.segs; i += 64) {
+        if (!f && s > kNever)
+            for (int i = tid & 3; i < p.segs; i += 4) {
                 const float2 st = stat[k * p.segs + i];
-                if (st.x > kNever) sum += st.x == m ? st.y : st.y * exp_below(st.x - m);
+                if (st.x > m) {
+                    sum = sum * exp_below(m - st.x) + st.y;
+                    m = st.x;
+                } else if (st.x > kNever) {
+                    sum += st.x == m ? st.y : st.y * exp_below(st.x - m);
+                }
             }
-            sum = wave_sum(sum);
-        }
-        if (lane == 0) {
+        float all = fmaxf(m, across<1>(m));
+        all = fmaxf(all, across<2>(all));
+        if (m != all) sum = m > kNever ? sum * exp_below(m - all) : 0.f;
+        sum += across<1>(sum);
+        sum += across<2>(sum);
+        if ((tid & 3) == 0) {
             score0[k] = s;
             ended[k] = f;
-            top[k] = m;
+            top[k] = all;
             lse[k] = logf(sum);
         }
     }
