@@ -377,8 +377,9 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                 float o[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float d = (float)(gt - gs[s + r]);
-                    o[r] = x[n][r] * __builtin_amdgcn_exp2f(s + r <= t ? d : -__builtin_inff());
+                    // chosen after the product: a later token's may have overflowed
+                    const float w = x[n][r] * __builtin_amdgcn_exp2f((float)(gt - gs[s + r]));
+                    o[r] = s + r <= t ? w : 0.f;
                 }
 #pragma unroll
                 for (int w = 0; w < NP; ++w) {
@@ -561,13 +562,14 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         };
         auto store_y = [&](int c) {
             const int64_t t0 = (int64_t)c * C, n = end - begin - t0;
+            const int own = rows - t0 < C ? (int)(rows - t0) : C;  // tokens; rows past them are zero whatever the state
             const int vc = 16 * wave + 4 * lg;
             T *at = y + (t0 + li) * a.ld_y + vc;
             const bool whole = n >= C;
 #pragma unroll
             for (int j = 0; j < TT; ++j, at += 16 * a.ld_y) {
                 if (vc >= vcols || !(whole || 16 * j + li < n)) continue;
-                const f32x4 o = acc[j] * a.s.scale;
+                const f32x4 o = 16 * j + li < own ? acc[j] * a.s.scale : f32x4{0.f, 0.f, 0.f, 0.f};
                 if constexpr (G == 16 || (G == 8 && ACT == kBF16)) {
                     if constexpr (ACT == kBF16)
                         *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));

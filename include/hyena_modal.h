@@ -576,7 +576,10 @@ hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L
  * Sums and the state are float32.  The prompt runs in chunks on the matrix
  * cores: decays inside a chunk are formed from float64 sums of a, float32
  * operands keep about 24 significant bits, and of bfloat16 ones only what the
- * chunk rounds on its way to y (never to the state) has fewer.
+ * chunk rounds on its way to y (never to the state) has fewer.  A token or a
+ * state that is not finite makes the y after it, in its row and heads, not
+ * finite (NaN where the recurrence may have an infinity), and a token may make
+ * those of up to 63 tokens before it so; never other rows.
  */
 hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const int32_t *lengths,
                                 const void *q, int64_t ld_q, const void *k, int64_t ld_k,

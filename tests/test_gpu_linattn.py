@@ -398,3 +398,49 @@ def test_short_prompt(kw, act):
         y, _ = p.op.prefill(p.q, p.k, p.v, p.a, lengths=p.lengths, state_in=S, state_out=S)
         torch.cuda.synchronize()
         p.check(y, S)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [7, 40, 100])
+def test_later_tokens_that_would_overflow(act, L):
+    """q of the first tokens times k of the later ones passes float32; neither is paired in the sum."""
+    torch = require_gpu()
+    B, H, dk, dv = 2, 3, 64, 48
+    op = LinearAttention(B, H, dk, dv, act)
+    g = torch.Generator().manual_seed(L)
+    q, k, v = (torch.randn(B, L, H, d, generator=g) for d in (dk, dk, dv))
+    first = L // 3
+    q[:, :first] *= 1e22
+    q[:, first:] *= 1e-22
+    k[:, first:] *= 1e22
+    q, k, v = (x.reshape(B, L, -1).to(op.tdtype).cuda() for x in (q, k, v))
+    a = -torch.rand(B, L, H, generator=g).cuda()
+    log(f"linattn later overflow {act} L={L}")
+    y, S = op.prefill(q, k, v, a)
+    torch.cuda.synchronize()
+    q64, k64, v64 = (_heads64(x, H, H, d) for x, d in ((q, dk), (k, dk), (v, dv)))
+    a64, zero = a.cpu().double().numpy(), np.zeros((B, H, dk, dv))
+    ry, rS = _recurrence(q64, k64, v64, a64, zero, [L] * B)
+    my, mS = _recurrence(abs(q64), abs(k64), abs(v64), a64, zero, [L] * B)
+    ry, my = ry * op.scale, my * op.scale
+    tol = (dk + 128 + 8 * L / 64 + 16) * 2.0 ** -24
+    ty = tol * my + (2.0 ** -8 * (abs(ry) + 2 * my) if act == "bf16" else 0.0)
+    assert (abs(y.cpu().double().numpy().reshape(ry.shape) - ry) <= ty).all()
+    assert (abs(S.cpu().double().numpy() - rS) <= tol * mS).all()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [7, 40, 200])
+def test_rows_past_the_tokens_are_zero_whatever_the_state(act, L):
+    torch = require_gpu()
+    B, H, dk, dv = 2, 2, 64, 40
+    op = LinearAttention(B, H, dk, dv, act)
+    q, k, v = (torch.ones(B, L, H * d, device="cuda", dtype=op.tdtype) for d in (dk, dk, dv))
+    state = torch.full((B, H, dk, dv), float("inf"), device="cuda")
+    n = torch.tensor([L - 4, 0], dtype=torch.int32, device="cuda")
+    log(f"linattn zero rows {act} L={L}")
+    y, S = op.prefill(q, k, v, None, lengths=n, state_in=state)
+    torch.cuda.synchronize()
+    assert not y[0, : L - 4].isfinite().any()
+    assert (y[0, L - 4:] == 0).all() and (y[1] == 0).all()
+    assert (S == float("inf")).all()
