@@ -483,8 +483,8 @@ hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *par
                     ++a.n;
                 }
             }
-            // (a buffer has at most 2^26 workgroups)
-            if (a.n == kBuffers || a.first[a.n] >= 1 << 29 || (i == n && a.n > 0)) {
+            // (a launch has fewer than 2^24 workgroups, a buffer at most 2^23)
+            if (a.n == kBuffers || a.first[a.n] >= 1 << 23 || (i == n && a.n > 0)) {
                 switch (size) {
                     case 16: launch_reorder<u32x4, 16>(a, groups, stream); break;
                     case 8: launch_reorder<u32x2, 32>(a, groups, stream); break;

@@ -831,6 +831,10 @@ static hm_status linattn_args(const hm_linattn_desc *d, int64_t L, const void *q
     return HM_OK;
 }
 
+// Rows and heads of a launch: fewer than 2^32 threads, up to four value tiles of 512
+// each, rounded up to eight.
+constexpr int64_t kMostHeads = (int64_t(1) << 21) - 8;
+
 hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L, size_t *bytes) {
     hm_status st = check_linattn(desc);
     if (st != HM_OK) return st;
@@ -858,7 +862,7 @@ hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const in
         if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
         if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;
     }
-    if (desc->batch * desc->heads > INT32_MAX / 64) return HM_ERR_UNSUPPORTED;  // grid limit
+    if (desc->batch * desc->heads > kMostHeads) return HM_ERR_UNSUPPORTED;
     // a chunk of 64 rows is addressed by 32-bit byte offsets
     for (int64_t ld : {ld_q, ld_k, ld_v})
         if (L > 0 && ld >= int64_t(1) << 22) return HM_ERR_UNSUPPORTED;
@@ -883,16 +887,18 @@ hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, 
         if (state_in == state_out) return HM_ERR_INVALID_ARG;
         if (!aligned(src_rows, 4)) return HM_ERR_UNSUPPORTED;
     }
-    if (desc->batch * desc->heads > INT32_MAX / 64) return HM_ERR_UNSUPPORTED;  // grid limit
+    if (desc->batch * desc->heads > kMostHeads) return HM_ERR_UNSUPPORTED;
     a.src_rows = src_rows;
     return hm::launch_linattn_decode(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
+// A launch has fewer than 2^32 threads: at most 2^23 rows and one segment of 8192
+// logits more for each 8192 (segments are shorter only where they are few).
 static hm_status check_beams(int64_t groups, int64_t beams, int64_t vocab, int64_t select) {
     if (groups < 0 || beams < 1 || vocab < 1 || select < 1 || beams > HM_BEAM_MAX || select > HM_BEAM_MAX)
         return HM_ERR_INVALID_ARG;
-    if (vocab > INT32_MAX / beams || groups > INT32_MAX / 64 / beams) return HM_ERR_UNSUPPORTED;
-    if (groups * beams > (int64_t(1) << 42) / vocab) return HM_ERR_UNSUPPORTED;
+    if (vocab > INT32_MAX / beams || groups >= (int64_t(1) << 23) / beams) return HM_ERR_UNSUPPORTED;
+    if (groups * beams > (int64_t(1) << 36) / vocab) return HM_ERR_UNSUPPORTED;
     if (select > beams * vocab) return HM_ERR_INVALID_ARG;
     return HM_OK;
 }
@@ -919,6 +925,7 @@ hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_
         !aligned(out_tokens, 4) || !aligned(out_parents, 4))
         return HM_ERR_UNSUPPORTED;
     if (groups * beams > kMaxElems / ld) return HM_ERR_INVALID_ARG;
+    if (out_scores == scores && select != beams) return HM_ERR_INVALID_ARG;  // a group's would land on another's
     const size_t need = hm::beam_select_workspace(groups, beams, vocab, select);
     if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;
@@ -954,7 +961,7 @@ hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *paren
     if (!parents) return HM_ERR_INVALID_ARG;
     if (groups > 65535) return HM_ERR_UNSUPPORTED;  // grid limits
     for (int64_t i = 0; i < n; ++i)
-        if (row_bytes[i] > int64_t(1) << 36) return HM_ERR_UNSUPPORTED;
+        if (row_bytes[i] > int64_t(1) << 33) return HM_ERR_UNSUPPORTED;  // 2^23 workgroups of single bytes
     if (!aligned(parents, 4)) return HM_ERR_UNSUPPORTED;
     return hm::launch_beam_reorder(groups, beams, parents, n, buffers, row_bytes,
                                    static_cast<hipStream_t>(stream)) == hipSuccess

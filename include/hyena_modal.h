@@ -572,7 +572,7 @@ hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L
  *   state_in  [batch][heads][key_dim][value_dim] float32, or NULL for zero.
  *   state_out the state after each row's last token (may equal state_in).
  *   workspace 256-byte aligned scratch, hyena_linattn_prefill_workspace bytes.
- * ld_q, ld_k, ld_v < 2^22 and L < 2^30 (else HM_ERR_UNSUPPORTED).
+ * batch * heads < 2^21 - 7, ld_q, ld_k, ld_v < 2^22 and L < 2^30 (else HM_ERR_UNSUPPORTED).
  * Sums and the state are float32.  The prompt runs in chunks on the matrix
  * cores: decays inside a chunk are formed from float64 sums of a, float32
  * operands keep about 24 significant bits, and of bfloat16 ones only what the
@@ -597,6 +597,7 @@ hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const in
  *   state_in, state_out  as in hyena_linattn_prefill.  state_out may equal
  *             state_in only without src_rows (else HM_ERR_INVALID_ARG); they
  *             must not overlap otherwise.
+ * batch * heads < 2^21 - 7 (else HM_ERR_UNSUPPORTED).
  */
 hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, int64_t ld_q,
                                     const void *k, int64_t ld_k, const void *v, int64_t ld_v,
@@ -626,13 +627,14 @@ hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, 
  *   end_token in 0 .. vocab-1, or -1 for none (then finished must be NULL).
  *   out_scores, out_tokens, out_parents (beam in the group), out_finished (the
  *   parent had ended, or the token is end_token): [groups][select] float32,
- *   int32, int32, bytes.  out_finished may be NULL; out_scores may equal scores.
+ *   int32, int32, bytes.  out_finished may be NULL; out_scores may equal scores
+ *   where select = beams (else HM_ERR_INVALID_ARG).
  * Continuations of score -infinity are returned only where fewer than select
  * have another.  Softmax statistics and scores are float32; two continuations
  * whose scores differ by no more than their rounding may come in either order.
  *   1 <= beams, select <= HM_BEAM_MAX, select <= beams * vocab (else
- *   HM_ERR_INVALID_ARG), beams * vocab < 2^31, groups * beams < 2^31 / 64,
- *   groups * beams * vocab <= 2^42 (else HM_ERR_UNSUPPORTED).  ld >= vocab.
+ *   HM_ERR_INVALID_ARG), beams * vocab < 2^31, groups < 2^23 / beams,
+ *   groups * beams * vocab <= 2^36 (else HM_ERR_UNSUPPORTED).  ld >= vocab.
  *   workspace: hyena_beam_select_workspace bytes, 256-byte aligned, scratch.
  */
 hm_status hyena_beam_select_workspace(int64_t groups, int64_t beams, int64_t vocab, int64_t select,
@@ -655,7 +657,7 @@ hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_
  *             deferred u_prev and rho, a linear-attention state, ...).
  * Rows that stay are neither read nor written.  Buffers must not overlap.
  * n < 0, row_bytes[i] < 0, null pointers -> HM_ERR_INVALID_ARG; groups > 65535,
- * row_bytes[i] > 2^36 -> HM_ERR_UNSUPPORTED.
+ * row_bytes[i] > 2^33 -> HM_ERR_UNSUPPORTED.
  */
 hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n,
                              void *const *buffers, const int64_t *row_bytes, void *stream);

@@ -152,3 +152,29 @@ def test_beam_reorder_arguments(args, status):
         hb.hyena_beam_reorder(2, 4, FAKE, [FAKE], [], stream=0)
     assert hb.load().hyena_beam_reorder(2, 4, FAKE, -1, None, None, None) == BAD
     assert hb.load().hyena_beam_reorder(2, 4, FAKE, 1, None, None, None) == BAD
+
+
+def test_linattn_rows_of_a_launch():
+    """Rows and heads that four value tiles of 512 threads each give a launch of 2^32 threads."""
+    d, kw = _desc(batch=1 << 18, value_dim=256), dict(ld_v=2048, ld_y=2048)
+    _refused(NO, _prefill, d, L=3, **kw)
+    _refused(NO, _prefill, d, **kw)
+    _refused(NO, _token, d, **kw)
+
+
+@pytest.mark.parametrize("G,K,V", [(1 << 23, 1, 2), (1 << 21, 4, 2), (1 << 20, 4, 1 << 15), (1 << 17, 64, 2)])
+def test_beam_sizes_of_a_launch(G, K, V):
+    """Segments that a launch has no threads for are refused; half as many rows are not."""
+    _refused(NO, hb.hyena_beam_select_workspace, G, K, V, 1)
+    assert hb.hyena_beam_select_workspace(G // 2, K, V, 1) > 0
+
+
+def test_beam_select_scores_in_place():
+    """Only where every group's new scores take the place of its own."""
+    _refused(BAD, _select, select=3)
+    _refused(BAD, _select, select=8)
+    _refused(WS, _select, workspace=None)
+
+
+def test_beam_reorder_row_limit():
+    _refused(NO, hb.hyena_beam_reorder, 1, 4, FAKE, [FAKE], [(1 << 33) + 1], stream=0)
