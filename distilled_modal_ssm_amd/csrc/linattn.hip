@@ -33,13 +33,13 @@
 //
 // A prompt of too few rows and heads to fill the GPU is cut into segments of
 // chunks: the state-only form of the kernel runs over every segment but the last
-// from a zero state (k and v only), a scan joins the states, and the full form
-// starts every segment from its own.
+// from a zero state (k and v only, the last chunk first), a scan joins the states,
+// and the full form starts every segment from its own.
 //
 // What bounds it (MI355X).  Many rows and heads: the way of q, k, v and y through
 // HBM; taking out any of the products changes nothing (16 rows x 2048 tokens, 16
 // heads of 128, bfloat16: 556 MB in 122-126 us, 4.5 TB/s; a large copy has 5.4).  A
-// prompt in segments reads k and v twice (65536 tokens, 16 heads: 1.6 GB in 362 us).
+// prompt in segments reads k and v twice (65536 tokens, 16 heads: 1.6 GB in 363 us).
 // float32: the matrix cores and the vector ALUs in turn, six products of parts for
 // one.  Few tokens: the two barriers and memory latency of each chunk, some 2.5 us.
 //
@@ -100,13 +100,13 @@ __device__ __forceinline__ void split8(float (&x)[8], uint4 (&out)[N]) {
 
 // 16 bytes at `off` of a bounded region, from column c of a row of n on: zero past
 // the row's columns, and past the region's end.  G: bytes that every row and its
-// width are a multiple of (16, 8 or an element).  Loads are non-temporal: tokens are
-// read once (16 x 2048 tokens, 16 heads: 121.6 us against 126.9).
-template <int ACT, int G>
+// width are a multiple of (16, 8 or an element).  ONCE: non-temporal, for tokens that
+// are read once (16 x 2048 tokens, 16 heads: 121.6 us against 126.9).
+template <int ACT, int G, bool ONCE>
 __device__ __forceinline__ uint4 load_piece(__amdgpu_buffer_rsrc_t region, uint32_t off, int c, int n) {
     constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
     constexpr uint32_t kNowhere = 0x80000000u;
-    constexpr int kStream = 2;  // non-temporal
+    constexpr int kStream = ONCE ? 2 : 0;
     if constexpr (G == 16) {
         return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(region, c < n ? off : kNowhere, 0, kStream));
     } else if constexpr (G == 8) {
@@ -269,11 +269,17 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         const T *const v = static_cast<const T *>(a.v) + (b * a.L + begin) * a.ld_v + h * a.s.vh / a.s.H * dv + v0;
         const float *const decay = a.decay ? a.decay + (a.ld_decay ? (b * a.L + begin) * a.ld_decay : 0) + h : nullptr;
 
+        // The state-only form goes through its segment backwards, values weighted to the
+        // segment's end: the full form starts where it ended, on tokens that may still be
+        // in the Infinity Cache, and the state has no factor (65536 tokens, 16 heads: 363
+        // us, 370 forwards).
+        auto first_token = [&](int c) { return (int64_t)(FULL ? c : chunks - 1 - c) * C; };
+
         // tokens of a chunk, on their way
         const int qr = mt / RP, qc = mt % RP * PER, vr = mt / VR, vc = mt % VR * PER;
         uint4 rq[NQ], rk[NQ], rv[NV];
         auto fetch = [&](int c) {
-            const int64_t t0 = (int64_t)c * C, n = rows - t0;
+            const int64_t t0 = first_token(c), n = !FULL && t0 < 0 ? 0 : rows - t0;
             // rows past the last token read as zero by the bounds of the buffer
             const uint32_t last = n <= 0 ? 0 : (uint32_t)(n < C ? n - 1 : C - 1);
             const uint32_t sq = (uint32_t)a.ld_q * M::EB, sk = (uint32_t)a.ld_k * M::EB, sv = (uint32_t)a.ld_v * M::EB;
@@ -285,14 +291,14 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             asm volatile("" : "+v"(oq), "+v"(ok), "+v"(ov));
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                if (FULL) rq[i] = load_piece<ACT, G>(bq, oq + i * RSTEP * sq, qc, dk);
+                if (FULL) rq[i] = load_piece<ACT, G, FULL>(bq, oq + i * RSTEP * sq, qc, dk);
                 if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);  // elements are packed as they come
-                rk[i] = load_piece<ACT, G>(bk, ok + i * RSTEP * sk, qc, dk);
+                rk[i] = load_piece<ACT, G, FULL>(bk, ok + i * RSTEP * sk, qc, dk);
                 if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                rv[i] = load_piece<ACT, G>(bv, ov + i * VSTEP * sv, vc, vcols);
+                rv[i] = load_piece<ACT, G, FULL>(bv, ov + i * VSTEP * sv, vc, vcols);
                 if constexpr (G < 8) __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -315,16 +321,20 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
         float ra = 0.f;
         double total = 0.0, error = 1.0;
         auto fetch_decay = [&](int c) {
-            const int64_t t = (int64_t)c * C + lane;
+            const int64_t t0 = first_token(c), t = t0 + lane;
             ra = 0.f;
-            if (decay && lane < C && t < rows) ra = bound_decay(decay[t * a.ld_decay]);
+            if (decay && lane < C && (FULL || t0 >= 0) && t < rows) ra = bound_decay(decay[t * a.ld_decay]);
         };
         auto form_decays = [&](int c) {
             constexpr double kLog2e = 1.4426950408889634074;
             const int at = c & 1;
             const double g = scan_sum(ra * kLog2e);
             const double e = read_lane(g, C - 1);
-            total += e;
+            if constexpr (!FULL) {  // to the segment's end
+                if (lane < C) E0[at * C + lane] = __builtin_amdgcn_exp2f((float)(total + (e - g)));
+                total += e;
+                return;
+            }
             if (lane < C) {
                 G0[at * C + lane] = g;
                 F0[at * C + lane] = __builtin_amdgcn_exp2f((float)g);
@@ -601,9 +611,11 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                 }
             };
             load(0);
-            const float f = factor[c & 1];
+            if constexpr (FULL) {
+                const float f = factor[c & 1];
 #pragma unroll
-            for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
+                for (int t = 0; t < 2 * PAIRS; ++t) S[t] *= f;
+            }
 #pragma unroll
             for (int n = 0; n < KN; ++n) {
                 const int kk = n / KPK, first = n % KPK * KG;
