@@ -14,9 +14,12 @@
 //   q, k, v      one part (bfloat16) or three (float32: 24 bits);
 //   weighted V   three parts, for both types: the state keeps float32 precision
 //                over any length;
-//   S, weighted K Q^T  as operands of y only: three parts (float32), one
-//                (bfloat16: each adds a rounding like that of y itself, so y's
-//                error is at most 1.41 of the one its own rounding makes);
+//   S, weighted K Q^T  as operands of y only: three parts (float32), two
+//                (bfloat16: off by at most 2^-16 of a term, so y by 2^-16 of the
+//                sum of its terms' absolute values beside its own rounding of
+//                2^-8; one part: 16 x 2048 tokens, 16 heads of 128: 124 us against
+//                146, but y's error is 1.41 times that of its rounding for terms
+//                of random sign and has no bound where they cancel; three: 165);
 //   products of parts i and j are left out where i + j > 2 (below 2^-24).
 // G is summed in float64 (and in units of log 2, for the exponential's
 // instruction).  The rounding of the state's factor exp(E) is made good in the
@@ -192,7 +195,8 @@ constexpr int kMakers = 4;  // waves that fetch, form decays and weigh K Q^T
 
 template <int ACT, int DK, int VT> struct ChunkGeom {
     static constexpr int C = (ACT == kBF16 && DK <= 128) ? 64 : 32;
-    static constexpr int NP = ACT == kBF16 ? 1 : 3;  // parts of q, k, v, and of what y's products round
+    static constexpr int NP = ACT == kBF16 ? 1 : 3;  // parts of q, k, v
+    static constexpr int NS = ACT == kBF16 ? 2 : 3;  // parts of S and weighted K Q^T, as operands of y
     static constexpr int EB = Act<ACT>::kBytes;
     // LDS rows in elements, by the counted conflicts of each access (cycles beyond
     // the first ones of a wave's instruction): Q, read in rows of 16 bytes, has none
@@ -203,7 +207,7 @@ template <int ACT, int DK, int VT> struct ChunkGeom {
     static constexpr int VS = VT + 8, PS = C + 8;
     static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
     static constexpr int buffers(int depth) {
-        return 2 * NP * (depth * (QP + KP + VP) + PP) + 2 * (C * 16 + 4) + 8;
+        return 2 * (NP * depth * (QP + KP + VP) + NS * PP) + 2 * (C * 16 + 4) + 8;
     }
     // chunks in the LDS: two, or one where two do not fit
     static constexpr int kDepth = buffers(2) <= kLds ? 2 : 1;
@@ -227,7 +231,7 @@ __global__ __launch_bounds__((ChunkGeom<ACT, DK, VT>::kThreads), (ChunkGeom<ACT,
 void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
     using T = typename Act<ACT>::T;
     using M = ChunkGeom<ACT, DK, VT>;
-    constexpr int C = M::C, NP = M::NP, PER = 16 / M::EB, MT = 64 * kMakers;
+    constexpr int C = M::C, NP = M::NP, NS = M::NS, PER = 16 / M::EB, MT = 64 * kMakers;
     constexpr int RP = DK / PER, NQ = C * RP / MT, RSTEP = MT / RP;     // q, k pieces of a row, of a maker's thread
     constexpr int VR = VT / PER, NV = C * VR / MT, VSTEP = MT / VR;     // v pieces
     constexpr int TT = C / 16, KK = C / 32, PAIRS = DK / 32;
@@ -236,7 +240,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
     // by the chunk's parity where two chunks fit
     uint16_t *const Q0 = reinterpret_cast<uint16_t *>(smem), *const K0 = Q0 + M::kDepth * NP * M::QP,
              *const V0 = K0 + M::kDepth * NP * M::KP, *const Ps = V0 + M::kDepth * NP * M::VP;
-    double *const G0 = reinterpret_cast<double *>(Ps + NP * M::PP);  // [2][C] by parity, as the next three
+    double *const G0 = reinterpret_cast<double *>(Ps + NS * M::PP);  // [2][C] by parity, as the next three
     float *const F0 = reinterpret_cast<float *>(G0 + 2 * C), *const E0 = F0 + 2 * C, *const factor = E0 + 2 * C;
 
     // neighbouring value tiles of a head and segment on one XCD (workgroups go
@@ -392,7 +396,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                     o[r] = s + r <= t ? w : 0.f;
                 }
 #pragma unroll
-                for (int w = 0; w < NP; ++w) {
+                for (int w = 0; w < NS; ++w) {
                     const uint32_t lo = take_part(o[0], o[1]);
                     *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(o[2], o[3]));
                 }
@@ -409,7 +413,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
 
         // tiles above the diagonal that the products read: zero, once
         if (FULL)
-            for (int i = mt; i < NP * M::PP; i += MT) Ps[i] = 0;
+            for (int i = mt; i < NS * M::PP; i += MT) Ps[i] = 0;
         if (chunks > 0) {
             fetch(0);
             if (maker == kMakers - 1) {
@@ -539,14 +543,13 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                 float x[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) x[r] = S[2 * pr + r / 4][r % 4];
-                uint4 sa[TT][NP];
+                uint4 sa[TT][NS];
                 split8(x, sa[0]);
 #pragma unroll
                 for (int j = 1; j < TT; ++j)
 #pragma unroll
-                    for (int w = 0; w < NP; ++w) sa[j][w] = sa[0][w];
+                    for (int w = 0; w < NS; ++w) sa[j][w] = sa[0][w];
                 mfma_tiles<TT>(sa, qb[pr & 1], acc);
-                __builtin_amdgcn_sched_barrier(0);
             }
             const float *const fs = F0 + (c & 1) * C;
 #pragma unroll
@@ -556,14 +559,15 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             const uint16_t *const pat = Ps + li * M::PS + 8 * lg;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                uint4 pb[TT][NP], vv[TT][NP];  // tiles j from 2 kk on
+                uint4 pb[TT][NS], vv[TT][NP];  // tiles j from 2 kk on
 #pragma unroll
-                for (int j = 2 * kk; j < TT; ++j)
+                for (int j = 2 * kk; j < TT; ++j) {
 #pragma unroll
-                    for (int w = 0; w < NP; ++w) {
+                    for (int w = 0; w < NS; ++w)
                         pb[j - 2 * kk][w] = *reinterpret_cast<const uint4 *>(pat + w * M::PP + 16 * j * M::PS + 32 * kk);
-                        vv[j - 2 * kk][w] = va[kk][w];
-                    }
+#pragma unroll
+                    for (int w = 0; w < NP; ++w) vv[j - 2 * kk][w] = va[kk][w];
+                }
                 if (kk == 0)
                     mfma_tiles<TT>(vv, pb, acc);
                 else

@@ -575,8 +575,10 @@ hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L
  * batch * heads < 2^21 - 7, ld_q, ld_k, ld_v < 2^22 and L < 2^30 (else HM_ERR_UNSUPPORTED).
  * Sums and the state are float32.  The prompt runs in chunks on the matrix
  * cores: decays inside a chunk are formed from float64 sums of a, float32
- * operands keep about 24 significant bits, and of bfloat16 ones only what the
- * chunk rounds on its way to y (never to the state) has fewer.  A token or a
+ * operands keep about 24 significant bits; with bfloat16 ones what the chunk
+ * rounds on its way to y (never to the state) keeps 16, so that y is off by
+ * at most some 2^-16 of the sum of its terms' absolute values before its own
+ * rounding.  A token or a
  * state that is not finite makes the y after it, in its row and heads, not
  * finite (NaN where the recurrence may have an infinity), and a token may make
  * those of up to 63 tokens before it so; never other rows.
