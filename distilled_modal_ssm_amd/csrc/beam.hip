@@ -195,7 +195,8 @@ SelectPlan select_plan(int64_t groups, int64_t beams, int64_t vocab, int64_t sel
 }
 
 // One workgroup a segment of a row: 16 bytes a thread and load, E logits in
-// registers, read once.  Bound by that read.
+// registers, read once.  Bound by that read.  (Places in a row are int: the last
+// segment ends less than 2^14 past the row, and vocab is below 2^31 - 2^14.)
 template <int ACT, int E>
 __global__ __launch_bounds__(kThreads) void beam_segment_kernel(BeamSelectArgs a, SelectPlan p) {
     using T = typename Act<ACT>::T;

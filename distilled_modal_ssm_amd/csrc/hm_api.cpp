@@ -897,7 +897,8 @@ hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, 
 static hm_status check_beams(int64_t groups, int64_t beams, int64_t vocab, int64_t select) {
     if (groups < 0 || beams < 1 || vocab < 1 || select < 1 || beams > HM_BEAM_MAX || select > HM_BEAM_MAX)
         return HM_ERR_INVALID_ARG;
-    if (vocab > INT32_MAX / beams || groups >= (int64_t(1) << 23) / beams) return HM_ERR_UNSUPPORTED;
+    // Places in a row are 32-bit: its last segment goes up to 2 * 8192 past the row's end.
+    if (vocab > (INT32_MAX - (1 << 14)) / beams || groups >= (int64_t(1) << 23) / beams) return HM_ERR_UNSUPPORTED;
     if (groups * beams > (int64_t(1) << 36) / vocab) return HM_ERR_UNSUPPORTED;
     if (select > beams * vocab) return HM_ERR_INVALID_ARG;
     return HM_OK;

@@ -635,7 +635,7 @@ hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, 
  * have another.  Softmax statistics and scores are float32; two continuations
  * whose scores differ by no more than their rounding may come in either order.
  *   1 <= beams, select <= HM_BEAM_MAX, select <= beams * vocab (else
- *   HM_ERR_INVALID_ARG), beams * vocab < 2^31, groups < 2^23 / beams,
+ *   HM_ERR_INVALID_ARG), beams * vocab < 2^31 - 2^14, groups < 2^23 / beams,
  *   groups * beams * vocab <= 2^36 (else HM_ERR_UNSUPPORTED).  ld >= vocab.
  *   workspace: hyena_beam_select_workspace bytes, 256-byte aligned, scratch.
  */

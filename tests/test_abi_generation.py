@@ -178,3 +178,17 @@ def test_beam_select_scores_in_place():
 
 def test_beam_reorder_row_limit():
     _refused(NO, hb.hyena_beam_reorder, 1, 4, FAKE, [FAKE], [(1 << 33) + 1], stream=0)
+
+
+@pytest.mark.parametrize("beams", [1, 2, 3, 64])
+def test_beam_vocabulary_fits_32_bit_places(beams):
+    """A row's last segment starts less than 8 places before the row and ends up to a whole segment
+    past it; each place, and the 16 bytes from it on, has to have a 32-bit number."""
+    most = ((1 << 31) - 1 - (1 << 14)) // beams
+    for vocab in (most + 1, ((1 << 31) - 1) // beams - 1, ((1 << 31) - 1) // beams):
+        _refused(NO, hb.hyena_beam_select_workspace, 1, beams, vocab, 1)
+        _refused(NO, _select, groups=1, beams=beams, vocab=vocab, ld=vocab, select=1, ws_bytes=1 << 60)
+    assert hb.hyena_beam_select_workspace(1, beams, most, 1) > 0
+    for segment in (2048, 8192):
+        segs = -(-(most + 7) // segment)
+        assert segs * segment + 8 < 1 << 31
