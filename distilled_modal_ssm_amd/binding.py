@@ -583,6 +583,21 @@ class _On:
         return self.guard.__exit__(*exc) if self.guard is not None else None
 
 
+def _scratch(kept, n, stream, device):
+    """n bytes of scratch memory for a call on the current stream, whose hipStream_t is ``stream``: a
+    handle's buffer of that stream, out of its dict ``kept``, or a longer one in its place.
+
+    A graph's replays write to the addresses that its capture saw, so a call that torch captures has
+    memory of that graph's own, which lives as long as the graph and which no other call is given."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    ws = kept.get(stream)
+    if ws is None or ws.numel() < n:
+        ws = kept[stream] = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws
+
+
 def _expect(name, t, dtype, shape, device):
     """A contiguous tensor of this type, shape and device."""
     if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():

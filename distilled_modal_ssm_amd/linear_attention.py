@@ -36,7 +36,7 @@ class LinearAttention:
         self.desc = hb.make_linattn_desc(self.B, self.H, self.dk, self.dv, hb.HM_BF16 if act == "bf16" else hb.HM_F32,
                                          self.scale, self.q_heads, self.k_heads, self.v_heads)
         hb.hyena_linattn_prefill_workspace(self.desc, 0)  # raises for sizes that the library refuses
-        self._ws = {}  # scratch memory of each stream
+        self._ws = {}  # scratch memory of each stream; a captured graph has its own
         self._state_shape = (self.B, self.H, self.dk, self.dv)
         self._token_shapes = ((self.B, self.q_heads * self.dk), (self.B, self.k_heads * self.dk),
                               (self.B, self.v_heads * self.dv), (self.B, self.H * self.dv))
@@ -49,10 +49,7 @@ class LinearAttention:
         n = hb.hyena_linattn_prefill_workspace(self.desc, L)
         if n == 0:
             return None, 0
-        ws = self._ws.get(stream)
-        if ws is None or ws.numel() < n:
-            ws = self._ws[stream] = self.torch.empty(n, dtype=self.torch.uint8, device=self.device)
-        return ws, n
+        return hb._scratch(self._ws, n, stream, self.device), n
 
     def _rows(self, name, t, shape, dtype):
         """Row stride of rows [..][width] of this shape, row (b, t) at (b * L + t) * stride."""

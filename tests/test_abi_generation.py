@@ -192,3 +192,69 @@ def test_beam_vocabulary_fits_32_bit_places(beams):
     for segment in (2048, 8192):
         segs = -(-(most + 7) // segment)
         assert segs * segment + 8 < 1 << 31
+
+
+class _NoDevice:
+    """Stands in for the binding's _On where there is no GPU: stream 1 is current."""
+
+    def __init__(self, device, stream):
+        pass
+
+    def __enter__(self):
+        return 1
+
+    def __exit__(self, *exc):
+        return None
+
+
+def _scratch_users(monkeypatch):
+    """Calls that use scratch memory on stream 1, in place of the library's: each returns the address it was given."""
+    import torch
+    from distilled_modal_ssm_amd import BeamSearch, LinearAttention
+    seen = []
+    monkeypatch.setattr(hb, "_On", _NoDevice)
+    monkeypatch.setattr(hb, "hyena_linattn_prefill",
+                        lambda desc, L, *a: seen.append((a[-3].data_ptr(), a[-3].numel())))
+    attn = LinearAttention(1, 2, 16, 16, "f32", device="cpu")
+
+    def prompt(L):
+        x = torch.zeros(1, L, 32)
+        attn.prefill(x, x, x, y=x, state_out=torch.zeros(1, 2, 16, 16))
+        return seen[-1]
+
+    beam = BeamSearch(2, 3, 50, device="cpu")
+    beam._select = lambda *a: seen.append((a[-3], a[-2])) or hb.HM_OK
+
+    def select(_):
+        beam.select(torch.zeros(6, 50), torch.zeros(2, 3))
+        return seen[-1]
+
+    return {"prompt": (attn, prompt), "select": (beam, select)}
+
+
+@pytest.mark.parametrize("user", ["prompt", "select"])
+def test_captured_calls_have_scratch_of_their_own(monkeypatch, user):
+    """A graph replays the addresses of its capture: they are not a buffer that the handle may replace by
+    a longer one or give to another call, and no memory of a graph is kept for later calls."""
+    import torch
+    handle, call = _scratch_users(monkeypatch)[user]
+    capturing = []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(capturing))
+    capturing.append(1)
+    at, n = call(5000)
+    assert at and n > 0 and not handle._ws
+    capturing.clear()
+    eager = call(5000)[0]
+    assert call(5000)[0] == eager and len(handle._ws) == 1
+    capturing.append(1)
+    assert call(5000)[0] != eager
+    capturing.clear()
+    assert call(5000)[0] == eager and len(handle._ws) == 1
+
+
+def test_scratch_grows_for_longer_prompts(monkeypatch):
+    import torch
+    _, call = _scratch_users(monkeypatch)["prompt"]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    sizes = [call(L)[1] for L in (2000, 60000, 2000)]
+    assert sizes[0] < sizes[1] == sizes[2]

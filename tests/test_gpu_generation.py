@@ -33,3 +33,78 @@ def test_bf16_y_has_only_its_own_rounding(kw):
     off = abs(y.cpu().double().numpy().reshape(p.y.shape) - p.y)
     most = 2.0 ** -8 * abs(p.y) + (1 + 2.0 ** -8) * (2.0 ** -16 + p.tol) * p.my
     assert (off <= most).all(), float((off - most).max())
+
+
+def _prompt_users(torch):
+    """One handle, two problems: calls that write the given outputs, the outputs, and the inputs."""
+    ps = [Problem(torch, 1, 2500, 2, 128, 128, "bf16", resume=True, seed=s) for s in (1, 2)]
+    op = ps[0].op
+
+    def call(i, out):
+        p = ps[i]
+        op.prefill(p.q, p.k, p.v, p.a, state_in=p.state, y=out[0], state_out=out[1])
+
+    def longer():
+        p = Problem(torch, 1, 4500, 2, 128, 128, "bf16")
+        op.prefill(p.q, p.k, p.v, p.a)
+
+    outs = [(torch.empty_like(ps[0].q[..., :256].contiguous()), op.new_state()) for _ in ps]
+    return call, longer, outs, [(p.buf, p.a, p.state) for p in ps]
+
+
+def _select_users(torch):
+    from distilled_modal_ssm_amd import BeamSearch
+    op = BeamSearch(4, 4, 40009)
+    g = torch.Generator().manual_seed(1)
+    xs = [(torch.randn(16, 40009, generator=g).cuda(), -torch.rand(4, 4, generator=g).cuda()) for _ in range(2)]
+
+    def call(i, out):
+        op.select(*xs[i], out=out)
+
+    outs = [tuple(torch.empty(4, 4, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32, torch.uint8))
+            for _ in xs]
+    return call, lambda: None, outs, xs
+
+
+@pytest.mark.parametrize("users", [_prompt_users, _select_users])
+def test_graphs_keep_their_scratch(users):
+    """Two graphs of one handle, captured on one stream after eager calls there; then a longer eager call, the
+    handle dropped, and other tensors in whatever memory is free.  Both replays, on streams of their own at
+    once, are right and leave those tensors alone."""
+    torch = require_gpu()
+    call, longer, outs, inputs = users(torch)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs = [torch.cuda.CUDAGraph() for _ in outs]
+    with torch.cuda.stream(side):
+        for i, out in enumerate(outs):
+            log(f"graph scratch eager {i}")
+            call(i, out)
+    side.synchronize()
+    want = [[x.clone() for x in out] for out in outs]
+    for i, out in enumerate(outs):
+        log(f"graph scratch capture {i}")
+        with torch.cuda.graph(graphs[i], stream=side):
+            call(i, out)
+    log("graph scratch longer")
+    with torch.cuda.stream(side):
+        longer()
+    side.synchronize()
+    del call, longer
+    filled = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in [1 << 10, 1 << 16, 1 << 21, 1 << 22] * 8]
+    streams = [torch.cuda.Stream() for _ in outs]
+    for r in range(4):
+        for out in outs:
+            for x in out:
+                x.fill_(3)
+        torch.cuda.synchronize()
+        log(f"graph scratch replay {r}")
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            for x, e in zip(out, w):
+                assert torch.equal(x, e)
+        assert all(bool((x == 77).all()) for x in filled)
+    del inputs
