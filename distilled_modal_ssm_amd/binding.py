@@ -649,6 +649,8 @@ class ModalHyena:
 
     def workspace(self, L: int, chunk: int = 0, algo="auto"):
         n = hyena_modal_prefill_workspace(self.desc, L, chunk, algo)
+        if self.torch.cuda.is_current_stream_capturing():  # as in _scratch: the graph's own
+            return self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device), n
         if self._ws is None or self._ws.numel() < n:
             self._ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device)
         return self._ws, n

@@ -258,3 +258,21 @@ def test_scratch_grows_for_longer_prompts(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     sizes = [call(L)[1] for L in (2000, 60000, 2000)]
     assert sizes[0] < sizes[1] == sizes[2]
+
+
+def test_captured_modal_prompts_have_scratch_of_their_own(monkeypatch):
+    import numpy as np
+    import torch
+    op = hb.ModalHyena(np.zeros((2, 8, 2)), np.zeros((2, 8, 2)), np.zeros(2), 1, 64, "f32", device="cpu")
+    capturing = []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(capturing))
+    capturing.append(1)
+    first, n = op.workspace(70000)
+    assert n > 0 and first.numel() >= n and op._ws is None
+    capturing.clear()
+    eager = op.workspace(70000)[0]
+    capturing.append(1)
+    own = op.workspace(70000)[0]
+    assert own.data_ptr() != eager.data_ptr()
+    capturing.clear()
+    assert op.workspace(70000)[0] is eager
