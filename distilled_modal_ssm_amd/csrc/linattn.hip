@@ -391,9 +391,10 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                 float o[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    // chosen after the product: a later token's may have overflowed
-                    const float w = x[n][r] * __builtin_amdgcn_exp2f((float)(gt - gs[s + r]));
-                    o[r] = s + r <= t ? w : 0.f;
+                    // the product may have overflowed with a later token's key, or one from before
+                    // a reset, and is not used then: 0 times it would be NaN
+                    const float f = __builtin_amdgcn_exp2f((float)(gt - gs[s + r]));
+                    o[r] = s + r <= t && f != 0.f ? x[n][r] * f : 0.f;
                 }
 #pragma unroll
                 for (int w = 0; w < NS; ++w) {
@@ -553,7 +554,10 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             }
             const float *const fs = F0 + (c & 1) * C;
 #pragma unroll
-            for (int j = 0; j < TT; ++j) acc[j] *= fs[16 * j + li];
+            for (int j = 0; j < TT; ++j) {
+                const float f = fs[16 * j + li];
+                acc[j] = f != 0.f ? acc[j] * f : f32x4{0.f, 0.f, 0.f, 0.f};  // S^T q may have overflowed
+            }
         };
         auto add_near = [&](int c) {
             const uint16_t *const pat = Ps + li * M::PS + 8 * lg;

@@ -108,3 +108,37 @@ def test_graphs_keep_their_scratch(users):
                 assert torch.equal(x, e)
         assert all(bool((x == 77).all()) for x in filled)
     del inputs
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("L,reset", [(7, 4), (40, 20), (40, 32), (100, 50), (100, 70), (200, 128), (2500, 1100)])
+def test_a_reset_forgets_what_would_overflow(act, L, reset):
+    """Keys of 1e22 before a decay of -infinity and queries of 1e22 from it on: q . k and S^T q pass
+    float32, but no term of the recurrence pairs them."""
+    torch = require_gpu()
+    from test_gpu_linattn import _heads64, _recurrence
+    from distilled_modal_ssm_amd import LinearAttention
+    B, H, dk, dv = 1, 3, 64, 48
+    op = LinearAttention(B, H, dk, dv, act)
+    g = torch.Generator().manual_seed(L + reset)
+    q, k, v = (torch.randn(B, L, H, d, generator=g) for d in (dk, dk, dv))
+    k[:, :reset] *= 1e22
+    q[:, :reset] *= 1e-22
+    q[:, reset:] *= 1e22
+    k[:, reset:] *= 1e-22
+    q, k, v = (x.reshape(B, L, -1).to(op.tdtype).cuda() for x in (q, k, v))
+    a = -torch.rand(B, L, H, generator=g)
+    a[:, reset] = -float("inf")
+    a = a.cuda()
+    log(f"linattn reset overflow {act} L={L} reset={reset}")
+    y, S = op.prefill(q, k, v, a)
+    torch.cuda.synchronize()
+    q64, k64, v64 = (_heads64(x, H, H, d) for x, d in ((q, dk), (k, dk), (v, dv)))
+    a64, zero = a.cpu().double().numpy(), np.zeros((B, H, dk, dv))
+    ry, rS = _recurrence(q64, k64, v64, a64, zero, [L] * B)
+    my, mS = _recurrence(abs(q64), abs(k64), abs(v64), a64, zero, [L] * B)
+    ry, my = ry * op.scale, my * op.scale
+    tol = (dk + 128 + 8 * L / 64 + 16) * 2.0 ** -24
+    ty = tol * my + (2.0 ** -8 * (abs(ry) + 2 * my) if act == "bf16" else 0.0)
+    assert (abs(y.cpu().double().numpy().reshape(ry.shape) - ry) <= ty).all()
+    assert (abs(S.cpu().double().numpy() - rS) <= tol * mS).all()
