@@ -578,10 +578,13 @@ hm_status hyena_linattn_prefill_workspace(const hm_linattn_desc *desc, int64_t L
  * operands keep about 24 significant bits; with bfloat16 ones what the chunk
  * rounds on its way to y (never to the state) keeps 16, so that y is off by
  * at most some 2^-16 of the sum of its terms' absolute values before its own
- * rounding.  A token or a
- * state that is not finite makes the y after it, in its row and heads, not
- * finite (NaN where the recurrence may have an infinity), and a token may make
- * those of up to 63 tokens before it so; never other rows.
+ * rounding.  A token or a state that is not finite makes the y after it, in
+ * its row and heads, not finite (NaN where the recurrence may have an infinity;
+ * behind decays whose product is 0, either), and a token may make those of up
+ * to 63 tokens before it so; never other rows.  Not finite counts a float32
+ * value above bfloat16's largest (3.39e38) too.  y_t is also not finite where
+ * q_t . k_s of an s <= t in its chunk, or S^T q_t, passes float32 before the
+ * decay's factor, unless that factor is 0.
  */
 hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const int32_t *lengths,
                                 const void *q, int64_t ld_q, const void *k, int64_t ld_k,
