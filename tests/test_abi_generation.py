@@ -276,3 +276,17 @@ def test_captured_modal_prompts_have_scratch_of_their_own(monkeypatch):
     assert own.data_ptr() != eager.data_ptr()
     capturing.clear()
     assert op.workspace(70000)[0] is eager
+
+
+@pytest.mark.parametrize("act", [hb.HM_F32, hb.HM_BF16])
+@pytest.mark.parametrize("dims", [(32, 32), (64, 128), (128, 128), (256, 256)])
+def test_long_prompts_of_few_heads_run_in_segments(act, dims):
+    """Their states need memory (a first state, and one a segment, at least two); a missing, small or
+    misaligned one is refused."""
+    d = _desc(batch=1, heads=2, key_dim=dims[0], value_dim=dims[1], act_dtype=act)
+    n = hb.hyena_linattn_prefill_workspace(d, 60000)
+    assert n >= 2 * 2 * dims[0] * dims[1] * 4
+    ld = dict(ld_q=512, ld_k=512, ld_v=512, ld_y=512, ld_decay=0)
+    _refused(WS, _prefill, d, L=60000, workspace=None, ws_bytes=n, **ld)
+    _refused(WS, _prefill, d, L=60000, workspace=FAKE, ws_bytes=n - 1, **ld)
+    _refused(NO, _prefill, d, L=60000, workspace=FAKE + 16, ws_bytes=n, **ld)

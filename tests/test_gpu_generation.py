@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from _gpu_common import log, require_gpu
+from distilled_modal_ssm_amd import binding as hb
 from test_gpu_linattn import Problem, _prefill
 
 pytestmark = pytest.mark.gpu
@@ -142,3 +143,41 @@ def test_a_reset_forgets_what_would_overflow(act, L, reset):
     ty = tol * my + (2.0 ** -8 * (abs(ry) + 2 * my) if act == "bf16" else 0.0)
     assert (abs(y.cpu().double().numpy().reshape(ry.shape) - ry) <= ty).all()
     assert (abs(S.cpu().double().numpy() - rS) <= tol * mS).all()
+
+
+# The prompt kernel's forms that smaller problems do not reach: 128 value columns a workgroup over
+# several chunks, in one pass and in segments (True), and segments of the narrowest and widest keys.
+FORMS = [
+    ("bf16", False, dict(B=16, H=16, L=200, dk=128, dv=128)),
+    ("bf16", False, dict(B=16, H=16, L=200, dk=100, dv=100, special="reset", resume=True)),  # rows of 8 bytes
+    ("bf16", False, dict(B=16, H=16, L=200, dk=100, dv=101, lengths=[200, 0, 64, 65] * 4)),  # of 2
+    ("bf16", False, dict(B=8, H=64, L=200, dk=32, dv=128, lengths=[200, 199, 128, 1] * 2, resume=True)),
+    ("bf16", True, dict(B=1, H=16, L=1300, dk=128, dv=128, special="reset")),
+    ("bf16", True, dict(B=1, H=50, L=800, dk=128, dv=128, special="reset", resume=True)),
+    ("bf16", True, dict(B=1, H=50, L=750, dk=100, dv=100, lengths=[733])),
+    ("bf16", True, dict(B=1, H=20, L=1300, dk=128, dv=124, kh=4, vh=5, decay="head", resume=True)),
+    ("bf16", True, dict(B=2, H=2, L=600, dk=256, dv=72, lengths=[600, 411], resume=True)),
+    ("bf16", True, dict(B=2, H=2, L=1500, dk=30, dv=40, special="reset", resume=True)),
+    ("bf16", True, dict(B=2, H=2, L=1501, dk=32, dv=130, lengths=[1501, 257], pad=4)),
+    ("f32", False, dict(B=6, H=32, L=150, dk=64, dv=128, kh=8, vh=8, lengths=[150, 31, 0, 64, 149, 97], resume=True)),
+    ("f32", False, dict(B=6, H=32, L=150, dk=64, dv=70, special="reset")),
+    ("f32", False, dict(B=8, H=64, L=100, dk=32, dv=128, decay="none", resume=True)),
+    ("f32", True, dict(B=1, H=16, L=700, dk=64, dv=128, special="reset", resume=True)),
+    ("f32", True, dict(B=1, H=16, L=700, dk=62, dv=126, lengths=[500])),
+    ("f32", True, dict(B=1, H=50, L=450, dk=64, dv=128, lengths=[449], resume=True)),
+    ("f32", True, dict(B=1, H=20, L=1000, dk=62, dv=126, special="reset")),
+    ("f32", True, dict(B=2, H=2, L=600, dk=256, dv=72, lengths=[600, 411], resume=True)),
+    ("f32", True, dict(B=1, H=2, L=900, dk=250, dv=200, special="reset")),
+    ("f32", True, dict(B=2, H=4, L=700, dk=30, dv=40, decay="head", lengths=[10, 700])),
+]
+
+
+@pytest.mark.parametrize("act,segments,kw", FORMS, ids=str)
+def test_prompt_forms(act, segments, kw):
+    torch = require_gpu()
+    p = Problem(torch, act=act, **kw)
+    assert (hb.hyena_linattn_prefill_workspace(p.op.desc, p.L) > 0) == segments
+    log(f"linattn form {act} {kw}")
+    y, S = _prefill(p)
+    torch.cuda.synchronize()
+    p.check(y, S)
