@@ -59,8 +59,9 @@ class HybridLM:
     def _new(self, *shape):
         return self.torch.empty(shape, dtype=self.torch.bfloat16, device=self.device)
 
-    def prefill(self, tokens):
-        """tokens [B][L] -> (logits [B * L][vocab], the layers' states)."""
+    def prefill(self, tokens, last=False):
+        """tokens [B][L] -> (logits [B * L][vocab], or [B][vocab] of each prompt's ``last`` position
+        alone, and the layers' states)."""
         B, L = tokens.shape
         D = self.D
         x = self.embedding[tokens.long()].reshape(B * L, D)
@@ -70,16 +71,18 @@ class HybridLM:
             y, state = op.prefill(q, k, v) if kind == "hyena" else op.prefill(q, k, v, p)
             states.append(state)
             x = self._dense(y.view(B * L, D), w_out, self._new(B * L, D))
-        return self._dense(x, self.head, self._new(B * L, self.vocab)), states
+        if last:
+            x = x.view(B, L, D)[:, -1].contiguous()
+        return self._dense(x, self.head, self._new(x.shape[0], self.vocab)), states
 
     def generate(self, prompts, beams: int, steps: int, end_token=None):
         """The best ``beams`` continuations of every prompt [G][L]: (tokens [G][beams][steps],
         scores [G][beams]), best first.  Past its end a sequence repeats end_token."""
         torch, D = self.torch, self.D
-        G, L = prompts.shape
+        G = prompts.shape[0]
         rows = G * beams
-        logits, states = self.prefill(prompts)
-        logits = logits.view(G, L, -1)[:, -1].repeat_interleave(beams, 0)
+        logits, states = self.prefill(prompts, last=True)
+        logits = logits.repeat_interleave(beams, 0)
         states = [s.repeat_interleave(beams, 0) for s in states]
         other = [torch.empty_like(s) if kind == "attention" else None for s, (kind, *_) in zip(states, self.layers)]
         modal = [s for s, (kind, *_) in zip(states, self.layers) if kind == "hyena"]

@@ -181,3 +181,43 @@ def test_prompt_forms(act, segments, kw):
     y, S = _prefill(p)
     torch.cuda.synchronize()
     p.check(y, S)
+
+
+def _hybrid(torch, **kw):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    from beam_generate import random_model
+    return random_model(torch, **kw)
+
+
+def test_a_search_forms_the_prompts_last_logits_only():
+    """No memory for the logits of every position of a long prompt (492 MB here, the rest is below 100)."""
+    torch = require_gpu()
+    L, V = 30000, 8192
+    model = _hybrid(torch, layers=2, width=128, vocab=V, heads=4, modes=8)
+    prompt = torch.randint(0, V, (1, L), generator=torch.Generator().manual_seed(1)).cuda()
+    model.generate(prompt[:, :100], 2, 2)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    log("hybrid last logits")
+    model.generate(prompt, 2, 2)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < L * V * 2 // 2
+
+
+def test_last_logits_are_the_last_of_all():
+    """Both are the same sums in another order, rounded to bfloat16 once: a neighbouring value at most."""
+    torch = require_gpu()
+    model = _hybrid(torch, layers=2, width=128, vocab=600, heads=4, modes=8)
+    prompts = torch.randint(0, 600, (3, 90), generator=torch.Generator().manual_seed(1)).cuda()
+    log("hybrid last of all")
+    every, states = model.prefill(prompts)
+    last, states1 = model.prefill(prompts, last=True)
+    torch.cuda.synchronize()
+    every = every.view(3, 90, 600)[:, -1]
+    assert last.shape == every.shape
+    assert bool(((last.float() - every.float()).abs() <= 2.0 ** -7 * every.float().abs() + 2.0 ** -16).all())
+    assert all(torch.equal(a, b) for a, b in zip(states, states1))
