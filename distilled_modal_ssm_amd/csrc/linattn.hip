@@ -204,8 +204,12 @@ template <int ACT, int DK, int VT> struct ChunkGeom {
     // often transposed, with 2 where its row is an odd multiple of 32 (4 to 6 else).
     static constexpr int QS = DK + 16;
     static constexpr int KS = DK == 32 ? 32 : DK + 32;
-    static constexpr int VS = VT + 8, PS = C + 8;
-    static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = C * PS;  // planes
+    static constexpr int VS = VT + 8;
+    // Weighted K Q^T has C columns a row, but only 32 in its first 32 rows: later tokens'.
+    // (Two workgroups of 64 bfloat16 keys and 64 value columns fit a CU with that: 128 x 16
+    // heads, 16 tokens: 40 us against 67.)
+    static constexpr int PS0 = 32 + 8, PS1 = C + 8;
+    static constexpr int QP = C * QS, KP = C * KS, VP = C * VS, PP = 32 * PS0 + (C - 32) * PS1;  // planes
     static constexpr int buffers(int depth) {
         return 2 * (NP * depth * (QP + KP + VP) + NS * PP) + 2 * (C * 16 + 4) + 8;
     }
@@ -387,6 +391,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             for (int n = 0; n < N; ++n) {
                 const uint32_t code = tiles >> (4 * n) & 15;
                 const int t = 16 * (code & 3) + li, s = 16 * (code >> 2) + 4 * lg;
+                uint16_t *const to = Ps + (t < 32 ? t * M::PS0 : 32 * M::PS0 + (t - 32) * M::PS1) + s;
                 const double gt = gs[t];
                 float o[4];
 #pragma unroll
@@ -399,7 +404,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
 #pragma unroll
                 for (int w = 0; w < NS; ++w) {
                     const uint32_t lo = take_part(o[0], o[1]);
-                    *reinterpret_cast<uint2 *>(Ps + w * M::PP + t * M::PS + s) = make_uint2(lo, take_part(o[2], o[3]));
+                    *reinterpret_cast<uint2 *>(to + w * M::PP) = make_uint2(lo, take_part(o[2], o[3]));
                 }
             }
         };
@@ -560,7 +565,7 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
             }
         };
         auto add_near = [&](int c) {
-            const uint16_t *const pat = Ps + li * M::PS + 8 * lg;
+            const uint16_t *const pat0 = Ps + li * M::PS0 + 8 * lg, *const pat1 = Ps + 32 * M::PS0 + li * M::PS1 + 8 * lg;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 uint4 pb[TT][NS], vv[TT][NP];  // tiles j from 2 kk on
@@ -568,7 +573,8 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
                 for (int j = 2 * kk; j < TT; ++j) {
 #pragma unroll
                     for (int w = 0; w < NS; ++w)
-                        pb[j - 2 * kk][w] = *reinterpret_cast<const uint4 *>(pat + w * M::PP + 16 * j * M::PS + 32 * kk);
+                        pb[j - 2 * kk][w] = *reinterpret_cast<const uint4 *>(
+                            (j < 2 ? pat0 + 16 * j * M::PS0 : pat1 + 16 * (j - 2) * M::PS1 + 32 * kk) + w * M::PP);
 #pragma unroll
                     for (int w = 0; w < NP; ++w) vv[j - 2 * kk][w] = va[kk][w];
                 }
