@@ -61,6 +61,22 @@ constexpr int kMaxDk = 256;
 // exp(a) of a log decay; a is bounded below so that sums of it stay finite
 __device__ __forceinline__ float bound_decay(float a) { return a < -1000.f ? -1000.f : a; }
 
+// The factor exp(a) of one token's state in two floats: a float32 one is off by up to
+// 2^-24, the same way at every token, so that a head that remembers 3000 of them would
+// drift by 1e-4 of its state and disagree with the prompt's.  A head that remembers more
+// than eight gets 1 and exp(a) - 1, by Taylor's series (to 2^-24 of it), others exp(a)
+// and nothing.
+__device__ __forceinline__ float2 decay_factor(float a) {
+    const float m = a * fmaf(a, fmaf(a, fmaf(a, fmaf(a, 1 / 120.f, 1 / 24.f), 1 / 6.f), 0.5f), 1.f);
+    return fabsf(a) <= 0.125f ? make_float2(1.f, m) : make_float2(expf(bound_decay(a)), 0.f);
+}
+
+// f s + kv, or s + kv of a layer without decay (whose infinite states stay infinite).
+template <bool DECAY>
+__device__ __forceinline__ float decayed(float2 f, float s, float kv) {
+    return DECAY ? fmaf(f.x, s, fmaf(f.y, s, kv)) : s + kv;
+}
+
 // ------------------------------------------------------------------ prompt
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -724,7 +740,7 @@ constexpr int short_prompt_tokens(int act) { return act == kF32 ? 16 : 8; }
 
 // LDS of linattn_short_kernel: a token's q, k, decay, values, and y of four waves
 constexpr int short_bytes(int tokens, int dk, int tile) {
-    return tokens * (8 * dk + 4 + 4 * tile + 4 * tile * (kThreads / kWave));
+    return tokens * (8 * dk + 8 + 4 * tile + 4 * tile * (kThreads / kWave));
 }
 
 // A prompt of at most so many tokens, all float32: the layout of one token's kernel
@@ -732,7 +748,7 @@ constexpr int short_bytes(int tokens, int dk, int tile) {
 // the tokens in registers and written once.  Bound by the state's way out, and past
 // some 8 tokens by the vector ALUs.  (37 x 4 heads of 256 x 256, 3 float32 tokens:
 // 12.7 us, 50.8 in chunks; 44 x 24 of 16 x 16, 8 bfloat16 ones: 14.3, 17.7 in chunks.)
-template <int ACT, int LANES, int V>
+template <int ACT, int LANES, int V, bool DECAY>
 __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, int vtiles) {
     using T = typename Act<ACT>::T;
     typedef float vec __attribute__((ext_vector_type(V)));
@@ -746,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, 
     vec *const part = reinterpret_cast<vec *>(smem);                    // [waves][L][LANES]
     float *const vs = reinterpret_cast<float *>(part + kThreads / kWave * L * LANES);  // [L][TILE]
     float2 *const qk = reinterpret_cast<float2 *>(vs + L * TILE);       // [L][dk]: q scale, k
-    float *const g = reinterpret_cast<float *>(qk + L * dk);            // [L]
+    float2 *const g = qk + L * dk;                                      // [L]
     const T *const q = static_cast<const T *>(a.q) + b * L * a.ld_q + h * a.s.qh / a.s.H * dk;
     const T *const k = static_cast<const T *>(a.k) + b * L * a.ld_k + h * a.s.kh / a.s.H * dk;
     const T *const v = static_cast<const T *>(a.v) + b * L * a.ld_v + h * a.s.vh / a.s.H * dv + col0;
@@ -759,7 +775,7 @@ __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, 
         vs[i] = col0 + c < dv ? Act<ACT>::ld(v + t * a.ld_v + c) : 0.f;
     }
     if (tid < len)
-        g[tid] = a.decay ? expf(bound_decay(a.decay[a.ld_decay ? (b * L + tid) * a.ld_decay + h : h])) : 1.f;
+        g[tid] = DECAY ? decay_factor(a.decay[a.ld_decay ? (b * L + tid) * a.ld_decay + h : h]) : float2{};
     __syncthreads();
     const int64_t base = unit * (int64_t)dk * dv + col;
     const bool own = col < dv;  // V divides dv
@@ -774,7 +790,7 @@ __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, 
         }
         for (int t = 0; t < len; ++t) {
             const vec x = reinterpret_cast<const vec *>(vs + t * TILE)[lane];
-            const float f = g[t];
+            const float2 f = g[t];
             vec y = {};
 #pragma unroll
             for (int n = 0; n < FLY; ++n) {
@@ -783,7 +799,7 @@ __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, 
                     const float2 w = qk[t * dk + i];
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        s[n][e] = fmaf(f, s[n][e], w.y * x[e]);
+                        s[n][e] = decayed<DECAY>(f, s[n][e], w.y * x[e]);
                         y[e] = fmaf(w.x, s[n][e], y[e]);
                     }
                 }
@@ -821,7 +837,7 @@ __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, 
 // LANES threads of V columns a key row, 256 / LANES rows at a time, every row's
 // load of a thread in flight before the first is used (in turns of 16).
 // Bound by the state's way in and out.
-template <int ACT, int LANES, int V>
+template <int ACT, int LANES, int V, bool DECAY>
 __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, int vtiles) {
     using T = typename Act<ACT>::T;
     typedef float vec __attribute__((ext_vector_type(V)));
@@ -849,7 +865,7 @@ __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, 
         qk[i] = make_float2(
             a.s.scale * Act<ACT>::ld(static_cast<const T *>(a.q) + b * a.ld_q + h * a.s.qh / a.s.H * dk + i),
             Act<ACT>::ld(static_cast<const T *>(a.k) + b * a.ld_k + h * a.s.kh / a.s.H * dk + i));
-    const float g = a.decay ? expf(bound_decay(a.decay[a.ld_decay ? b * a.ld_decay + h : h])) : 1.f;
+    const float2 g = DECAY ? decay_factor(a.decay[a.ld_decay ? b * a.ld_decay + h : h]) : float2{};
     vec v = {}, y = {};
     if (own) {
         const T *at = static_cast<const T *>(a.v) + b * a.ld_v + h * a.s.vh / a.s.H * dv + col;
@@ -871,7 +887,7 @@ __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, 
                 const float2 w = qk[i];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    s[n][e] = fmaf(g, s[n][e], w.y * v[e]);
+                    s[n][e] = decayed<DECAY>(g, s[n][e], w.y * v[e]);
                     y[e] = fmaf(w.x, s[n][e], y[e]);
                 }
                 __builtin_nontemporal_store(s[n], reinterpret_cast<vec *>(out + (int64_t)i * dv));
@@ -894,16 +910,16 @@ __global__ __launch_bounds__(kThreads) void linattn_token_kernel(LinAttnArgs a, 
 }
 
 // One token (short_prompt false) or a short prompt.
-template <int ACT, int LANES, int V>
+template <int ACT, int LANES, int V, bool DECAY>
 hipError_t launch_token(const LinAttnArgs &a, bool short_prompt, hipStream_t stream) {
     const int vtiles = (a.s.dv + LANES * V - 1) / (LANES * V);
     const dim3 grid((unsigned)(a.s.B * a.s.H * vtiles));
     if (!short_prompt) {
-        linattn_token_kernel<ACT, LANES, V><<<grid, kThreads, 0, stream>>>(a, vtiles);
+        linattn_token_kernel<ACT, LANES, V, DECAY><<<grid, kThreads, 0, stream>>>(a, vtiles);
         return hipGetLastError();
     }
     const int bytes = short_bytes((int)a.L, a.s.dk, LANES * V);
-    const auto kernel = linattn_short_kernel<ACT, LANES, V>;
+    const auto kernel = linattn_short_kernel<ACT, LANES, V, DECAY>;
     if (bytes > 65536) {
         const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -911,6 +927,12 @@ hipError_t launch_token(const LinAttnArgs &a, bool short_prompt, hipStream_t str
     }
     kernel<<<grid, kThreads, bytes, stream>>>(a, vtiles);
     return hipGetLastError();
+}
+
+template <int ACT, int LANES, int V>
+hipError_t launch_token(const LinAttnArgs &a, bool short_prompt, hipStream_t stream) {
+    return a.decay ? launch_token<ACT, LANES, V, true>(a, short_prompt, stream)
+                   : launch_token<ACT, LANES, V, false>(a, short_prompt, stream);
 }
 
 // 16-byte pieces of the state where its rows allow them.  128 value columns a

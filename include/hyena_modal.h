@@ -593,7 +593,10 @@ hm_status hyena_linattn_prefill(const hm_linattn_desc *desc, int64_t L, const in
                                 void *workspace, size_t ws_bytes, void *stream);
 
 /*
- * One generated token for every batch row: the recurrence once, all float32.
+ * One generated token for every batch row: the recurrence once, all float32, with
+ * a factor exp(a) that is not rounded where a head remembers more than a few
+ * tokens, so that many steps do not drift from a prompt of the same tokens (an
+ * infinite state may become NaN).
  *   q [batch][ld_q], k, v, y alike; log_decay [heads] with ld_decay = 0,
  *   [batch][ld_decay], or NULL.
  *   src_rows  [batch] int32 or NULL: row b continues row src_rows[b] of

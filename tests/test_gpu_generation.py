@@ -221,3 +221,32 @@ def test_last_logits_are_the_last_of_all():
     assert last.shape == every.shape
     assert bool(((last.float() - every.float()).abs() <= 2.0 ** -7 * every.float().abs() + 2.0 ** -16).all())
     assert all(torch.equal(a, b) for a, b in zip(states, states1))
+
+
+@pytest.mark.parametrize("piece", [1, 16])
+def test_slow_heads_do_not_drift_over_many_tokens(piece):
+    """8000 tokens one at a time, and in prompts of 16, through heads that remember 300 to 3000 of them.
+
+    A step rounds the state once, by 2^-24 / sqrt(3) of it at random (2-norm), and the T tokens that a
+    head remembers leave sqrt(T / 2) times that: 1.4e-6 for T = 3000, 5e-6 with room for a state that was
+    larger before.  A factor that is off by up to 2^-25 the same way at each token leaves T times that."""
+    torch = require_gpu()
+    from distilled_modal_ssm_amd import LinearAttention
+    n, H, d = 8000, 16, 32
+    op = LinearAttention(1, H, d, d, "f32")
+    g = torch.Generator().manual_seed(9)
+    q, k, v = (torch.randn(1, n, H * d, generator=g).cuda() for _ in range(3))
+    a = -torch.exp(-torch.linspace(5.7, 8.0, H)).cuda()
+    S = op.new_state()
+    log(f"linattn long generation by {piece}")
+    for t in range(0, n, piece):
+        if piece == 1:
+            op.decode_step(q[:, t], k[:, t], v[:, t], S, a)
+        else:
+            op.prefill(*(x[:, t:t + piece].contiguous() for x in (q, k, v)), a, state_in=S, state_out=S)
+    ref = torch.zeros(H, d, d, dtype=torch.float64, device="cuda")
+    f = torch.exp(a.double())[:, None, None]
+    for t in range(n):
+        ref = f * ref + k[0, t].double().view(H, d, 1) * v[0, t].double().view(H, 1, d)
+    off = (S[0].double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+    assert float(off.max()) <= 5e-6, off.tolist()
