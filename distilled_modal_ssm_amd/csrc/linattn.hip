@@ -734,9 +734,13 @@ __global__ __launch_bounds__(kThreads) void linattn_join_kernel(LinAttnArgs a, L
 
 // ------------------------------------------------------------------ a few tokens
 
-// Tokens of a prompt that the chunks are too long for.  (40 x 16 heads of 128 x 128:
-// 12 float32 tokens 28 us, 54 in chunks; 16 bfloat16 ones 62, 40 in chunks.)
-constexpr int short_prompt_tokens(int act) { return act == kF32 ? 16 : 8; }
+// Tokens of a prompt that the chunks are too long for.  Of eight shapes of 16 to 2048
+// rows and heads, keys of 16 to 256: 10 bfloat16 tokens take all of them less time here
+// (40 x 16 heads of 128 x 128: 31 us, 41 in chunks; 128 x 16 of 64 x 64: 39, 40), 12 not
+// (43, 40).  A float32 chunk has six products for one: with 14 tokens shapes of many
+// heads are faster here (38, 58), of few in chunks (1 x 16 heads: 13.4, 11.4), and with
+// 16 most are (70, 58).
+constexpr int short_prompt_tokens(int act) { return act == kF32 ? 14 : 10; }
 
 // LDS of linattn_short_kernel: a token's q, k, decay, values, and y of four waves
 constexpr int short_bytes(int tokens, int dk, int tile) {

@@ -250,3 +250,16 @@ def test_slow_heads_do_not_drift_over_many_tokens(piece):
         ref = f * ref + k[0, t].double().view(H, d, 1) * v[0, t].double().view(H, 1, d)
     off = (S[0].double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
     assert float(off.max()) <= 5e-6, off.tolist()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [10, 11, 14, 15])
+@pytest.mark.parametrize("kw", [dict(B=40, H=16, dk=256, dv=128, lengths=[15, 3, 14, 0] * 10, resume=True),
+                                dict(B=2, H=3, dk=100, dv=33, special="reset", pad=1)], ids=str)
+def test_the_longest_short_prompts_and_the_next(act, L, kw):
+    torch = require_gpu()
+    p = Problem(torch, act=act, L=L, **kw)
+    log(f"linattn short or in chunks {act} L={L} {kw}")
+    y, S = _prefill(p)
+    torch.cuda.synchronize()
+    p.check(y, S)
