@@ -926,7 +926,8 @@ hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_
         !aligned(out_tokens, 4) || !aligned(out_parents, 4))
         return HM_ERR_UNSUPPORTED;
     if (groups * beams > kMaxElems / ld) return HM_ERR_INVALID_ARG;
-    if (out_scores == scores && select != beams) return HM_ERR_INVALID_ARG;  // a group's would land on another's
+    // in place, a group's would land on another's
+    if ((out_scores == scores || (finished && out_finished == finished)) && select != beams) return HM_ERR_INVALID_ARG;
     const size_t need = hm::beam_select_workspace(groups, beams, vocab, select);
     if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return HM_ERR_UNSUPPORTED;

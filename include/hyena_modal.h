@@ -635,8 +635,8 @@ hm_status hyena_linattn_decode_step(const hm_linattn_desc *desc, const void *q, 
  *   end_token in 0 .. vocab-1, or -1 for none (then finished must be NULL).
  *   out_scores, out_tokens, out_parents (beam in the group), out_finished (the
  *   parent had ended, or the token is end_token): [groups][select] float32,
- *   int32, int32, bytes.  out_finished may be NULL; out_scores may equal scores
- *   where select = beams (else HM_ERR_INVALID_ARG).
+ *   int32, int32, bytes.  out_finished may be NULL; out_scores may equal scores,
+ *   and out_finished finished, where select = beams (else HM_ERR_INVALID_ARG).
  * Continuations of score -infinity are returned only where fewer than select
  * have another.  Softmax statistics and scores are float32; two continuations
  * whose scores differ by no more than their rounding may come in either order.

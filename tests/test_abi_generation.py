@@ -290,3 +290,12 @@ def test_long_prompts_of_few_heads_run_in_segments(act, dims):
     _refused(WS, _prefill, d, L=60000, workspace=None, ws_bytes=n, **ld)
     _refused(WS, _prefill, d, L=60000, workspace=FAKE, ws_bytes=n - 1, **ld)
     _refused(NO, _prefill, d, L=60000, workspace=FAKE + 16, ws_bytes=n, **ld)
+
+
+def test_beam_select_finished_in_place():
+    """As for the scores: only where every group's new bytes take the place of its own."""
+    kw = dict(finished=FAKE, out_finished=FAKE, end_token=0, out_scores=2 * FAKE)
+    _refused(BAD, _select, select=3, **kw)
+    _refused(BAD, _select, select=8, **kw)
+    _refused(WS, _select, select=4, workspace=None, **kw)
+    _refused(WS, _select, select=8, workspace=None, **{**kw, "out_finished": 3 * FAKE})

@@ -263,3 +263,25 @@ def test_the_longest_short_prompts_and_the_next(act, L, kw):
     y, S = _prefill(p)
     torch.cuda.synchronize()
     p.check(y, S)
+
+
+def test_select_with_scores_and_finished_in_place():
+    """Eight steps on the same buffers, against the same steps on new ones."""
+    torch = require_gpu()
+    from distilled_modal_ssm_amd import BeamSearch
+    G, K, V = 7, 4, 3001
+    op = BeamSearch(G, K, V, end_token=5)
+    g = torch.Generator().manual_seed(4)
+    scores, finished = op.first_scores(), torch.zeros(G, K, dtype=torch.uint8, device="cuda")
+    s, f = scores.clone(), finished.clone()
+    tokens, parents = (torch.empty(G, K, dtype=torch.int32, device="cuda") for _ in range(2))
+    for step in range(8):
+        x = torch.randn(G * K, V, generator=g).cuda()
+        x[:, 5] += 6.0
+        log(f"beam in place {step}")
+        scores, want_t, want_p, finished = op.select(x, scores, finished)
+        op.select(x, s, f, out=(s, tokens, parents, f))
+        torch.cuda.synchronize()
+        for got, want in ((s, scores), (tokens, want_t), (parents, want_p), (f, finished)):
+            assert torch.equal(got, want)
+    assert bool(f.any())
