@@ -18,7 +18,7 @@
 //                (bfloat16: off by at most 2^-16 of a term, so y by 2^-16 of the
 //                sum of its terms' absolute values beside its own rounding of
 //                2^-8; one part: 16 x 2048 tokens, 16 heads of 128: 124 us against
-//                146, but y's error is 1.41 times that of its rounding for terms
+//                147, but y's error is 1.41 times that of its rounding for terms
 //                of random sign and has no bound where they cancel; three: 165);
 //   products of parts i and j are left out where i + j > 2 (below 2^-24).
 // G is summed in float64 (and in units of log 2, for the exponential's
@@ -39,10 +39,11 @@
 // from a zero state (k and v only, the last chunk first), a scan joins the states,
 // and the full form starts every segment from its own.
 //
-// What bounds it (MI355X).  Many rows and heads: the way of q, k, v and y through
-// HBM; taking out any of the products changes nothing (16 rows x 2048 tokens, 16
-// heads of 128, bfloat16: 556 MB in 122-126 us, 4.5 TB/s; a large copy has 5.4).  A
-// prompt in segments reads k and v twice (65536 tokens, 16 heads: 1.6 GB in 363 us).
+// What bounds it (MI355X).  Many rows and heads of bfloat16: the takers' instructions,
+// whose vector part (the operands' parts) and matrix part go in turn: 52 and 37 % of
+// the cycles by counters; 16 rows x 2048 tokens, 16 heads of 128: 556 MB in 146-150
+// us, 3.8 TB/s (a large copy has 5.4; 124 us with y's operands in one part).  A prompt
+// in segments reads k and v twice (65536 tokens, 16 heads: 1.6 GB in 400 us).
 // float32: the matrix cores and the vector ALUs in turn, six products of parts for
 // one.  Few tokens: the two barriers and memory latency of each chunk, some 2.5 us.
 //
@@ -120,7 +121,8 @@ __device__ __forceinline__ void split8(float (&x)[8], uint4 (&out)[N]) {
 // 16 bytes at `off` of a bounded region, from column c of a row of n on: zero past
 // the row's columns, and past the region's end.  G: bytes that every row and its
 // width are a multiple of (16, 8 or an element).  ONCE: non-temporal, for tokens that
-// are read once (16 x 2048 tokens, 16 heads: 121.6 us against 126.9).
+// are read once (six rows of up to 1501 float32 tokens, 32 heads: 103 us against 108;
+// 16 x 2048 bfloat16 ones, 16 heads of 128: 150, 152; but 8 x 2000 of 32 x 32: 46, 42).
 template <int ACT, int G, bool ONCE>
 __device__ __forceinline__ uint4 load_piece(__amdgpu_buffer_rsrc_t region, uint32_t off, int c, int n) {
     constexpr int EB = Act<ACT>::kBytes, PER = 16 / EB;
@@ -295,8 +297,8 @@ void linattn_chunk_kernel(LinAttnArgs a, LinAttnPlan p) {
 
         // The state-only form goes through its segment backwards, values weighted to the
         // segment's end: the full form starts where it ended, on tokens that may still be
-        // in the Infinity Cache, and the state has no factor (65536 tokens, 16 heads: 363
-        // us, 370 forwards).
+        // in the Infinity Cache, and the state has no factor (65536 tokens, 16 heads: 2 to
+        // 4 % of the call).
         auto first_token = [&](int c) { return (int64_t)(FULL ? c : chunks - 1 - c) * C; };
 
         // tokens of a chunk, on their way
@@ -750,8 +752,9 @@ constexpr int short_bytes(int tokens, int dk, int tile) {
 // A prompt of at most so many tokens, all float32: the layout of one token's kernel
 // (LANES threads of V value columns a key row), the state read once, taken through
 // the tokens in registers and written once.  Bound by the state's way out, and past
-// some 8 tokens by the vector ALUs.  (37 x 4 heads of 256 x 256, 3 float32 tokens:
-// 12.7 us, 50.8 in chunks; 44 x 24 of 16 x 16, 8 bfloat16 ones: 14.3, 17.7 in chunks.)
+// some 8 tokens by the vector ALUs.  (Going on from a state, 37 x 4 heads of 256 x 256,
+// 4 float32 tokens: 18.9 us, 61.4 in chunks; 44 x 24 of 16 x 16, 8 bfloat16 ones: 14.9,
+// 20.3 in chunks.)
 template <int ACT, int LANES, int V, bool DECAY>
 __global__ __launch_bounds__(kThreads) void linattn_short_kernel(LinAttnArgs a, int vtiles) {
     using T = typename Act<ACT>::T;
@@ -960,11 +963,14 @@ LinAttnPlan linattn_plan(const LinAttnShape &s, int64_t L) {
     // Value columns of a workgroup and segments of the prompt: the least of rounds of
     // workgroups x chunks of one.
     //   One workgroup a CU; two of 64 columns and up to 32 bfloat16 keys, which leave room
-    //     (8 rows of 2000 tokens, 16 heads of 32 x 32: 49 us against 62).
-    //   64 columns take kNarrow of the time of 128 a chunk (77 tokens of 16 heads: 12.3 us
-    //     against 14.3).  128 are for more than 64 where the LDS holds two chunks of them
+    //     (8 rows of 2000 tokens, 16 heads of 32 x 32: 46 us against 59).
+    //   64 columns take kNarrow of the time of 128 a chunk (77 tokens of 16 heads: 14.3 us
+    //     against 16.4; of 17 shapes of both types, key widths of 32 to 256, this picks the
+    //     faster tile or one within 5 % at all but 8 x 700 tokens, 32 heads of 32 x 128:
+    //     44.6 us, 38 with 128 columns).  128 are for more than 64 where the LDS holds two chunks of them
     //     and the registers of three waves a SIMD the state.
-    //   Segments cost a second pass over k and v, kAgain of the full one.  (Cutting rows of
+    //   Segments cost a second pass over k and v, kAgain of the full one (0.4 takes the same
+    //     time at the 17 shapes).  (Cutting rows of
     //     their own lengths finer, for balance, did not pay: six rows of up to 1501 float32
     //     tokens, 32 heads: 152 us in four segments, 124 us whole.)
     constexpr double kNarrow = 0.75, kAgain = 0.6;
