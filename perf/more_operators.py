@@ -18,7 +18,7 @@ products and beam search:
               probabilities p, with given numbers u in [0, 1): x_i is kept while
               u_i q_i(x_i) < p_i(x_i); behind the last one kept comes a token
               drawn from max(p - q, 0) of that place (from p, behind all), the
-              first whose cumulated weight exceeds u times the whole.
+              first whose cumulated weight exceeds the last u times the whole.
 
 A case is a dict of sizes; `run` takes it through the plain form or, with
 ``own``, through this repository's entry points.
@@ -345,7 +345,7 @@ def _plain_verify(s, c):
         rest = torch.where(rest.sum(-1, keepdim=True) > 0, rest, weight)
         weight = torch.where((accepted < n)[:, None], rest, weight)
     whole = weight.cumsum(-1)
-    token = (whole > u[row, accepted].double()[:, None] * whole[:, -1:]).int().argmax(-1)
+    token = (whole > u[:, T:].double() * whole[:, -1:]).int().argmax(-1)
     place = torch.arange(T + 1, device=p.device)[None]
     tokens = torch.nn.functional.pad(drafted, (0, 1))
     tokens = torch.where(place < accepted[:, None], tokens, torch.where(place == accepted[:, None], token[:, None], -1))
@@ -505,7 +505,7 @@ def _exact_verify(s, c):
                 r[int(drafted[b, k])] = 0
             w = r if bool((r > 0).any()) else w
         sums = torch.cumsum(w, 0)
-        tokens[b, k] = int(torch.searchsorted(sums, u[b, k].to(sums.device) * sums[-1], right=True))
+        tokens[b, k] = int(torch.searchsorted(sums, u[b, T].to(sums.device) * sums[-1], right=True))
         counts[b] = k
     return tokens.to(DEVICE), counts.to(DEVICE)
 
