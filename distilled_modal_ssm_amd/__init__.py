@@ -11,4 +11,7 @@ from .binding import (HMError, LibraryMissing, ModalHyena, hm_desc, hyena_filter
                       hyena_modal_decode_step, hyena_modal_prefill, hyena_modal_prefill_workspace,
                       make_desc)
 from .beam import BeamSearch  # noqa: F401
+from .drafts import DraftVerify  # noqa: F401
+from .int8 import Int8Dense  # noqa: F401
 from .linear_attention import LinearAttention  # noqa: F401
+from .recurrence import GatedRecurrence  # noqa: F401

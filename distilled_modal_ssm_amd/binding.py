@@ -26,6 +26,13 @@ HM_OK, HM_ERR_INVALID_ARG, HM_ERR_UNSUPPORTED, HM_ERR_WORKSPACE, HM_ERR_HIP = ra
 HM_PREFILL_AUTO, HM_PREFILL_SCAN, HM_PREFILL_MFMA = 0, 1, 2
 HM_LINATTN_MAX_DIM = 256
 HM_BEAM_MAX = 64
+HM_GATE_LOG, HM_GATE_SIGMOID = 0, 1
+HM_GATE_INPUT_FREE, HM_GATE_INPUT_CONVEX, HM_GATE_INPUT_NORM = 0, 1, 2
+HM_RECURRENCE_CHUNK = 64
+HM_INT8_MAX_K = 131072
+HM_DRAFT_MAX = 63
+GATES = {"log": HM_GATE_LOG, "sigmoid": HM_GATE_SIGMOID}
+GATE_INPUTS = {"free": HM_GATE_INPUT_FREE, "convex": HM_GATE_INPUT_CONVEX, "norm": HM_GATE_INPUT_NORM}
 HM_NOALLOC_SCRATCH_BYTES = 16 << 20  # per-GPU scratch of hyena_modal_prefill_noalloc
 ALGOS = {"auto": HM_PREFILL_AUTO, "scan": HM_PREFILL_SCAN, "mfma": HM_PREFILL_MFMA}
 
@@ -68,6 +75,14 @@ EXPORTS = (
     "hyena_beam_select_workspace",
     "hyena_beam_select",
     "hyena_beam_reorder",
+    "hyena_recurrence_workspace",
+    "hyena_recurrence_prefill",
+    "hyena_recurrence_backward",
+    "hyena_recurrence_decode_step",
+    "hyena_quantize_rows",
+    "hyena_dense_int8",
+    "hyena_draft_verify_workspace",
+    "hyena_draft_verify",
 )
 
 
@@ -120,6 +135,17 @@ class hm_linattn_desc(ctypes.Structure):
     ]
 
 
+class hm_recurrence_desc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int64),
+        ("channels", ctypes.c_int64),
+        ("gate", ctypes.c_int32),
+        ("input", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -138,7 +164,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                 "(or __graft_entry__.build()); there is no CPU fallback")
         lib = ctypes.CDLL(path)
         i64, p, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
-        D, A = ctypes.POINTER(hm_desc), ctypes.POINTER(hm_linattn_desc)
+        D, A, R = ctypes.POINTER(hm_desc), ctypes.POINTER(hm_linattn_desc), ctypes.POINTER(hm_recurrence_desc)
+        i32 = ctypes.c_int32
         sig = {
             "hm_abi_version": ([], ctypes.c_int),
             "hm_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -187,6 +214,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "hyena_beam_select": ([i64, i64, i64, i64, ctypes.c_int32, p, i64, p, p, i64, p, p, p, p, p, sz, p],
                                   ctypes.c_int),
             "hyena_beam_reorder": ([i64, i64, p, i64, p, p, p], ctypes.c_int),
+            "hyena_recurrence_workspace": ([R, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_recurrence_prefill": ([R, i64, p, p, i64, p, i64, p, i64, p, i64, p, p, p, p, sz, p], ctypes.c_int),
+            "hyena_recurrence_backward": ([R, i64, p, p, i64, p, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, i64, p, p,
+                                           sz, p], ctypes.c_int),
+            "hyena_recurrence_decode_step": ([R, p, i64, p, i64, p, i64, p, i64, p, p, p, p], ctypes.c_int),
+            "hyena_quantize_rows": ([i64, i64, i32, p, i64, i32, f32, p, i64, p, p], ctypes.c_int),
+            "hyena_dense_int8": ([i64, i64, i64, p, i64, p, p, i64, p, i32, p, i64, p], ctypes.c_int),
+            "hyena_draft_verify_workspace": ([i64, i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_draft_verify": ([i64, i64, i64, i32, p, i64, p, i64, p, p, p, p, p, p, sz, p], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -546,6 +582,70 @@ def hyena_beam_reorder(groups, beams, parents, buffers, row_bytes, stream=None) 
     st = load().hyena_beam_reorder(groups, beams, _ptr(parents), n, (ctypes.c_void_p * n)(*[_ptr(b) for b in buffers]),
                                    (ctypes.c_int64 * n)(*row_bytes), _stream(stream))
     _check(st, "hyena_beam_reorder")
+
+
+# ----------------------------------------------------------------- gated recurrence, 8-bit products, drafts
+
+
+def make_recurrence_desc(batch, channels, act_dtype, gate=HM_GATE_SIGMOID, input=HM_GATE_INPUT_CONVEX) -> hm_recurrence_desc:
+    return hm_recurrence_desc(HM_ABI_VERSION, act_dtype, batch, channels, gate, input)
+
+
+def hyena_recurrence_workspace(desc: hm_recurrence_desc, L: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_recurrence_workspace(ctypes.byref(desc), L, ctypes.byref(n)), "hyena_recurrence_workspace")
+    return n.value
+
+
+def hyena_recurrence_prefill(desc: hm_recurrence_desc, L, lengths, q, ld_q, g, ld_g, v, ld_v, y, ld_y, state_in,
+                             state_out, chunk_states, workspace, ws_bytes=None, stream=None) -> None:
+    st = load().hyena_recurrence_prefill(ctypes.byref(desc), L, _ptr(lengths), _ptr(q), ld_q, _ptr(g), ld_g, _ptr(v),
+                                         ld_v, _ptr(y), ld_y, _ptr(state_in), _ptr(state_out), _ptr(chunk_states),
+                                         _ptr(workspace), _ws_bytes(workspace, ws_bytes), _stream(stream))
+    _check(st, "hyena_recurrence_prefill")
+
+
+def hyena_recurrence_backward(desc: hm_recurrence_desc, L, lengths, q, ld_q, g, ld_g, v, ld_v, dy, ld_dy, chunk_states,
+                              dstate_out, dq, ld_dq, dg, ld_dg, dv, ld_dv, dstate_in, workspace, ws_bytes=None,
+                              stream=None) -> None:
+    st = load().hyena_recurrence_backward(ctypes.byref(desc), L, _ptr(lengths), _ptr(q), ld_q, _ptr(g), ld_g, _ptr(v),
+                                          ld_v, _ptr(dy), ld_dy, _ptr(chunk_states), _ptr(dstate_out), _ptr(dq), ld_dq,
+                                          _ptr(dg), ld_dg, _ptr(dv), ld_dv, _ptr(dstate_in), _ptr(workspace),
+                                          _ws_bytes(workspace, ws_bytes), _stream(stream))
+    _check(st, "hyena_recurrence_backward")
+
+
+def hyena_recurrence_decode_step(desc: hm_recurrence_desc, q, ld_q, g, ld_g, v, ld_v, y, ld_y, state_in, src_rows,
+                                 state_out, stream=None) -> None:
+    st = load().hyena_recurrence_decode_step(ctypes.byref(desc), _ptr(q), ld_q, _ptr(g), ld_g, _ptr(v), ld_v, _ptr(y),
+                                             ld_y, _ptr(state_in), _ptr(src_rows), _ptr(state_out), _stream(stream))
+    _check(st, "hyena_recurrence_decode_step")
+
+
+def hyena_quantize_rows(M, K, dtype, x, ldx, rms, eps, q, ldq, scale, stream=None) -> None:
+    st = load().hyena_quantize_rows(M, K, dtype, _ptr(x), ldx, int(rms), eps, _ptr(q), ldq, _ptr(scale),
+                                    _stream(stream))
+    _check(st, "hyena_quantize_rows")
+
+
+def hyena_dense_int8(M, N, K, A, lda, a_scale, W, ldw, w_scale, dtype, C, ldc, stream=None) -> None:
+    st = load().hyena_dense_int8(M, N, K, _ptr(A), lda, _ptr(a_scale), _ptr(W), ldw, _ptr(w_scale), dtype, _ptr(C), ldc,
+                                 _stream(stream))
+    _check(st, "hyena_dense_int8")
+
+
+def hyena_draft_verify_workspace(batch: int, drafts: int, vocab: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_draft_verify_workspace(batch, drafts, vocab, ctypes.byref(n)), "hyena_draft_verify_workspace")
+    return n.value
+
+
+def hyena_draft_verify(batch, drafts, vocab, dtype, p, ld_p, q, ld_q, tokens, lengths, u, out_tokens, out_accepted,
+                       workspace, ws_bytes=None, stream=None) -> None:
+    st = load().hyena_draft_verify(batch, drafts, vocab, dtype, _ptr(p), ld_p, _ptr(q), ld_q, _ptr(tokens),
+                                   _ptr(lengths), _ptr(u), _ptr(out_tokens), _ptr(out_accepted), _ptr(workspace),
+                                   _ws_bytes(workspace, ws_bytes), _stream(stream))
+    _check(st, "hyena_draft_verify")
 
 
 # ----------------------------------------------------------------- tensor helpers

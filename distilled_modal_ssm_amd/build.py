@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhyena_modal.so")
 
 SOURCES = ["hm_api.cpp", "decode.hip", "filter.hip", "prefill.hip", "prefill_mfma.hip", "dense.hip", "fir.hip", "fft.hip", "distill.hip",
-           "gen_step.hip", "modal_fit.cpp", "linattn.hip", "beam.hip"]
+           "gen_step.hip", "modal_fit.cpp", "linattn.hip", "beam.hip", "recurrence.hip", "int8.hip", "drafts.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -35,13 +35,14 @@ FLAGS = [
 # argument segment (gfx950 kernarg preloading; the code keeps a prologue that
 # loads them for firmware without it).
 #
-# No kernel of linear attention or beam search may use stack memory: the compiler
+# No kernel of the generation operators may use stack memory: the compiler
 # has been seen to save a vector register there where only some lanes were active
 # and to reload it where all were (a wrong address in a final store).  A kernel
 # that needs more registers than it has is an error, not a slow kernel.
 NO_STACK = ["-Xarch_device", "-Wframe-larger-than=0", "-Xarch_device", "-Werror=frame-larger-than"]
 SOURCE_FLAGS = {"decode.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=9"],
-                "linattn.hip": NO_STACK, "beam.hip": NO_STACK}
+                "linattn.hip": NO_STACK, "beam.hip": NO_STACK, "recurrence.hip": NO_STACK, "int8.hip": NO_STACK,
+                "drafts.hip": NO_STACK}
 
 
 def _compile(src: str) -> str:

@@ -971,4 +971,243 @@ hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *paren
                : HM_ERR_HIP;
 }
 
+static hm_status check_recurrence(const hm_recurrence_desc *d) {
+    if (!d || d->abi_version != HM_ABI_VERSION) return HM_ERR_INVALID_ARG;
+    if (d->act_dtype != HM_F32 && d->act_dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (d->batch < 0 || d->channels < 1) return HM_ERR_INVALID_ARG;
+    if (d->gate != HM_GATE_LOG && d->gate != HM_GATE_SIGMOID) return HM_ERR_INVALID_ARG;
+    if (d->input != HM_GATE_INPUT_FREE && d->input != HM_GATE_INPUT_CONVEX && d->input != HM_GATE_INPUT_NORM)
+        return HM_ERR_INVALID_ARG;
+    if (d->batch > kMaxElems / d->channels) return HM_ERR_INVALID_ARG;
+    return HM_OK;
+}
+
+// Rows of activations of `rows` tokens: pointer, alignment, stride and extent.
+static hm_status check_rows(const void *p, int64_t ld, int64_t width, int64_t rows, uintptr_t e) {
+    if (!p || ld < width) return HM_ERR_INVALID_ARG;
+    if (!aligned(p, e)) return HM_ERR_UNSUPPORTED;
+    return rows > kMaxElems / ld ? HM_ERR_INVALID_ARG : HM_OK;
+}
+
+// Sizes of a call over L tokens, and its inputs' rows.
+static hm_status recurrence_args(const hm_recurrence_desc *d, int64_t L, const void *q, int64_t ld_q, const void *g,
+                                 int64_t ld_g, const void *v, int64_t ld_v, hm::RecurArgs *a) {
+    const uintptr_t e = d->act_dtype == HM_BF16 ? 2 : 4;
+    if (L > 0) {
+        const int64_t rows = kMaxElems / L >= d->batch ? d->batch * L : kMaxElems;
+        hm_status st;
+        if ((q && (st = check_rows(q, ld_q, d->channels, rows, e)) != HM_OK) ||
+            (st = check_rows(g, ld_g, d->channels, rows, e)) != HM_OK ||
+            (st = check_rows(v, ld_v, d->channels, rows, e)) != HM_OK)
+            return st;
+    }
+    *a = hm::RecurArgs{};
+    a->B = d->batch;
+    a->D = d->channels;
+    a->L = L;
+    a->act = d->act_dtype == HM_BF16 ? hm::kBF16 : hm::kF32;
+    a->gate = d->gate == HM_GATE_LOG ? hm::kGateLog : hm::kGateSigmoid;
+    a->input = d->input == HM_GATE_INPUT_FREE     ? hm::kInputFree
+               : d->input == HM_GATE_INPUT_CONVEX ? hm::kInputConvex
+                                                  : hm::kInputNorm;
+    a->q = q;
+    a->g = g;
+    a->v = v;
+    a->ld_q = ld_q;
+    a->ld_g = ld_g;
+    a->ld_v = ld_v;
+    return HM_OK;
+}
+
+// Workgroups of a launch: fewer than 2^32 threads of at most 512 each.
+constexpr int64_t kMostGroups = int64_t(1) << 23;
+
+static hm_status check_recurrence_length(const hm_recurrence_desc *d, int64_t L) {
+    if (L < 0) return HM_ERR_INVALID_ARG;
+    if (L > INT32_MAX / 2) return HM_ERR_UNSUPPORTED;
+    const int64_t tiles = (d->channels + 63) / 64, chunks = L > 0 ? (L + 127) / 128 : 1;
+    if (d->batch > 0 && (tiles >= kMostGroups || chunks >= kMostGroups || tiles * chunks >= kMostGroups ||
+                         d->batch >= (kMostGroups + tiles * chunks - 1) / (tiles * chunks)))
+        return HM_ERR_UNSUPPORTED;
+    return HM_OK;
+}
+
+static hm_status check_workspace(const void *workspace, size_t ws_bytes, size_t need) {
+    if (need == 0) return HM_OK;
+    if (!workspace || ws_bytes < need) return HM_ERR_WORKSPACE;
+    return aligned(workspace, 256) ? HM_OK : HM_ERR_UNSUPPORTED;
+}
+
+hm_status hyena_recurrence_workspace(const hm_recurrence_desc *desc, int64_t L, size_t *bytes) {
+    hm_status st = check_recurrence(desc);
+    if (st != HM_OK) return st;
+    if (!bytes) return HM_ERR_INVALID_ARG;
+    if ((st = check_recurrence_length(desc, L)) != HM_OK) return st;
+    *bytes = desc->batch > 0 ? hm::recurrence_workspace(desc->batch, desc->channels, L) : 0;
+    return HM_OK;
+}
+
+hm_status hyena_recurrence_prefill(const hm_recurrence_desc *desc, int64_t L, const int32_t *lengths, const void *q,
+                                   int64_t ld_q, const void *g, int64_t ld_g, const void *v, int64_t ld_v, void *y,
+                                   int64_t ld_y, const float *state_in, float *state_out, float *chunk_states,
+                                   void *workspace, size_t ws_bytes, void *stream) {
+    hm_status st = check_recurrence(desc);
+    if (st != HM_OK) return st;
+    if ((st = check_recurrence_length(desc, L)) != HM_OK) return st;
+    if (desc->batch == 0) return HM_OK;
+    hm::RecurArgs a;
+    if ((st = recurrence_args(desc, L, q, ld_q, g, ld_g, v, ld_v, &a)) != HM_OK) return st;
+    if (L > 0 && (st = check_rows(y, ld_y, desc->channels, desc->batch * L, desc->act_dtype == HM_BF16 ? 2 : 4)) != HM_OK)
+        return st;
+    if (!state_out) return HM_ERR_INVALID_ARG;
+    if (!aligned(state_out, 4) || !aligned(state_in, 4) || !aligned(chunk_states, 4) || !aligned(lengths, 4))
+        return HM_ERR_UNSUPPORTED;
+    if ((st = check_workspace(workspace, ws_bytes, hm::recurrence_workspace(a.B, a.D, L))) != HM_OK) return st;
+    a.lengths = lengths;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.chunk_states = chunk_states;
+    a.ws = static_cast<unsigned char *>(workspace);
+    return hm::launch_recurrence_prefill(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_recurrence_backward(const hm_recurrence_desc *desc, int64_t L, const int32_t *lengths, const void *q,
+                                    int64_t ld_q, const void *g, int64_t ld_g, const void *v, int64_t ld_v,
+                                    const void *dy, int64_t ld_dy, const float *chunk_states, const float *dstate_out,
+                                    void *dq, int64_t ld_dq, void *dg, int64_t ld_dg, void *dv, int64_t ld_dv,
+                                    float *dstate_in, void *workspace, size_t ws_bytes, void *stream) {
+    hm_status st = check_recurrence(desc);
+    if (st != HM_OK) return st;
+    if ((st = check_recurrence_length(desc, L)) != HM_OK) return st;
+    if (desc->batch == 0) return HM_OK;
+    hm::RecurArgs a;
+    if ((st = recurrence_args(desc, L, q, ld_q, g, ld_g, v, ld_v, &a)) != HM_OK) return st;
+    if ((q == nullptr) != (dq == nullptr)) return HM_ERR_INVALID_ARG;
+    if (L > 0) {
+        const uintptr_t e = desc->act_dtype == HM_BF16 ? 2 : 4;
+        const int64_t rows = desc->batch * L;
+        if ((st = check_rows(dy, ld_dy, desc->channels, rows, e)) != HM_OK ||
+            (dq && (st = check_rows(dq, ld_dq, desc->channels, rows, e)) != HM_OK) ||
+            (st = check_rows(dg, ld_dg, desc->channels, rows, e)) != HM_OK ||
+            (st = check_rows(dv, ld_dv, desc->channels, rows, e)) != HM_OK)
+            return st;
+        if (!chunk_states) return HM_ERR_INVALID_ARG;
+    }
+    if (!aligned(chunk_states, 4) || !aligned(dstate_out, 4) || !aligned(dstate_in, 4) || !aligned(lengths, 4))
+        return HM_ERR_UNSUPPORTED;
+    if ((st = check_workspace(workspace, ws_bytes, hm::recurrence_workspace(a.B, a.D, L))) != HM_OK) return st;
+    a.lengths = lengths;
+    a.dy = dy;
+    a.ld_dy = ld_dy;
+    a.chunk_states = const_cast<float *>(chunk_states);
+    a.dstate_out = dstate_out;
+    a.dq = dq;
+    a.dg = dg;
+    a.dv = dv;
+    a.ld_dq = ld_dq;
+    a.ld_dg = ld_dg;
+    a.ld_dv = ld_dv;
+    a.dstate_in = dstate_in;
+    a.ws = static_cast<unsigned char *>(workspace);
+    return hm::launch_recurrence_backward(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_recurrence_decode_step(const hm_recurrence_desc *desc, const void *q, int64_t ld_q, const void *g,
+                                       int64_t ld_g, const void *v, int64_t ld_v, void *y, int64_t ld_y,
+                                       const float *state_in, const int32_t *src_rows, float *state_out,
+                                       void *stream) {
+    hm_status st = check_recurrence(desc);
+    if (st != HM_OK) return st;
+    if (desc->batch == 0) return HM_OK;
+    hm::RecurArgs a;
+    if ((st = recurrence_args(desc, 1, q, ld_q, g, ld_g, v, ld_v, &a)) != HM_OK) return st;
+    if ((st = check_rows(y, ld_y, desc->channels, desc->batch, desc->act_dtype == HM_BF16 ? 2 : 4)) != HM_OK) return st;
+    if (!state_in || !state_out) return HM_ERR_INVALID_ARG;
+    if (!aligned(state_in, 4) || !aligned(state_out, 4) || !aligned(src_rows, 4)) return HM_ERR_UNSUPPORTED;
+    if (src_rows && state_in == state_out) return HM_ERR_INVALID_ARG;
+    const int64_t tiles = (desc->channels + 255) / 256;
+    if (desc->batch >= (kMostGroups + tiles - 1) / tiles) return HM_ERR_UNSUPPORTED;
+    a.y = y;
+    a.ld_y = ld_y;
+    a.state_in = state_in;
+    a.src_rows = src_rows;
+    a.state_out = state_out;
+    return hm::launch_recurrence_decode(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps,
+                              int8_t *q, int64_t ldq, float *scale, void *stream) {
+    if (M < 0 || K < 1) return HM_ERR_INVALID_ARG;
+    if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (rms && !(std::isfinite(eps) && eps >= 0.0f)) return HM_ERR_INVALID_ARG;
+    if (K > HM_INT8_MAX_K || M > INT32_MAX) return HM_ERR_UNSUPPORTED;
+    if (ldx < K || ldq < K) return HM_ERR_INVALID_ARG;
+    if (ldq % 64 != 0) return HM_ERR_UNSUPPORTED;
+    if (M == 0) return HM_OK;
+    if (!x || !q || !scale) return HM_ERR_INVALID_ARG;
+    if (!aligned(x, dtype == HM_BF16 ? 2 : 4) || !aligned(q, 16) || !aligned(scale, 4)) return HM_ERR_UNSUPPORTED;
+    if (M > kMaxElems / ldx || M > kMaxElems / ldq) return HM_ERR_INVALID_ARG;
+    const hm::QuantArgs a{M, K, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, ldq, scale};
+    return hm::launch_quantize_rows(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *a_scale,
+                           const int8_t *W, int64_t ldw, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
+                           void *stream) {
+    if (M < 0 || N < 0 || K < 1) return HM_ERR_INVALID_ARG;
+    if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (K > HM_INT8_MAX_K || M >= INT32_MAX - 511 || N >= INT32_MAX - 511) return HM_ERR_UNSUPPORTED;
+    if (lda < K || ldw < K || ldc < N) return HM_ERR_INVALID_ARG;
+    if (lda % 64 != 0 || ldw % 64 != 0) return HM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return HM_OK;
+    if ((M + 15) / 16 > INT32_MAX / ((N + 15) / 16)) return HM_ERR_UNSUPPORTED;
+    if (!A || !a_scale || !W || !w_scale || !C) return HM_ERR_INVALID_ARG;
+    if (!aligned(A, 16) || !aligned(W, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(C, dtype == HM_BF16 ? 2 : 4))
+        return HM_ERR_UNSUPPORTED;
+    if (M > kMaxElems / lda || N > kMaxElems / ldw || M > kMaxElems / ldc) return HM_ERR_INVALID_ARG;
+    const hm::Int8GemmArgs a{M, N, K, A, lda, a_scale, W, ldw, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
+    return hm::launch_dense_int8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+static hm_status check_drafts(int64_t batch, int64_t drafts, int64_t vocab) {
+    if (batch < 0 || drafts < 0 || drafts > HM_DRAFT_MAX || vocab < 1) return HM_ERR_INVALID_ARG;
+    if (vocab > INT32_MAX - (1 << 14)) return HM_ERR_UNSUPPORTED;
+    const int64_t parts = (vocab + 1023) / 1024;
+    return batch >= (kMostGroups + parts - 1) / parts ? HM_ERR_UNSUPPORTED : HM_OK;
+}
+
+hm_status hyena_draft_verify_workspace(int64_t batch, int64_t drafts, int64_t vocab, size_t *bytes) {
+    const hm_status st = check_drafts(batch, drafts, vocab);
+    if (st != HM_OK) return st;
+    if (!bytes) return HM_ERR_INVALID_ARG;
+    *bytes = batch > 0 ? hm::draft_verify_workspace(batch, vocab) : 0;
+    return HM_OK;
+}
+
+hm_status hyena_draft_verify(int64_t batch, int64_t drafts, int64_t vocab, int32_t dtype, const void *p, int64_t ld_p,
+                             const void *q, int64_t ld_q, const int32_t *tokens, const int32_t *lengths, const float *u,
+                             int32_t *out_tokens, int32_t *out_accepted, void *workspace, size_t ws_bytes,
+                             void *stream) {
+    hm_status st = check_drafts(batch, drafts, vocab);
+    if (st != HM_OK) return st;
+    if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    const uintptr_t e = dtype == HM_BF16 ? 2 : 4;
+    if (batch == 0) return HM_OK;
+    if ((st = check_rows(p, ld_p, vocab, batch * (drafts + 1), e)) != HM_OK) return st;
+    if (q && drafts > 0 && (st = check_rows(q, ld_q, vocab, batch * drafts, e)) != HM_OK) return st;
+    if ((drafts > 0 && !tokens) || !u || !out_tokens || !out_accepted) return HM_ERR_INVALID_ARG;
+    if (!aligned(tokens, 4) || !aligned(lengths, 4) || !aligned(u, 4) || !aligned(out_tokens, 4) ||
+        !aligned(out_accepted, 4))
+        return HM_ERR_UNSUPPORTED;
+    if ((st = check_workspace(workspace, ws_bytes, hm::draft_verify_workspace(batch, vocab))) != HM_OK) return st;
+    const hm::VerifyArgs a{batch,  (int)drafts, vocab, dtype == HM_BF16 ? hm::kBF16 : hm::kF32,
+                           p,      ld_p,        q,     ld_q,
+                           tokens, lengths,     u,     out_tokens,
+                           out_accepted, static_cast<unsigned char *>(workspace)};
+    return hm::launch_draft_verify(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
 }  // extern "C"

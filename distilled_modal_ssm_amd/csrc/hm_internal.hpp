@@ -385,6 +385,81 @@ hipError_t launch_beam_select(const BeamSelectArgs &a, hipStream_t stream);
 hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n, void *const *buffers,
                                const int64_t *row_bytes, hipStream_t stream);
 
+// Gated recurrence.
+enum RecurGate : int { kGateLog = 0, kGateSigmoid = 1 };
+enum RecurInput : int { kInputFree = 0, kInputConvex = 1, kInputNorm = 2 };
+constexpr int kRecurChunk = 64;  // tokens between two kept states
+struct RecurArgs {
+    int64_t B, D, L;
+    int act, gate, input;
+    const int32_t *lengths;  // nullable
+    const void *q, *g, *v;   // q nullable
+    int64_t ld_q, ld_g, ld_v;
+    void *y;
+    int64_t ld_y;
+    const float *state_in;   // nullable for a prompt
+    float *state_out;
+    float *chunk_states;     // [B][ceil(L / kRecurChunk)][D]; nullable for a prompt
+    const int32_t *src_rows; // nullable; one token only
+    // backward only
+    const void *dy;
+    int64_t ld_dy;
+    const float *dstate_out; // nullable
+    void *dq, *dg, *dv;      // dq null where q is
+    int64_t ld_dq, ld_dg, ld_dv;
+    float *dstate_in;        // nullable
+    unsigned char *ws;
+};
+size_t recurrence_workspace(int64_t B, int64_t D, int64_t L);
+hipError_t launch_recurrence_prefill(const RecurArgs &a, hipStream_t stream);
+hipError_t launch_recurrence_backward(const RecurArgs &a, hipStream_t stream);
+hipError_t launch_recurrence_decode(const RecurArgs &a, hipStream_t stream);
+
+// Products in 8-bit integers.
+struct QuantArgs {
+    int64_t M, K;
+    int act;
+    const void *x;
+    int64_t ldx;
+    bool rms;
+    float eps;
+    int8_t *q;
+    int64_t ldq;
+    float *scale;
+};
+struct Int8GemmArgs {
+    int64_t M, N, K;
+    const int8_t *A;
+    int64_t lda;
+    const float *a_scale;
+    const int8_t *W;
+    int64_t ldw;
+    const float *w_scale;
+    int act;
+    void *C;
+    int64_t ldc;
+};
+hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream);
+hipError_t launch_dense_int8(const Int8GemmArgs &a, hipStream_t stream);
+
+// Verification of drafted tokens.
+struct VerifyArgs {
+    int64_t B;
+    int T;
+    int64_t V;
+    int act;
+    const void *p;
+    int64_t ld_p;
+    const void *q;  // nullable
+    int64_t ld_q;
+    const int32_t *tokens, *lengths;  // lengths nullable
+    const float *u;
+    int32_t *out_tokens, *out_accepted;
+    unsigned char *ws;
+};
+size_t draft_verify_workspace(int64_t B, int64_t V);
+hipError_t launch_draft_verify(const VerifyArgs &a, hipStream_t stream);
+
 // ---------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error; none synchronises.
 

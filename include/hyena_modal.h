@@ -670,6 +670,176 @@ hm_status hyena_beam_select(int64_t groups, int64_t beams, int64_t vocab, int64_
 hm_status hyena_beam_reorder(int64_t groups, int64_t beams, const int32_t *parents, int64_t n,
                              void *const *buffers, const int64_t *row_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated recurrence: a layer whose state is one number a channel, kept or replaced
+ * as each token's gate says (the hybrid stacks of the pages' surveys keep such
+ * layers beside convolutions; StripedHyena article, Hyena層次結構, for the gate
+ * y = q * (...) behind it).  Per batch row and channel:
+ *     h_t = f_t h_{t-1} + i_t v_t,      y_t = q_t h_t      (y_t = h_t without q)
+ * with f and i from the gate g_t.
+ * ------------------------------------------------------------------------ */
+
+typedef enum hm_gate {
+    HM_GATE_LOG = 0,     /* f = exp(g); g <= 0 is expected, -infinity forgets the state */
+    HM_GATE_SIGMOID = 1, /* f = 1 / (1 + exp(-g)) */
+    /* an f below 2^-126 (float32's smallest normal number) counts as 0 */
+} hm_gate;
+
+typedef enum hm_gate_input {
+    HM_GATE_INPUT_FREE = 0,   /* i = 1 */
+    HM_GATE_INPUT_CONVEX = 1, /* i = 1 - f */
+    HM_GATE_INPUT_NORM = 2,   /* i = sqrt(1 - f^2); 0 where f > 1 */
+} hm_gate_input;
+
+typedef struct hm_recurrence_desc {
+    int32_t abi_version; /* must be HM_ABI_VERSION */
+    int32_t act_dtype;   /* hm_dtype of q, g, v, y and of their gradients */
+    int64_t batch;       /* >= 0 */
+    int64_t channels;    /* >= 1 */
+    int32_t gate;        /* hm_gate */
+    int32_t input;       /* hm_gate_input */
+} hm_recurrence_desc;
+
+#define HM_RECURRENCE_CHUNK 64 /* tokens between two of the states that a prompt keeps for its backward pass */
+
+/* Workspace bytes of hyena_recurrence_prefill and hyena_recurrence_backward for
+ * this descriptor and length L >= 0 (0 is possible).  Pure host computation. */
+hm_status hyena_recurrence_workspace(const hm_recurrence_desc *desc, int64_t L, size_t *bytes);
+
+/*
+ * The recurrence over L tokens, and the state after them.
+ *   lengths   [batch] int32 or NULL (every row has L tokens).  Row b's tokens
+ *             from lengths[b] on are not read, do not move the state, and get
+ *             y = 0.  A value outside 0 .. L counts as the nearer of the two.
+ *   q         [batch][L][ld_q] or NULL (y = h); g, v, y alike with their own ld.
+ *   state_in  [batch][channels] float32, or NULL for zero.
+ *   state_out the state after each row's last token (may equal state_in).
+ *   chunk_states  NULL, or [batch][ceil(L / HM_RECURRENCE_CHUNK)][channels]
+ *             float32: the state before every chunk, for the backward pass
+ *             (rows' chunks past their end are left as they are).
+ *   workspace 256-byte aligned scratch, hyena_recurrence_workspace bytes.
+ * The state is float32.  A value that is not finite makes the h after it in its
+ * row and channel not finite (NaN where the recurrence may have an infinity,
+ * behind a gate of 0 too); never other rows or channels.  Apart from state_in,
+ * outputs must not overlap inputs.  Results do not depend on timing.
+ * L < 2^30, and batch * ceil(channels / 64) * ceil(L / 128) < 2^23 (else
+ * HM_ERR_UNSUPPORTED).
+ */
+hm_status hyena_recurrence_prefill(const hm_recurrence_desc *desc, int64_t L, const int32_t *lengths,
+                                   const void *q, int64_t ld_q, const void *g, int64_t ld_g,
+                                   const void *v, int64_t ld_v, void *y, int64_t ld_y,
+                                   const float *state_in, float *state_out, float *chunk_states,
+                                   void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of the prompt form, of its y (dy) and of its state_out:
+ *     dh_t = q_t dy_t + f_{t+1} dh_{t+1},
+ *     dq_t = dy_t h_t,  dv_t = i_t dh_t,  dg_t = dh_t (f'_t h_{t-1} + i'_t v_t).
+ *   q, g, v, lengths, chunk_states  as the prompt had and left them.
+ *   dy        [batch][L][ld_dy] of the activation type.
+ *   dstate_out  [batch][channels] float32, the gradient of state_out, or NULL for 0.
+ *   dq        NULL exactly where q is; dq, dg, dv of the activation type, 0
+ *             past a row's end.
+ *   dstate_in [batch][channels] float32, or NULL: the gradient of state_in
+ *             (may equal dstate_out).
+ * Where i = 0 (sqrt's border) the gradient through i counts as 0.  h is formed
+ * again from the inputs, so y's rounding does not enter.  Else as above.
+ */
+hm_status hyena_recurrence_backward(const hm_recurrence_desc *desc, int64_t L, const int32_t *lengths,
+                                    const void *q, int64_t ld_q, const void *g, int64_t ld_g,
+                                    const void *v, int64_t ld_v, const void *dy, int64_t ld_dy,
+                                    const float *chunk_states, const float *dstate_out,
+                                    void *dq, int64_t ld_dq, void *dg, int64_t ld_dg,
+                                    void *dv, int64_t ld_dv, float *dstate_in,
+                                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * One generated token for every batch row.  q [batch][ld_q] or NULL, g, v, y
+ * alike; state_in, src_rows, state_out as in hyena_linattn_decode_step.
+ * batch * ceil(channels / 256) < 2^23 (else HM_ERR_UNSUPPORTED).
+ */
+hm_status hyena_recurrence_decode_step(const hm_recurrence_desc *desc, const void *q, int64_t ld_q,
+                                       const void *g, int64_t ld_g, const void *v, int64_t ld_v,
+                                       void *y, int64_t ld_y, const float *state_in,
+                                       const int32_t *src_rows, float *state_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Products in 8-bit integers, beside the bfloat16 ones above: half the bytes of
+ * the weights a generated token reads, and twice the matrix cores' rate.
+ * ------------------------------------------------------------------------ */
+
+#define HM_INT8_MAX_K 131072 /* most inputs: sums of products stay below 2^31 */
+
+/*
+ * Rows in 8-bit integers, each with a scale of its own:
+ *     amax = max_k |x[m][k]|,  q[m][k] = rint(127 x[m][k] / amax) (ties to even),
+ *     scale[m] = amax / 127,  or with rms != 0  amax / 127 / sqrt(mean_k x^2 + eps).
+ * The integers are those of the exact quotient.  A row of zeros gets zeros and
+ * scale 0; a row with a value that is not finite gets zeros and scale NaN.
+ *   x [M][ldx] of dtype (hm_dtype), K columns;  q [M][ldq] bytes, columns K up to
+ *   the next multiple of 64 are set to 0 (the products read them);  scale [M].
+ * Tokens (rows of activations) and output channels (rows of W) alike.
+ * 1 <= K <= HM_INT8_MAX_K, ldq a multiple of 64, q 16-byte aligned, M < 2^31
+ * (else HM_ERR_UNSUPPORTED).
+ */
+hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx,
+                              int32_t rms, float eps, int8_t *q, int64_t ldq, float *scale,
+                              void *stream);
+
+/*
+ *     C[m][n] = a_scale[m] w_scale[n] sum_k A[m][k] W[n][k],
+ * the sum exact in 32-bit integers, C of dtype (hm_dtype) rounded once from
+ * float32.  A [M][lda] and W [N][ldw] bytes as hyena_quantize_rows writes them:
+ * lda, ldw multiples of 64, 16-byte aligned, zeros (in one of the two) from K to
+ * the next multiple of 64 (else HM_ERR_UNSUPPORTED for what can be checked).
+ * C [M][ldc].  K <= HM_INT8_MAX_K; M, N < 2^31 - 2^9, and
+ * ceil(M / 16) * ceil(N / 16) < 2^31 (else HM_ERR_UNSUPPORTED).
+ */
+hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
+                           const float *a_scale, const int8_t *W, int64_t ldw, const float *w_scale,
+                           int32_t dtype, void *C, int64_t ldc, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens: a small model drafts a few tokens, the target
+ * model reads them all at once, and what is kept of them and drawn behind them
+ * is distributed as the target's own tokens would be.
+ * ------------------------------------------------------------------------ */
+
+#define HM_DRAFT_MAX 63 /* most drafted tokens of a sequence */
+
+/*
+ * For every sequence, of its n drafted tokens x_0 .. x_{n-1}, the longest run
+ * from the first with
+ *     u_i q_i(x_i) < p_i(x_i),
+ * then one more token, at the place a behind that run: drawn from
+ * max(p_a - q_a, 0) where a draft was refused there, from p_a where none was
+ * left, as the first token whose cumulated weight exceeds u_drafts times the
+ * whole (a number of its own: a refused draft's u_a is no longer spread evenly).
+ *   p         [batch][drafts + 1][ld_p] of dtype (hm_dtype): the target's
+ *             probabilities at each place, vocab columns used.
+ *   q         [batch][drafts][ld_q]: the drafting model's; or NULL where it
+ *             drafts without chance (q_i(x_i) = 1, all else 0).
+ *   tokens    [batch][drafts] int32.  One outside 0 .. vocab-1 is refused.
+ *   lengths   [batch] int32 or NULL (all of them): drafted tokens of each
+ *             sequence; a value outside 0 .. drafts counts as the nearer.
+ *   u         [batch][drafts + 1] float32 in [0, 1): one a draft, and the last one
+ *             for the drawn token, wherever it comes.
+ *   out_tokens    [batch][drafts + 1] int32: the kept drafts, the drawn token, then -1.
+ *   out_accepted  [batch] int32: drafts kept.
+ * Probabilities that are NaN, negative or infinite count as 0.  Weights are
+ * compared and summed in float64.  Where max(p - q, 0) is 0 all over, the token
+ * is drawn from p; where p is, it is -1.  drafts = 0 draws one token a sequence.
+ * 0 <= drafts <= HM_DRAFT_MAX (else HM_ERR_INVALID_ARG); vocab < 2^31 - 2^14 and
+ * batch * ceil(vocab / 1024) < 2^23 (else HM_ERR_UNSUPPORTED).  workspace:
+ * hyena_draft_verify_workspace bytes, 256-byte aligned, scratch.
+ */
+hm_status hyena_draft_verify_workspace(int64_t batch, int64_t drafts, int64_t vocab, size_t *bytes);
+
+hm_status hyena_draft_verify(int64_t batch, int64_t drafts, int64_t vocab, int32_t dtype, const void *p,
+                             int64_t ld_p, const void *q, int64_t ld_q, const int32_t *tokens,
+                             const int32_t *lengths, const float *u, int32_t *out_tokens,
+                             int32_t *out_accepted, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

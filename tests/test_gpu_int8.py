@@ -1,0 +1,163 @@
+"""8-bit products against exact integers.
+
+The integers of a row are those of 127 x / amax rounded to the nearest, ties to even:
+float64 decides every case (127 x has at most 31 bits, and a quotient of 24-bit
+numbers below 128 is on a border or at least 2^-32 away from it), so they are compared
+for equality.  Sums are exact; y is the sum as float32, times two scales: 2^-24 each
+for the sum, the two products and the two scales, 5 in all, and where rows are scaled
+by their root mean square the mean (K / 256 + 10 additions of squares, half of whose
+error a root passes on), the root, the quotient and one more: K / 256 + 20 at most.
+A bfloat16 y is rounded once more, 2^-8 of itself.
+"""
+
+import numpy as np
+import pytest
+
+from _gpu_common import log, require_gpu
+from distilled_modal_ssm_amd import HMError, Int8Dense
+from distilled_modal_ssm_amd import binding as hb
+
+pytestmark = pytest.mark.gpu
+
+
+def quantized64(x):
+    amax = abs(x).max(-1, keepdims=True)
+    return np.rint(x * 127 / np.where(amax > 0, amax, 1)), amax[:, 0] / 127
+
+
+def _quantize(torch, x, rms_eps=None, ldq=None):
+    M, K = x.shape
+    ldq = ldq or -(-K // 64) * 64
+    q = torch.full((M, ldq), 99, dtype=torch.int8, device="cuda")
+    s = torch.empty(M, device="cuda")
+    hb.hyena_quantize_rows(M, K, hb.HM_BF16 if x.dtype == torch.bfloat16 else hb.HM_F32, x, x.stride(0),
+                           rms_eps is not None, rms_eps or 0.0, q, ldq, s)
+    return q, s
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,pad", [(1, 1, 0), (3, 64, 0), (5, 515, 0), (2, 2048, 8), (300, 100, 3), (1, 20000, 1),
+                                     (7, 8191, 0), (1, 131072, 0)])
+def test_rows(act, M, K, pad):
+    torch = require_gpu()
+    log(f"rows {act} {M} {K} {pad}")
+    g = torch.Generator().manual_seed(M + K)
+    x = (torch.randn(M, K + pad, generator=g) * torch.exp(3 * torch.randn(M, 1, generator=g)))
+    x = x.to(torch.bfloat16 if act == "bf16" else torch.float32).cuda()[:, :K]
+    ref, scale = quantized64(x.double().cpu().numpy())
+    for eps in (None, 1e-6):
+        q, s = _quantize(torch, x, eps)
+        assert (q[:, :K].cpu().numpy() == ref).all()
+        assert (q[:, K:(K + 63) // 64 * 64] == 0).all()
+        want = scale
+        if eps is not None:
+            want = scale / np.sqrt((x.double().cpu().numpy() ** 2).mean(-1) + eps)
+        assert (abs(s.cpu().numpy() - want) <= (2 if eps is None else K / 256 + 18) * 2.0 ** -24 * want).all()
+
+
+def test_rows_at_borders():
+    """Ties, values next to them, the smallest and largest numbers, rows of zeros and rows that are not finite."""
+    torch = require_gpu()
+    log("borders")
+    n = torch.arange(-127, 127, dtype=torch.float32)
+    ties = torch.cat([n + 0.5, torch.tensor([127.0])])
+    up = torch.nextafter(ties, torch.full_like(ties, 1e9)).clamp(-127, 127)
+    down = torch.nextafter(ties, torch.full_like(ties, -1e9))
+    down[-1] = 127.0
+    third = ties / 3.0
+    rows = torch.stack([ties, up, down, third, ties * 2.0 ** -140, ties * 2.0 ** 120, ties * 1e-30, ties * 0.0])
+    x = rows.cuda()
+    q, s = _quantize(torch, x)
+    ref, scale = quantized64(x.double().cpu().numpy())
+    assert (q[:, :255].cpu().numpy() == ref).all()
+    assert (abs(s.cpu().numpy() - scale) <= 2.0 ** -24 * scale + 2.0 ** -150).all()
+    assert float(s[7]) == 0 and not q[7].any()
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(3, 700, generator=g)
+    x[0, 3], x[1, 600], x[1, 2] = float("nan"), float("inf"), -float("inf")
+    q, s = _quantize(torch, x.cuda(), 1e-6)
+    assert torch.isnan(s[:2]).all() and not q[:2].any() and torch.isfinite(s[2])
+    y = Int8Dense(torch.randn(40, 700, generator=g).cuda())(x.cuda())
+    assert torch.isnan(y[:2]).all() and torch.isfinite(y[2]).all()
+
+
+SHAPES = [(1, 1, 1), (1, 17, 64), (5, 6144, 2048), (3, 33, 65), (16, 100, 515), (17, 64, 128), (64, 2048, 2048),
+          (65, 129, 200), (100, 1001, 1000), (130, 256, 64), (255, 255, 255), (256, 256, 256), (257, 511, 320),
+          (513, 770, 2048), (1000, 300, 77), (2, 40, 131072), (1, 70000, 100), (2049, 300, 192)]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_products(act, M, N, K):
+    torch = require_gpu()
+    log(f"dense {act} {M} {N} {K}")
+    g = torch.Generator().manual_seed(M + 3 * N + K)
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    x = (torch.randn(M, K + 3, generator=g) * torch.exp(torch.randn(M, 1, generator=g))).to(dt).cuda()[:, 2:K + 2]
+    w = torch.randn(N, K + 1, generator=g).to(dt).cuda()[:, :K]
+    op = Int8Dense(w)
+    X, sx = quantized64(x.double().cpu().numpy())
+    W, sw = quantized64(w.double().cpu().numpy())
+    sums = (torch.from_numpy(X).cuda() @ torch.from_numpy(W).cuda().t()).cpu().numpy()  # exact: below 2^53
+    wide = torch.full((M, N + 6), 5.0, dtype=dt, device="cuda")
+    for eps, out in ((None, None), (1e-6, wide[:, 3:N + 3])):
+        y = op(x, out=out, rms_eps=eps).double().cpu().numpy()
+        s = sx if eps is None else sx / np.sqrt((x.double().cpu().numpy() ** 2).mean(-1) + eps)
+        ref = sums * s[:, None] * sw
+        tol = (5 if eps is None else K / 256 + 20) * 2.0 ** -24 + (2.0 ** -8 if act == "bf16" else 0)
+        bad = abs(y - ref) - tol * abs(ref) - 2.0 ** -126
+        assert bad.max() <= 0, (np.unravel_index(bad.argmax(), bad.shape), bad.max())
+    assert (wide[:, :3] == 5).all() and (wide[:, N + 3:] == 5).all()
+
+
+def test_largest_sums():
+    """All products 127^2 of 131072 inputs: 2.11e9, below 2^31."""
+    torch = require_gpu()
+    K = 131072
+    x, w = torch.ones(3, K, device="cuda"), -torch.ones(20, K, device="cuda")
+    y = Int8Dense(w)(x)
+    assert (abs(y + K) <= 5 * 2.0 ** -24 * K).all()
+
+
+def test_types_rows_and_refusals():
+    torch = require_gpu()
+    g = torch.Generator().manual_seed(1)
+    w, x = torch.randn(50, 130, generator=g).cuda(), torch.randn(9, 130, generator=g).cuda()
+    op = Int8Dense(w)
+    y = op(x)
+    assert torch.equal(op(x, out=torch.empty(9, 50, dtype=torch.bfloat16, device="cuda")), y.bfloat16())
+    assert op(x[:0]).shape == (0, 50)
+    assert torch.equal(op(x[4:5]), y[4:5]) and torch.equal(op(x[::2]), y[::2])
+    assert torch.equal(Int8Dense(w[:0])(x), y[:, :0])
+    for bad in (x[:, :129], x.half(), x.t(), x[0], x[:, None], x.cpu(), x[:1].expand(9, 130)):
+        with pytest.raises(ValueError):
+            op(bad)
+    with pytest.raises(ValueError):
+        op(x, out=y[:8])
+    with pytest.raises(HMError):
+        op(x, rms_eps=-1.0)
+    with pytest.raises(ValueError):
+        Int8Dense(torch.randn(3, 131073, device="cuda"))
+
+
+def test_captured_products_replay():
+    torch = require_gpu()
+    log("graph")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    op = Int8Dense(torch.randn(500, 300, generator=g, device="cuda"))
+    x = torch.randn(40, 300, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        op(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = op(x, rms_eps=1e-6)
+    for _ in range(4):
+        x.copy_(torch.randn(40, 300, generator=g, device="cuda"))
+        graph.replay()
+        got = y.clone()
+        torch.cuda.synchronize()
+        op(torch.randn(90, 300, generator=g, device="cuda"))
+        assert torch.equal(got, op(x, rms_eps=1e-6))
