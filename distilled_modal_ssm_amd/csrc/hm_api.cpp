@@ -1025,7 +1025,7 @@ constexpr int64_t kMostGroups = int64_t(1) << 23;
 static hm_status check_recurrence_length(const hm_recurrence_desc *d, int64_t L) {
     if (L < 0) return HM_ERR_INVALID_ARG;
     if (L > INT32_MAX / 2) return HM_ERR_UNSUPPORTED;
-    const int64_t tiles = (d->channels + 63) / 64, chunks = L > 0 ? (L + 127) / 128 : 1;
+    const int64_t tiles = (d->channels + 63) / 64, chunks = L > 0 ? (L + 63) / 64 : 1;
     if (d->batch > 0 && (tiles >= kMostGroups || chunks >= kMostGroups || tiles * chunks >= kMostGroups ||
                          d->batch >= (kMostGroups + tiles * chunks - 1) / (tiles * chunks)))
         return HM_ERR_UNSUPPORTED;

@@ -99,7 +99,7 @@ def test_recurrence_own_arguments():
     assert hb.load().hyena_recurrence_workspace(ctypes.byref(_desc()), 10, None) == BAD
 
 
-@pytest.mark.parametrize("B,D,L", [(1 << 23, 1, 1), (1 << 20, 512, 1), (1 << 10, 64, 1 << 20), (1, 1 << 29, 1)])
+@pytest.mark.parametrize("B,D,L", [(1 << 23, 1, 1), (1 << 20, 512, 1), (1 << 9, 64, 1 << 20), (1, 1 << 29, 1)])
 def test_recurrence_sizes_of_a_launch(B, D, L):
     """Batch rows, channel tiles and chunks that a launch has no threads for are refused; half as many are not."""
     for call in (lambda d: hb.hyena_recurrence_workspace(d, L), lambda d: _prompt(d, L, ld_q=D, ld_g=D, ld_v=D, ld_y=D)):
