@@ -10,20 +10,27 @@
 //     dh_t = q_t dy_t + b_t,   b_{t-1} = f_t dh_t      (b -> A b + K over a run)
 // beside the h, formed again from what the prompt kept every 64 tokens.
 //
-// Workgroups join through slots of the workspace, (A, H) as one 64-bit word a
-// channel, filled with a mark beforehand; a word that is not the mark is there.  A
-// workgroup waits for up to kGroup words: its group's earlier workgroups and the h
-// behind the group before.  Which words, and the order of the products, are fixed by
-// its place, so results do not depend on timing.  Places go by a counter that each
-// workgroup draws from when it starts, earlier runs first: whom it waits for has
-// started, and needs nothing from later ones, so every wait ends.
+// Workgroups join through words of the workspace, (A, H) as one of 64 bits a channel,
+// filled with a mark beforehand; a word that is not the mark is there.  A workgroup
+// waits for its group's earlier ones and for the h behind the group before.  Which
+// words, and the order of the products, are fixed by its place, so results do not
+// depend on timing.  Places go by a counter that each workgroup draws from when it
+// starts, earlier runs first: whom it waits for has started, and needs nothing from
+// later ones, so every wait ends.
+//
+// What bounds it (MI355X): HBM.  65536 x 4096 bfloat16 tokens, 2.15 GB: 420 us, 5.1
+// TB/s, as a large copy; without the join 379.  A workgroup's 8 waves hold 128 tokens of
+// 128 channels, two workgroups a CU (at most 128 registers: a third of a wave more and
+// there is one, which waits for others with nothing else to do: 539 us).  Runs of 64
+// tokens: 558 us, more to draw, mark and join for the same bytes.  Joined one by one in
+// groups of 8, the chain of places 8 times as long and waited for after the words: 586.
 #include "hm_internal.hpp"
 
 namespace hm {
 namespace {
 
-constexpr int kGroup = 8;               // workgroups that join one by one
-constexpr uint64_t kMark = ~0ull;       // a word that is not there yet
+constexpr int kGroup = 8;          // workgroups that join one by one
+constexpr uint64_t kMark = ~0ull;  // a word that is not there yet
 
 // ------------------------------------------------------------------ gates
 
@@ -79,64 +86,89 @@ __device__ __forceinline__ int64_t row_length(const RecurArgs &a, int64_t b) {
 
 // ------------------------------------------------------------------ a lane's channels
 
-template <int ACT, int V> struct Lane;
-template <> struct Lane<kBF16, 1> {
+constexpr int kStream = 2;  // aux of the buffer builtins: non-temporal
+
+// Memory of a lane's V neighbouring channels of a token, and its values.  Results are
+// stored past the caches, where the inputs are more use (8 x 2048 x 2048 bfloat16,
+// forward and backward: 159 us against 179).
+template <int BYTES> struct Piece;
+template <> struct Piece<2> {
     using R = uint16_t;
-    __device__ static void get(R r, float (&x)[1]) { x[0] = __uint_as_float((uint32_t)r << 16); }
-    __device__ static R put(const float (&x)[1]) { return (uint16_t)f32_to_bf16(x[0]); }
+    template <bool ONCE> __device__ static R load(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t row) {
+        return __builtin_amdgcn_raw_buffer_load_b16(r, at, row, ONCE ? kStream : 0);
+    }
+    __device__ static void store(R x, __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t row) {
+        __builtin_amdgcn_raw_buffer_store_b16(x, r, at, row, kStream);
+    }
 };
-template <> struct Lane<kBF16, 2> {
+template <> struct Piece<4> {
     using R = uint32_t;
-    __device__ static void get(R r, float (&x)[2]) {
-        x[0] = bf16_lo(r);
-        x[1] = bf16_hi(r);
+    template <bool ONCE> __device__ static R load(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t row) {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, at, row, ONCE ? kStream : 0);
     }
-    __device__ static R put(const float (&x)[2]) { return pack_bf16x2(x[0], x[1]); }
-};
-template <> struct Lane<kF32, 1> {
-    using R = float;
-    __device__ static void get(R r, float (&x)[1]) { x[0] = r; }
-    __device__ static R put(const float (&x)[1]) { return x[0]; }
-};
-template <> struct Lane<kF32, 2> {
-    using R = float2;
-    __device__ static void get(R r, float (&x)[2]) {
-        x[0] = r.x;
-        x[1] = r.y;
+    __device__ static void store(R x, __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t row) {
+        __builtin_amdgcn_raw_buffer_store_b32(x, r, at, row, kStream);
     }
-    __device__ static R put(const float (&x)[2]) { return make_float2(x[0], x[1]); }
+};
+template <int ACT, int V> struct Lane : Piece<V * Act<ACT>::kBytes> {
+    using R = typename Piece<V * Act<ACT>::kBytes>::R;
+    __device__ static void get(R r, float (&x)[V]) {
+        if constexpr (ACT == kF32) {
+            x[0] = __uint_as_float(r);
+        } else {
+            x[0] = bf16_lo(r);
+            if constexpr (V == 2) x[1] = bf16_hi(r);
+        }
+    }
+    __device__ static R put(const float (&x)[V]) {
+        if constexpr (ACT == kF32) return __float_as_uint(x[0]);
+        else if constexpr (V == 1) return (uint16_t)f32_to_bf16(x[0]);
+        else return pack_bf16x2(x[0], x[1]);
+    }
 };
 
-// Rows [..][ld] of activations of one batch row, from channel c0 on; the row is the
-// wave's, the channels behind it the lane's.
+// Hides from the compiler that x is what it was.
+template <typename R> __device__ __forceinline__ void opaque(R &x) { asm volatile("" : "+v"(x)); }
+
+// `rows` rows of activations of a tile of channels from row `first` on, none where
+// there is no memory: what lies behind the last one reads as 0 and is not written, nor
+// is a lane past the last channel.  Offsets stay below 2^31: at most 16 rows of fewer
+// than 2^22 elements.
+constexpr uint32_t kNowhere = 0x80000000u;
+constexpr int64_t kMostStride = int64_t(1) << 22;
 template <int ACT, int V> struct Rows {
     using L = Lane<ACT, V>;
     using R = typename L::R;
-    using T = typename Act<ACT>::T;
-    T *base;
-    int64_t ld;
-    uint32_t lane;
-    __device__ Rows(const void *p, int64_t ld, int64_t first, int64_t c0, uint32_t lane)
-        : base(const_cast<T *>(static_cast<const T *>(p)) + first * ld + c0), ld(ld), lane(lane) {}
-    __device__ R load(int64_t t) const { return *reinterpret_cast<const R *>(base + t * ld + lane); }
-    __device__ void store(int64_t t, const float (&x)[V]) const {
-        *reinterpret_cast<R *>(base + t * ld + lane) = L::put(x);
+    static constexpr uint32_t kBytes = Act<ACT>::kBytes;
+    __amdgpu_buffer_rsrc_t region;
+    uint32_t at, step;
+    __device__ Rows(const void *p, int64_t ld, int64_t first, int64_t rows, int64_t c0, int64_t D, int lane) {
+        const int64_t width = D - c0 < kWave * V ? D - c0 : kWave * V;
+        const bool any = p && rows > 0;
+        region = make_region(static_cast<const typename Act<ACT>::T *>(p) + (any ? first * ld + c0 : 0),
+                             any ? (uint32_t)((rows - 1) * ld + width) * kBytes : 0u);
+        step = (uint32_t)(ld < kMostStride ? ld : kMostStride) * kBytes;  // (larger ones come with one row)
+        at = lane * V < width ? lane * V * kBytes : kNowhere;
+    }
+    // ALL: every row is there, and its offset need not count for the bounds
+    template <bool ALL, bool ONCE> __device__ R load(int j) const {
+        return ALL ? L::template load<ONCE>(region, at, j * step) : L::template load<ONCE>(region, at + j * step, 0);
+    }
+    template <bool ALL> __device__ void store(int j, const float (&x)[V]) const {
+        ALL ? L::store(L::put(x), region, at, j * step) : L::store(L::put(x), region, at + j * step, 0);
     }
 };
 
 // ------------------------------------------------------------------ joining workgroups
 
-// slots[place][channel], then ends[group][channel] of a row's tile; a counter before all.
-struct Join {
-    uint64_t *slots, *ends;
-};
+// The workspace: a counter for each row's tile of channels, 128 bytes apart, then its
+// words: (A, H) of each place, (A, H) of each group of kGroup places, and the h behind
+// each kGroup groups, a word a channel each.
+constexpr int kCounter = 128;
 
-__device__ __forceinline__ uint64_t *counter_of(const RecurArgs &a) { return reinterpret_cast<uint64_t *>(a.ws); }
-
-template <int V> __device__ __forceinline__ Join join_of(const RecurArgs &a, int64_t row_tile, int places) {
-    const int groups = (places + kGroup - 1) / kGroup;
-    uint64_t *p = reinterpret_cast<uint64_t *>(a.ws + 256) + row_tile * (places + groups) * (kWave * V);
-    return {p, p + (int64_t)places * (kWave * V)};
+__host__ __device__ constexpr int groups_of(int n) { return (n + kGroup - 1) / kGroup; }
+__host__ __device__ constexpr int64_t words_of(int places) {
+    return (int64_t)places + groups_of(places) + groups_of(groups_of(places));
 }
 
 __device__ __forceinline__ void put_word(uint64_t *p, float A, float H) {
@@ -145,110 +177,309 @@ __device__ __forceinline__ void put_word(uint64_t *p, float A, float H) {
     __hip_atomic_store(p, (uint64_t)bits << 32 | __float_as_uint(H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// What comes into the workgroup at `place`, whose own run is (A, H) (a lane's
-// channels); first: what comes into place 0.
-template <int V>
-__device__ __forceinline__ void join(const Join &j, int place, int places, const float (&A)[V], const float (&H)[V],
-                                     const float (&first)[V], float (&in)[V]) {
-    const int lane = threadIdx.x % kWave, group = place / kGroup, member = place % kGroup;
-    const bool last = member == kGroup - 1;
-    uint64_t *own = j.slots + ((int64_t)place * kWave + lane) * V, *end = j.ends + ((int64_t)group * kWave + lane) * V;
-    if (place == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            in[e] = first[e];
-            if (places > 1) put_word(own + e, 0.0f, fmaf(A[e], in[e], H[e]));
-        }
-        return;
-    }
-    if (!last) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) put_word(own + e, A[e], H[e]);
-    }
-    // the group before, then this group's earlier members
-    uint64_t words[kGroup][V];
+// A lane's V words at p, as soon as they are there.
+template <int V> __device__ __forceinline__ void wait_words(const uint64_t *p, float2 *out) {
+    uint64_t word[V];
     for (;;) {
         bool there = true;
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) {
-            const uint64_t *p = k == 0 ? end - (int64_t)kWave * V : own - (int64_t)(member - k + 1) * kWave * V;
-            if (k == 0 ? group > 0 : k - 1 < member) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    words[k][e] = __hip_atomic_load(p + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    there = there && words[k][e] != kMark;
-                }
-            }
+        for (int e = 0; e < V; ++e) {
+            word[e] = __hip_atomic_load(p + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            there = there && word[e] != kMark;
         }
         if (__all(there)) break;
-        __builtin_amdgcn_s_sleep(2);
+        __builtin_amdgcn_s_sleep(1);
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        out[e] = make_float2(__uint_as_float((uint32_t)(word[e] >> 32)), __uint_as_float((uint32_t)word[e]));
+}
+
+template <int V> struct JoinShared {
+    float2 members[kGroup - 1][kWave * V], groups[kGroup - 1][kWave * V], before[kWave * V];
+};
+
+// What comes into the workgroup at `place` (a lane's channels).  Its last wave has its
+// own run (A, H); first: what comes into place 0.  Every wave looks out for other words:
+// those of the places before it in its group, of the groups before that in their group,
+// and the h before those, which is the only chain: one link for kGroup^2 places.
+template <int V, int W>
+__device__ __forceinline__ void join(const RecurArgs &a, uint32_t row_tile, uint32_t row_tiles, int places, int place, int w,
+                                     const float (&A)[V], const float (&H)[V], const float (&first)[V], JoinShared<V> &sh,
+                                     float (&in)[V]) {
+    const int lane = threadIdx.x % kWave, at = lane * V;
+    uint64_t *slots = reinterpret_cast<uint64_t *>(a.ws + (int64_t)row_tiles * kCounter) +
+                      (int64_t)row_tile * words_of(places) * (kWave * V) + at;
+    uint64_t *groups = slots + (int64_t)places * (kWave * V);
+    uint64_t *ends = groups + (int64_t)groups_of(places) * (kWave * V);
+    const int group = place / kGroup, member = place % kGroup, end = group / kGroup, behind = group % kGroup;
+    auto word = [&](uint64_t *p, int k) { return p + (int64_t)k * (kWave * V); };
+    if (w == W - 1 && member < kGroup - 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            put_word(word(slots, place) + e, place == 0 ? 0.0f : A[e], place == 0 ? fmaf(A[e], first[e], H[e]) : H[e]);
+    }
+    if (place == 0) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) in[e] = first[e];
+        return;
+    }
+    for (int k = w; k < member; k += W) wait_words<V>(word(slots, group * kGroup + k), &sh.members[k][at]);
+    if (member == kGroup - 1 && behind < kGroup - 1) {  // the whole group's, before waiting for others
+        __syncthreads();
+        if (w == W - 1) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float gA = 1.0f, gH = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kGroup - 1; ++k) {
+                    const float2 m = sh.members[k][at + e];
+                    gH = fmaf(m.x, gH, m.y);
+                    gA *= m.x;
+                }
+                put_word(word(groups, group) + e, gA * A[e], fmaf(A[e], gH, H[e]));
+            }
+        }
+    }
+    for (int k = w; k < behind; k += W) wait_words<V>(word(groups, end * kGroup + k), &sh.groups[k][at]);
+    if (end > 0 && w == W - 1) wait_words<V>(word(ends, end - 1), &sh.before[at]);
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        in[e] = 0.0f;
+        in[e] = end > 0 ? sh.before[at + e].y : 0.0f;
+        for (int k = 0; k < behind; ++k) in[e] = fmaf(sh.groups[k][at + e].x, in[e], sh.groups[k][at + e].y);
+        for (int k = 0; k < member; ++k) in[e] = fmaf(sh.members[k][at + e].x, in[e], sh.members[k][at + e].y);
+    }
+    if (w == W - 1 && member == kGroup - 1 && behind == kGroup - 1) {
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k)
-            if (k == 0 ? group > 0 : k - 1 < member)
-                in[e] = fmaf(__uint_as_float((uint32_t)(words[k][e] >> 32)), in[e], __uint_as_float((uint32_t)words[k][e]));
-        if (last) put_word(end + e, 0.0f, fmaf(A[e], in[e], H[e]));
+        for (int e = 0; e < V; ++e) put_word(word(ends, end) + e, 0.0f, fmaf(A[e], in[e], H[e]));
     }
 }
 
-// The workgroup's number: drawn, where workgroups wait for each other.
-__device__ __forceinline__ int64_t draw_number(const RecurArgs &a, int places) {
-    if (places == 1) return blockIdx.x;
-    __shared__ uint32_t number;
-    if (threadIdx.x == 0) number = atomicAdd(reinterpret_cast<unsigned int *>(counter_of(a)), 1u);
+// The workgroup's place in its row's tile: drawn, where workgroups wait for each other.
+// (One counter for all was drawn from every 14 ns at most: 65536 x 4096 tokens in runs
+// of 64, 460 us of drawing.)
+__device__ __forceinline__ int draw_place(const RecurArgs &a, uint32_t row_tile, int places) {
+    if (places == 1) return 0;
+    __shared__ uint32_t place;
+    if (threadIdx.x == 0) place = atomicAdd(reinterpret_cast<unsigned int *>(a.ws + (int64_t)row_tile * kCounter), 1u);
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane((int)number);
+    return __builtin_amdgcn_readfirstlane((int)place);
 }
 
-__global__ __launch_bounds__(256) void recurrence_mark_kernel(ulonglong2 *p, int64_t n) {
+__global__ __launch_bounds__(256) void recurrence_mark_kernel(ulonglong2 *p, int64_t counters, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    p[i] = i < 16 ? ulonglong2{0, 0} : ulonglong2{kMark, kMark};  // 256 bytes of counter before the words
+    if (i < n) p[i] = i < counters ? ulonglong2{0, 0} : ulonglong2{kMark, kMark};
 }
 
 // ------------------------------------------------------------------ a prompt
 
-template <int ACT, int GATE, int INPUT, int V, int W, int T>
-__global__ __launch_bounds__(W *kWave) void recurrence_kernel(RecurArgs a, int places) {
+template <int ACT, int GATE, int INPUT, int V, int W, int T, bool ONCE>
+__global__ __launch_bounds__(W *kWave, 4) void recurrence_kernel(RecurArgs a, int places) {
     using Lane = Lane<ACT, V>;
     using R = typename Lane::R;
     constexpr int kRun = W * T;
     __shared__ float2 runs[W][kWave * V];
-    __shared__ float came[kWave * V];
+    __shared__ JoinShared<V> joined;
     const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t tiles = (a.D + kWave * V - 1) / (kWave * V), number = draw_number(a, places);
-    const int place = (int)(number / (a.B * tiles));
-    const int64_t row_tile = number % (a.B * tiles), b = row_tile / tiles, c0 = row_tile % tiles * (kWave * V);
+    const uint32_t tiles = (uint32_t)((a.D + kWave * V - 1) / (kWave * V)), row_tiles = (uint32_t)a.B * tiles;
+    const uint32_t row_tile = blockIdx.x % row_tiles, tile = row_tile % tiles;
+    const int place = draw_place(a, row_tile, places);
+    const int64_t b = row_tile / tiles, c0 = (int64_t)tile * (kWave * V);
     const bool mine = c0 + lane * V < a.D;
-    // lanes past the last channel read its neighbours' and write nothing
+    // lanes past the last channel read their neighbours' states and write nothing
     const int64_t at = mine ? lane * V : a.D - V - c0;
-    const int64_t n = row_length(a, b), t0 = (int64_t)place * kRun + w * T;
-    const Rows<ACT, V> y(a.y, a.ld_y, b * a.L, c0, (uint32_t)(lane * V));
-    const float zero[V] = {};
-    if (place > 0 && (int64_t)place * kRun >= n) {
-        for (int64_t t = t0; t < t0 + T && t < a.L; ++t)
-            if (mine) y.store(t, zero);
+    const int64_t n = row_length(a, b), r0 = (int64_t)place * kRun, t0 = r0 + w * T, first_row = b * a.L + t0;
+    const Rows<ACT, V> y(a.y, a.ld_y, first_row, a.L - t0 < T ? a.L - t0 : T, c0, a.D, lane);
+    if (place > 0 && r0 >= n) {
+        const float zero[V] = {};
+#pragma unroll
+        for (int j = 0; j < T; ++j) y.template store<false>(j, zero);
         return;
     }
-    float f[T][V], x[T][V];
-    R q[T];
-    if (n > 0) {
-        // rows past the end: the last one again, not used
-        const Rows<ACT, V> gr(a.g, a.ld_g, b * a.L, c0, (uint32_t)at), vr(a.v, a.ld_v, b * a.L, c0, (uint32_t)at);
-        const Rows<ACT, V> qr(a.q ? a.q : a.g, a.q ? a.ld_q : a.ld_g, b * a.L, c0, (uint32_t)at);
-        R g[T], v[T];
+    const int64_t rows = n - t0 < T ? n - t0 : T;
+    const Rows<ACT, V> gr(a.g, a.ld_g, first_row, rows, c0, a.D, lane);
+    const Rows<ACT, V> vr(a.v, a.ld_v, first_row, rows, c0, a.D, lane);
+    const Rows<ACT, V> qr(a.q, a.ld_q, first_row, rows, c0, a.D, lane);
+    // whole: every token of the workgroup is before the row's end
+    auto go = [&](auto whole) {
+        constexpr bool ALL = decltype(whole)::value;
+        R g[T], v[T], q[T];
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            const int64_t t = t0 + j < n ? t0 + j : n - 1;
-            g[j] = gr.load(t);
-            v[j] = vr.load(t);
+            g[j] = gr.template load<ALL, ONCE>(j);
+            v[j] = vr.template load<ALL, ONCE>(j);
         }
-        if (a.q) {
 #pragma unroll
-            for (int j = 0; j < T; ++j) q[j] = qr.load(t0 + j < n ? t0 + j : n - 1);
+        for (int j = 0; j < T; ++j) q[j] = qr.template load<ALL, ONCE>(j);
+        const int live = ALL ? T : rows > 0 ? (int)rows : 0;
+        float f[T][V], x[T][V];
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            Lane::get(g[j], f[j]);
+            Lane::get(v[j], x[j]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                float i;
+                gate_of<GATE, INPUT>(f[j][e], f[j][e], i);
+                x[j][e] = ALL || j < live ? i * x[j][e] : 0.0f;
+                f[j][e] = ALL || j < live ? f[j][e] : 1.0f;
+            }
+        }
+        float A[V], H[V], h[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            A[e] = 1.0f;
+            H[e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                H[e] = fmaf(f[j][e], H[e], x[j][e]);
+                A[e] *= f[j][e];
+            }
+        }
+        // the state before everything (another lane's, past the last channel: not used)
+        float first[V] = {};
+        if (a.state_in && place == 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) first[e] = a.state_in[b * a.D + c0 + at + e];
+        }
+        if constexpr (W == 1) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) h[e] = first[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) runs[w][lane * V + e] = make_float2(A[e], H[e]);
+            __syncthreads();
+            float pA[V], pH[V];  // the waves before
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                pA[e] = 1.0f;
+                pH[e] = 0.0f;
+            }
+            for (int k = 0; k < w; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float2 r = runs[k][lane * V + e];
+                    pH[e] = fmaf(r.x, pH[e], r.y);
+                    pA[e] *= r.x;
+                }
+            if (w == W - 1) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    H[e] = fmaf(A[e], pH[e], H[e]);
+                    A[e] *= pA[e];
+                }
+            }
+            if (places > 1) {
+                join<V, W>(a, row_tile, row_tiles, places, place, w, A, H, first, joined, h);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) h[e] = first[e];
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) h[e] = fmaf(pA[e], h[e], pH[e]);
+        }
+        if (a.chunk_states && t0 % kRecurChunk == 0 && live > 0 && mine) {
+            const int64_t chunks = (a.L + kRecurChunk - 1) / kRecurChunk;
+            float *p = a.chunk_states + (b * chunks + t0 / kRecurChunk) * a.D + c0 + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; ++e) p[e] = h[e];
+        }
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            float out[V];
+            Lane::get(q[j], out);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                h[e] = fmaf(f[j][e], h[e], x[j][e]);
+                out[e] = !ALL && j >= live ? 0.0f : a.q ? out[e] * h[e] : h[e];
+            }
+            y.template store<ALL>(j, out);
+        }
+        // the row's last run: what is past its end left h as it was
+        if (w == W - 1 && mine && r0 + kRun >= n) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) a.state_out[b * a.D + c0 + lane * V + e] = h[e];
+        }
+    };
+    if (n - r0 >= kRun) go(std::true_type{});
+    else go(std::false_type{});
+}
+
+// ------------------------------------------------------------------ backward
+
+template <int ACT, int GATE, int INPUT, int V, int W, int T, bool ONCE>
+__global__ __launch_bounds__(W *kWave, 4) void recurrence_backward_kernel(RecurArgs a, int places) {
+    using Lane = Lane<ACT, V>;
+    using R = typename Lane::R;
+    constexpr int kRun = W * T;
+    static_assert(kRun <= kRecurChunk && kRecurChunk % kRun == 0, "a run starts from one kept state");
+    __shared__ float4 runs[W][kWave * V];  // A, H, K
+    __shared__ JoinShared<V> joined;
+    const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t tiles = (uint32_t)((a.D + kWave * V - 1) / (kWave * V)), row_tiles = (uint32_t)a.B * tiles;
+    const uint32_t row_tile = blockIdx.x % row_tiles, tile = row_tile % tiles;
+    const int run = places - 1 - draw_place(a, row_tile, places);  // the last ones first
+    const int64_t b = row_tile / tiles, c0 = (int64_t)tile * (kWave * V);
+    const bool mine = c0 + lane * V < a.D;
+    const int64_t at = mine ? lane * V : a.D - V - c0;
+    const int64_t n = row_length(a, b), r0 = (int64_t)run * kRun, t0 = r0 + w * T, first_row = b * a.L + t0;
+    const int64_t all = a.L - t0 < T ? a.L - t0 : T;
+    const Rows<ACT, V> dqr(a.dq, a.ld_dq, first_row, all, c0, a.D, lane);
+    const Rows<ACT, V> dgr(a.dg, a.ld_dg, first_row, all, c0, a.D, lane);
+    const Rows<ACT, V> dvr(a.dv, a.ld_dv, first_row, all, c0, a.D, lane);
+    if (r0 >= n) {  // behind the row's end, or a row of none
+        const float zero[V] = {};
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            dqr.template store<false>(j, zero);
+            dgr.template store<false>(j, zero);
+            dvr.template store<false>(j, zero);
+        }
+        if (run == 0 && w == 0 && mine && a.dstate_in) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                a.dstate_in[b * a.D + c0 + lane * V + e] = a.dstate_out ? a.dstate_out[b * a.D + c0 + lane * V + e] : 0.0f;
+        }
+        return;
+    }
+    const int last_run = (int)((n - 1) / kRun);
+    float back[V] = {};
+    if (a.dstate_out && run == last_run) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) back[e] = a.dstate_out[b * a.D + c0 + at + e];
+    }
+    const int64_t rows = n - t0 < T ? n - t0 : T;
+    const Rows<ACT, V> gr(a.g, a.ld_g, first_row, rows, c0, a.D, lane);
+    const Rows<ACT, V> vr(a.v, a.ld_v, first_row, rows, c0, a.D, lane);
+    const Rows<ACT, V> qr(a.q, a.ld_q, first_row, rows, c0, a.D, lane);
+    const Rows<ACT, V> dyr(a.dy, a.ld_dy, first_row, rows, c0, a.D, lane);
+    auto go = [&](auto whole) {
+        constexpr bool ALL = decltype(whole)::value;
+        R g[T], v[T], q[T], dy[T];
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            g[j] = gr.template load<ALL, ONCE>(j);
+            v[j] = vr.template load<ALL, ONCE>(j);
+        }
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            dy[j] = dyr.template load<ALL, ONCE>(j);
+            q[j] = qr.template load<ALL, ONCE>(j);
+        }
+        const int live = ALL ? T : rows > 0 ? (int)rows : 0;
+        float h[V];
+        {
+            const int64_t chunks = (a.L + kRecurChunk - 1) / kRecurChunk;
+            const float *p = a.chunk_states + (b * chunks + (int64_t)run * kRun / kRecurChunk) * a.D + c0 + at;
+#pragma unroll
+            for (int e = 0; e < V; ++e) h[e] = p[e];
+        }
+        float f[T][V], x[T][V], A[V], H[V], K[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            A[e] = 1.0f;
+            H[e] = K[e] = 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < T; ++j) {
@@ -258,192 +489,19 @@ __global__ __launch_bounds__(W *kWave) void recurrence_kernel(RecurArgs a, int p
             for (int e = 0; e < V; ++e) {
                 float i;
                 gate_of<GATE, INPUT>(f[j][e], f[j][e], i);
-                x[j][e] = t0 + j < n ? i * x[j][e] : 0.0f;
-                f[j][e] = t0 + j < n ? f[j][e] : 1.0f;
+                x[j][e] = ALL || j < live ? i * x[j][e] : 0.0f;
+                f[j][e] = ALL || j < live ? f[j][e] : 1.0f;
+                H[e] = fmaf(f[j][e], H[e], x[j][e]);
+                A[e] *= f[j][e];
             }
         }
-    } else {
+        // q dy of a token, 0 past the end
+        auto given = [&](int j, float (&s)[V]) {
+            float d[V];
+            Lane::get(dy[j], d);
+            Lane::get(q[j], s);
 #pragma unroll
-        for (int j = 0; j < T; ++j)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                f[j][e] = 1.0f;
-                x[j][e] = 0.0f;
-            }
-    }
-    float A[V], H[V], h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        A[e] = 1.0f;
-        H[e] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < T; ++j) {
-            H[e] = fmaf(f[j][e], H[e], x[j][e]);
-            A[e] *= f[j][e];
-        }
-    }
-    // the state before everything (another lane's, past the last channel: not used)
-    float first[V] = {};
-    if (a.state_in && (W == 1 || w == W - 1) && place == 0) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) first[e] = a.state_in[b * a.D + c0 + at + e];
-    }
-    if constexpr (W == 1) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = first[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) runs[w][lane * V + e] = make_float2(A[e], H[e]);
-        __syncthreads();
-        float pA[V], pH[V];  // the waves before
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            pA[e] = 1.0f;
-            pH[e] = 0.0f;
-        }
-        for (int k = 0; k < w; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float2 r = runs[k][lane * V + e];
-                pH[e] = fmaf(r.x, pH[e], r.y);
-                pA[e] *= r.x;
-            }
-        if (w == W - 1) {
-            float in[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                H[e] = fmaf(A[e], pH[e], H[e]);
-                A[e] *= pA[e];
-                in[e] = first[e];
-            }
-            if (places > 1) join<V>(join_of<V>(a, row_tile, places), place, places, A, H, first, in);
-#pragma unroll
-            for (int e = 0; e < V; ++e) came[lane * V + e] = in[e];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = fmaf(pA[e], came[lane * V + e], pH[e]);
-    }
-    if (a.chunk_states && t0 % kRecurChunk == 0 && t0 < n && mine) {
-        const int64_t chunks = (a.L + kRecurChunk - 1) / kRecurChunk;
-        float *p = a.chunk_states + (b * chunks + t0 / kRecurChunk) * a.D + c0 + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) p[e] = h[e];
-    }
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-        float out[V];
-        if (a.q && n > 0) Lane::get(q[j], out);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            h[e] = fmaf(f[j][e], h[e], x[j][e]);
-            out[e] = t0 + j >= n ? 0.0f : a.q ? out[e] * h[e] : h[e];
-        }
-        if (t0 + j < a.L && mine) y.store(t0 + j, out);
-    }
-    // the row's last run: what is past its end left h as it was
-    if (w == W - 1 && mine && (int64_t)(place + 1) * kRun >= n) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) a.state_out[b * a.D + c0 + lane * V + e] = h[e];
-    }
-}
-
-// ------------------------------------------------------------------ backward
-
-template <int ACT, int GATE, int INPUT, int V, int W, int T>
-__global__ __launch_bounds__(W *kWave) void recurrence_backward_kernel(RecurArgs a, int places) {
-    using Lane = Lane<ACT, V>;
-    using R = typename Lane::R;
-    constexpr int kRun = W * T;
-    static_assert(kRun <= kRecurChunk && kRecurChunk % kRun == 0, "a run starts from one kept state");
-    __shared__ float4 runs[W][kWave * V];  // A, H, K
-    __shared__ float came[kWave * V];
-    const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int64_t tiles = (a.D + kWave * V - 1) / (kWave * V), number = draw_number(a, places);
-    const int run = places - 1 - (int)(number / (a.B * tiles));  // the last ones first
-    const int64_t row_tile = number % (a.B * tiles), b = row_tile / tiles, c0 = row_tile % tiles * (kWave * V);
-    const bool mine = c0 + lane * V < a.D;
-    const int64_t at = mine ? lane * V : a.D - V - c0;
-    const int64_t n = row_length(a, b), t0 = (int64_t)run * kRun + w * T;
-    const Rows<ACT, V> dqr(a.dq, a.ld_dq, b * a.L, c0, (uint32_t)(lane * V));
-    const Rows<ACT, V> dgr(a.dg, a.ld_dg, b * a.L, c0, (uint32_t)(lane * V));
-    const Rows<ACT, V> dvr(a.dv, a.ld_dv, b * a.L, c0, (uint32_t)(lane * V));
-    const float zero[V] = {};
-    auto clear = [&](int64_t from) {
-        for (int64_t t = from > t0 ? from : t0; t < t0 + T && t < a.L; ++t)
-            if (mine) {
-                if (a.q) dqr.store(t, zero);
-                dgr.store(t, zero);
-                dvr.store(t, zero);
-            }
-    };
-    if (run > 0 && (int64_t)run * kRun >= n) {
-        clear(t0);
-        return;
-    }
-    const int last_run = n > 0 ? (int)((n - 1) / kRun) : 0;
-    float back[V] = {};
-    if (a.dstate_out && run == last_run) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) back[e] = a.dstate_out[b * a.D + c0 + at + e];
-    }
-    if (n == 0) {
-        clear(0);
-        if (w == 0 && mine && a.dstate_in) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) a.dstate_in[b * a.D + c0 + lane * V + e] = back[e];
-        }
-        return;
-    }
-    const Rows<ACT, V> gr(a.g, a.ld_g, b * a.L, c0, (uint32_t)at), vr(a.v, a.ld_v, b * a.L, c0, (uint32_t)at);
-    const Rows<ACT, V> qr(a.q ? a.q : a.g, a.q ? a.ld_q : a.ld_g, b * a.L, c0, (uint32_t)at);
-    const Rows<ACT, V> dyr(a.dy, a.ld_dy, b * a.L, c0, (uint32_t)at);
-    R g[T], v[T], q[T], dy[T];
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-        const int64_t t = t0 + j < n ? t0 + j : n - 1;
-        g[j] = gr.load(t);
-        v[j] = vr.load(t);
-        dy[j] = dyr.load(t);
-    }
-    if (a.q) {
-#pragma unroll
-        for (int j = 0; j < T; ++j) q[j] = qr.load(t0 + j < n ? t0 + j : n - 1);
-    }
-    float h[V];
-    {
-        const int64_t chunks = (a.L + kRecurChunk - 1) / kRecurChunk;
-        const float *p = a.chunk_states + (b * chunks + (int64_t)run * kRun / kRecurChunk) * a.D + c0 + at;
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = p[e];
-    }
-    float f[T][V], x[T][V], A[V], H[V], K[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        A[e] = 1.0f;
-        H[e] = K[e] = 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-        Lane::get(g[j], f[j]);
-        Lane::get(v[j], x[j]);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float i;
-            gate_of<GATE, INPUT>(f[j][e], f[j][e], i);
-            x[j][e] = t0 + j < n ? i * x[j][e] : 0.0f;
-            f[j][e] = t0 + j < n ? f[j][e] : 1.0f;
-            H[e] = fmaf(f[j][e], H[e], x[j][e]);
-            A[e] *= f[j][e];
-        }
-    }
-    // q dy of a token, 0 past the end
-    auto given = [&](int j, float (&s)[V]) {
-        float d[V];
-        Lane::get(dy[j], d);
-        if (a.q) Lane::get(q[j], s);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[e] = t0 + j >= n ? 0.0f : a.q ? s[e] * d[e] : d[e];
+            for (int e = 0; e < V; ++e) s[e] = !ALL && j >= live ? 0.0f : a.q ? s[e] * d[e] : d[e];
     };
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
@@ -476,20 +534,20 @@ __global__ __launch_bounds__(W *kWave) void recurrence_backward_kernel(RecurArgs
                 pA[e] *= r.x;
             }
         if (w == 0) {
-            float in[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 K[e] = fmaf(A[e], pK[e], K[e]);
                 A[e] *= pA[e];
-                in[e] = back[e];
             }
-            if (places > 1) join<V>(join_of<V>(a, row_tile, places), last_run - run, last_run + 1, A, K, back, in);
-#pragma unroll
-            for (int e = 0; e < V; ++e) came[lane * V + e] = in[e];
         }
-        __syncthreads();
+        if (last_run > 0) {
+            float in[V];
+            join<V, W>(a, row_tile, row_tiles, places, last_run - run, W - 1 - w, A, K, back, joined, in);
 #pragma unroll
-        for (int e = 0; e < V; ++e) back[e] = fmaf(pA[e], came[lane * V + e], pK[e]);
+            for (int e = 0; e < V; ++e) back[e] = in[e];
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) back[e] = fmaf(pA[e], back[e], pK[e]);
     }
     // the h before every token, in x's place; dq on the way
 #pragma unroll
@@ -501,13 +559,15 @@ __global__ __launch_bounds__(W *kWave) void recurrence_backward_kernel(RecurArgs
             const float before = h[e];
             h[e] = fmaf(f[j][e], h[e], x[j][e]);
             x[j][e] = before;
-            d[e] *= h[e];
+            d[e] = ALL || j < live ? d[e] * h[e] : 0.0f;
         }
-        if (a.q && t0 + j < n && mine) dqr.store(t0 + j, d);
+        dqr.template store<ALL>(j, d);
     }
 #pragma unroll
     for (int j = T - 1; j >= 0; --j) {
         float s[V], gj[V], vj[V], dg[V], dv[V];
+        // the gate is formed again: kept, it would take the registers of a second workgroup
+        opaque(g[j]);
         given(j, s);
         Lane::get(g[j], gj);
         Lane::get(v[j], vj);
@@ -516,20 +576,20 @@ __global__ __launch_bounds__(W *kWave) void recurrence_backward_kernel(RecurArgs
             float ff, i, df, di;
             gate_grad<GATE, INPUT>(gj[e], ff, i, df, di);
             const float dh = s[e] + back[e];
-            dg[e] = dh * fmaf(df, x[j][e], di * vj[e]);
-            dv[e] = dh * i;
-            back[e] = f[j][e] * dh;
+            dg[e] = ALL || j < live ? dh * fmaf(df, x[j][e], di * vj[e]) : 0.0f;
+            dv[e] = ALL || j < live ? dh * i : 0.0f;
+            back[e] = ALL || j < live ? ff * dh : dh;
         }
-        if (t0 + j < n && mine) {
-            dgr.store(t0 + j, dg);
-            dvr.store(t0 + j, dv);
-        }
+        dgr.template store<ALL>(j, dg);
+        dvr.template store<ALL>(j, dv);
     }
-    clear(n);
     if (run == 0 && w == 0 && mine && a.dstate_in) {
 #pragma unroll
         for (int e = 0; e < V; ++e) a.dstate_in[b * a.D + c0 + lane * V + e] = back[e];
     }
+    };
+    if (n - r0 >= kRun) go(std::true_type{});
+    else go(std::false_type{});
 }
 
 // ------------------------------------------------------------------ one token
@@ -570,28 +630,42 @@ template <typename F> hipError_t for_types(const RecurArgs &a, F launch) {
 
 constexpr int kWaves = 8, kLong = 16, kShort = 8;  // waves, and tokens of a wave
 
-// Tokens of a workgroup of a prompt: up to 8 in one wave, else 8 a wave to 64 in
-// all, else 16 a wave.
+// Tokens of a workgroup.  A prompt: up to 8 in one wave, else 8 a wave where 64 are
+// enough, else 16.  Backward 8 a wave, whose registers hold twice as much a token.
 int prompt_run(int64_t L) { return L <= kShort ? kShort : L <= kWaves * kShort ? kWaves * kShort : kWaves * kLong; }
-int backward_run(int64_t L) { return L <= kShort ? kShort : kRecurChunk; }
+int backward_run(int64_t L) { return L <= kShort ? kShort : kWaves * kShort; }
 int places_of(int64_t L, int run) { return L > 0 ? (int)((L + run - 1) / run) : 1; }
 
-// Pairs of channels a lane where all rows have them aligned.
+// Whether `tensors` inputs are read past the caches: non-temporal where they do not fit
+// the 256 MB of Infinity Cache (65536 x 4096 bfloat16 tokens: 420 us against 454;
+// backward over 8 x 2048 x 2048: 5 us of 80 less), else not, since backward finds there
+// what the prompt has read (6 x 1501 x 1000 float32: 77 us for both against 99).
+bool read_once(const RecurArgs &a, int tensors) {
+    return a.B * a.L * a.D * (a.act == kBF16 ? 2 : 4) * (tensors - (a.q ? 0 : 1)) > (int64_t(256) << 20);
+}
+
+// Pairs of bfloat16 channels a lane (4 bytes, as one float32 channel) where all rows have
+// them aligned.
 bool in_pairs(const RecurArgs &a) {
-    const uintptr_t e = a.act == kBF16 ? 4 : 8;
-    auto ok = [&](const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % e == 0 && (ld % 2 == 0 || a.L * a.B <= 1); };
-    return a.D % 2 == 0 && ok(a.q, a.ld_q) && ok(a.g, a.ld_g) && ok(a.v, a.ld_v) && ok(a.y, a.ld_y) && ok(a.dy, a.ld_dy) &&
-           ok(a.dq, a.ld_dq) && ok(a.dg, a.ld_dg) && ok(a.dv, a.ld_dv);
+    auto ok = [&](const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && (ld % 2 == 0 || a.L * a.B <= 1); };
+    return a.act == kBF16 && a.D % 2 == 0 && ok(a.q, a.ld_q) && ok(a.g, a.ld_g) && ok(a.v, a.ld_v) && ok(a.y, a.ld_y) &&
+           ok(a.dy, a.ld_dy) && ok(a.dq, a.ld_dq) && ok(a.dg, a.ld_dg) && ok(a.dv, a.ld_dv);
 }
 
+size_t counters_bytes(int64_t B, int64_t D) { return (size_t)(B * ((D + kWave - 1) / kWave)) * kCounter; }
+
+// (row tiles of 64 channels have the most counters, of more channels the most words)
 size_t words_bytes(int64_t B, int64_t D, int places) {
-    const int64_t channels = (D + 2 * kWave - 1) / (2 * kWave) * (2 * kWave), groups = (places + kGroup - 1) / kGroup;
-    return places > 1 ? 256 + (size_t)(B * channels) * (size_t)(places + groups) * sizeof(uint64_t) : 0;
+    constexpr int64_t kTile = 2 * kWave;
+    const int64_t channels = (D + kTile - 1) / kTile * kTile;
+    return places > 1 ? counters_bytes(B, D) + (size_t)(B * channels * words_of(places)) * sizeof(uint64_t) : 0;
 }
 
-hipError_t mark_words(const RecurArgs &a, int places, hipStream_t stream) {
-    const int64_t n = (int64_t)(words_bytes(a.B, a.D, places) / sizeof(ulonglong2));
-    if (n > 0) recurrence_mark_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(reinterpret_cast<ulonglong2 *>(a.ws), n);
+hipError_t mark_words(const RecurArgs &a, int V, int places, hipStream_t stream) {
+    if (places == 1) return hipSuccess;
+    const int64_t row_tiles = a.B * ((a.D + kWave * V - 1) / (kWave * V));
+    const int64_t counters = row_tiles * (kCounter / 16), n = counters + row_tiles * words_of(places) * (kWave * V / 2);
+    recurrence_mark_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(reinterpret_cast<ulonglong2 *>(a.ws), counters, n);
     return hipGetLastError();
 }
 
@@ -604,36 +678,46 @@ size_t recurrence_workspace(int64_t B, int64_t D, int64_t L) {
 
 hipError_t launch_recurrence_prefill(const RecurArgs &a, hipStream_t stream) {
     const int run = prompt_run(a.L), places = places_of(a.L, run);
-    const hipError_t e = mark_words(a, places, stream);
+    const int V = in_pairs(a) ? 2 : 1;
+    const hipError_t e = mark_words(a, V, places, stream);
     if (e != hipSuccess) return e;
+    const bool once = read_once(a, 3);
     return for_types(a, [&](auto act, auto gate, auto input) {
         constexpr int C = decltype(act)::value, G = decltype(gate)::value, I = decltype(input)::value;
         auto go = [&](auto v) {
             constexpr int V = decltype(v)::value;
             const dim3 grid((unsigned)(a.B * ((a.D + kWave * V - 1) / (kWave * V)) * places));
-            if (run == kShort) recurrence_kernel<C, G, I, V, 1, kShort><<<grid, kWave, 0, stream>>>(a, places);
-            else if (run == kWaves * kShort) recurrence_kernel<C, G, I, V, kWaves, kShort><<<grid, kWaves * kWave, 0, stream>>>(a, places);
-            else recurrence_kernel<C, G, I, V, kWaves, kLong><<<grid, kWaves * kWave, 0, stream>>>(a, places);
+            if (run == kShort) recurrence_kernel<C, G, I, V, 1, kShort, false><<<grid, kWave, 0, stream>>>(a, places);
+            else if (run == kWaves * kShort) recurrence_kernel<C, G, I, V, kWaves, kShort, false><<<grid, kWaves * kWave, 0, stream>>>(a, places);
+            else if (once) recurrence_kernel<C, G, I, V, kWaves, kLong, true><<<grid, kWaves * kWave, 0, stream>>>(a, places);
+            else recurrence_kernel<C, G, I, V, kWaves, kLong, false><<<grid, kWaves * kWave, 0, stream>>>(a, places);
         };
-        if (in_pairs(a)) go(std::integral_constant<int, 2>{});
-        else go(std::integral_constant<int, 1>{});
+        if constexpr (C == kBF16) {
+            if (V > 1) return go(std::integral_constant<int, 2>{});
+        }
+        go(std::integral_constant<int, 1>{});
     });
 }
 
 hipError_t launch_recurrence_backward(const RecurArgs &a, hipStream_t stream) {
     const int run = backward_run(a.L), places = places_of(a.L, run);
-    const hipError_t e = mark_words(a, places, stream);
+    const int V = in_pairs(a) ? 2 : 1;
+    const hipError_t e = mark_words(a, V, places, stream);
     if (e != hipSuccess) return e;
+    const bool once = read_once(a, 4);
     return for_types(a, [&](auto act, auto gate, auto input) {
         constexpr int C = decltype(act)::value, G = decltype(gate)::value, I = decltype(input)::value;
         auto go = [&](auto v) {
             constexpr int V = decltype(v)::value;
             const dim3 grid((unsigned)(a.B * ((a.D + kWave * V - 1) / (kWave * V)) * places));
-            if (run == kShort) recurrence_backward_kernel<C, G, I, V, 1, kShort><<<grid, kWave, 0, stream>>>(a, places);
-            else recurrence_backward_kernel<C, G, I, V, kWaves, kShort><<<grid, kWaves * kWave, 0, stream>>>(a, places);
+            if (run == kShort) recurrence_backward_kernel<C, G, I, V, 1, kShort, false><<<grid, kWave, 0, stream>>>(a, places);
+            else if (once) recurrence_backward_kernel<C, G, I, V, kWaves, kShort, true><<<grid, kWaves * kWave, 0, stream>>>(a, places);
+            else recurrence_backward_kernel<C, G, I, V, kWaves, kShort, false><<<grid, kWaves * kWave, 0, stream>>>(a, places);
         };
-        if (in_pairs(a)) go(std::integral_constant<int, 2>{});
-        else go(std::integral_constant<int, 1>{});
+        if constexpr (C == kBF16) {
+            if (V > 1) return go(std::integral_constant<int, 2>{});
+        }
+        go(std::integral_constant<int, 1>{});
     });
 }
 

@@ -722,8 +722,8 @@ hm_status hyena_recurrence_workspace(const hm_recurrence_desc *desc, int64_t L, 
  * row and channel not finite (NaN where the recurrence may have an infinity,
  * behind a gate of 0 too); never other rows or channels.  Apart from state_in,
  * outputs must not overlap inputs.  Results do not depend on timing.
- * L < 2^30, and batch * ceil(channels / 64) * ceil(L / 64) < 2^23 (else
- * HM_ERR_UNSUPPORTED).
+ * L < 2^30, strides of more than one token below 2^22, and
+ * batch * ceil(channels / 64) * ceil(L / 64) < 2^23 (else HM_ERR_UNSUPPORTED).
  */
 hm_status hyena_recurrence_prefill(const hm_recurrence_desc *desc, int64_t L, const int32_t *lengths,
                                    const void *q, int64_t ld_q, const void *g, int64_t ld_g,
