@@ -1,6 +1,9 @@
 // int8.hip -- products in 8-bit integers: rows of activations and of weights as
 // whole multiples of a scale of their own, their products summed exactly in 32 bits
 // on the matrix cores, the scales applied to the sums.
+#include <type_traits>
+#include <utility>
+
 #include "hm_internal.hpp"
 
 namespace hm {
@@ -66,26 +69,290 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     }
 }
 
-// ------------------------------------------------------------------ products
+// ------------------------------------------------------------------ products, tiles
 
-// One wave 16 x 16 outputs.  The W fragment is the first operand: lane l holds row
-// l % 16 of A's tile and columns 4 (l / 16) .. + 3.
-template <int ACT>
-__global__ __launch_bounds__(64) void dense_int8_kernel(Int8GemmArgs g) {
-    using A = Act<ACT>;
-    const int64_t tiles_n = (g.N + 15) / 16, m0 = blockIdx.x / tiles_n * 16, n0 = blockIdx.x % tiles_n * 16;
-    const int lane = threadIdx.x, r = lane % 16, c = lane / 16;
-    const int64_t m = m0 + r < g.M ? m0 + r : g.M - 1, n = n0 + r < g.N ? n0 + r : g.N - 1;
-    const int8_t *pa = g.A + m * g.lda + 16 * c, *pw = g.W + n * g.ldw + 16 * c;
-    i32x4 acc = {0, 0, 0, 0};
-    for (int64_t k = 0; k < g.K; k += 64)
-        acc = mfma_i8(*reinterpret_cast<const uint4 *>(pw + k), *reinterpret_cast<const uint4 *>(pa + k), acc);
-    if (m0 + r >= g.M) return;
-    const float sa = g.a_scale[m];
-    for (int j = 0; j < 4; ++j) {
-        const int64_t col = n0 + 4 * c + j;
-        if (col < g.N) A::st(static_cast<typename A::T *>(g.C) + m * g.ldc + col, (float)acc[j] * sa * g.w_scale[col]);
+template <int I, int N, typename F> __device__ __forceinline__ void static_for(F &&f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        static_for<I + 1, N>(f);
     }
+}
+
+// Place of the 16-byte chunk c of a 64-byte LDS row r: a fragment read (16 rows, one
+// chunk each) covers all banks in every 8 lanes and in all 16.
+__device__ __forceinline__ int swizzled(int r, int c) { return c ^ (((r >> 1) ^ (r >> 3)) & 3); }
+
+// WGM x WGN waves of MT x NT tiles of 16 x 16: a workgroup's outputs are BM x BN.  K is
+// staged 64 at a time by direct global -> LDS loads into four buffers, each stage's
+// loads issued four stages before its products.  Each buffer is its own array, and the
+// stage barrier a bare s_barrier behind a wait for the next stage's loads only.  Past
+// the last stage the last one is loaded again, so that the waits are the same for every
+// stage; rows past the last are the last row again.  A stage's A fragments are read
+// behind that barrier, before the products of the stage before; the W fragments of
+// column tile j as soon as the products with the last ones are issued.
+template <int ACT, int MT, int NT, int WGM, int WGN>
+__global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArgs g) {
+    using A = Act<ACT>;
+    constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN, BK = 64, NB = 4, kWaves = WGM * WGN;
+    constexpr int kBlocksA = BM / 16 / kWaves, kBlocksW = BN / 16 / kWaves, kLoads = kBlocksA + kBlocksW;
+    static_assert(kBlocksA * 16 * kWaves == BM && kBlocksW * 16 * kWaves == BN, "whole blocks a wave");
+    __shared__ __attribute__((aligned(16))) int8_t A0[BM * BK], A1[BM * BK], A2[BM * BK], A3[BM * BK];
+    __shared__ __attribute__((aligned(16))) int8_t W0[BN * BK], W1[BN * BK], W2[BN * BK], W3[BN * BK];
+
+    const int tiles_m = (int)((g.M + BM - 1) / BM), tiles_n = (int)((g.N + BN - 1) / BN);
+    const int nwg = tiles_m * tiles_n;
+    constexpr int GM = 4;
+    int id = blockIdx.x;
+    if (nwg % 8 == 0) id = (id % 8) * (nwg / 8) + id / 8;  // contiguous tile range per XCD
+    const int group = id / (GM * tiles_n);
+    const int first_m = group * GM;
+    const int gm = (tiles_m - first_m < GM) ? tiles_m - first_m : GM;
+    const int in_group = id - group * GM * tiles_n;
+    const int64_t m0 = (int64_t)(first_m + in_group % gm) * BM, n0 = (int64_t)(in_group / gm) * BN;
+
+    const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = w % WGM, wn = w / WGM;
+    const int stages = (int)((g.K + BK - 1) / BK);
+
+    uint32_t offa[kBlocksA], offw[kBlocksW];
+#pragma unroll
+    for (int h = 0; h < kBlocksA; ++h) {
+        const int lr = 16 * (kBlocksA * w + h) + lane / 4;
+        const int64_t row = m0 + lr < g.M ? lr : g.M - 1 - m0;
+        offa[h] = (uint32_t)(row * g.lda) + 16u * swizzled(lr, lane % 4);
+    }
+#pragma unroll
+    for (int h = 0; h < kBlocksW; ++h) {
+        const int lr = 16 * (kBlocksW * w + h) + lane / 4;
+        const int64_t row = n0 + lr < g.N ? lr : g.N - 1 - n0;
+        offw[h] = (uint32_t)(row * g.ldw) + 16u * swizzled(lr, lane % 4);
+    }
+    const int8_t *Ab = g.A + m0 * g.lda, *Wb = g.W + n0 * g.ldw;
+    auto bufs = [&](auto bc) {
+        constexpr int b = decltype(bc)::value;
+        int8_t *a = b == 0 ? A0 : b == 1 ? A1 : b == 2 ? A2 : A3;
+        int8_t *ww = b == 0 ? W0 : b == 1 ? W1 : b == 2 ? W2 : W3;
+        return std::make_pair(a, ww);
+    };
+    auto issue = [&](int8_t *as, int8_t *ws, int stage) {
+        const int64_t k0 = (int64_t)(stage < stages ? stage : stages - 1) * BK;
+#pragma unroll
+        for (int h = 0; h < kBlocksA; ++h)
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(Ab + k0 + offa[h]),
+                                             &as[16 * (kBlocksA * w + h) * BK], 16, 0, 0);
+#pragma unroll
+        for (int h = 0; h < kBlocksW; ++h)
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(Wb + k0 + offw[h]),
+                                             &ws[16 * (kBlocksW * w + h) * BK], 16, 0, 0);
+    };
+    auto frag = [&](const int8_t *buf, int row0) {
+        const int r = row0 + lane % 16;
+        return *reinterpret_cast<const uint4 *>(&buf[r * BK + 16 * swizzled(r, lane / 16)]);
+    };
+    uint4 af[2][MT], wf[NT];
+    i32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // (an s_waitcnt immediate: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8)
+    auto stage_barrier = [&](auto vc) {
+        constexpr int v = decltype(vc)::value;
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((v & 15) | (v >> 4) << 14 | (0x7 << 4));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    };
+    issue(A0, W0, 0);
+    issue(A1, W1, 1);
+    issue(A2, W2, 2);
+    issue(A3, W3, 3);
+    stage_barrier(std::integral_constant<int, kLoads * (NB - 1)>{});
+#pragma unroll
+    for (int i = 0; i < MT; ++i) af[0][i] = frag(A0, 16 * (MT * wm + i));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) wf[j] = frag(W0, 16 * (NT * wn + j));
+    // the W fragment is the first operand, so the C tiles are held transposed: lane l
+    // holds row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3
+    for (int s0 = 0; s0 < stages; s0 += NB)
+        static_for<0, NB>([&](auto sc) {
+            constexpr int b = decltype(sc)::value, cur = b % 2, next = (b + 1) % NB;
+            if (s0 + b >= stages) return;
+            stage_barrier(std::integral_constant<int, kLoads * (NB - 2)>{});
+            const auto here = bufs(sc), ahead = bufs(std::integral_constant<int, next>{});
+            issue(here.first, here.second, s0 + b + NB);
+            const int8_t *as = ahead.first, *ws = ahead.second;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) af[1 - cur][i] = frag(as, 16 * (MT * wm + i));
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[i][j] = mfma_i8(wf[j], af[cur][i], acc[i][j]);
+                wf[j] = frag(ws, 16 * (NT * wn + j));
+            }
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+
+    const int64_t row0 = m0 + 16 * MT * wm, col0 = n0 + 16 * NT * wn;
+    float sa[MT], sw[NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = row0 + 16 * i + lane % 16;
+        sa[i] = g.a_scale[m < g.M ? m : g.M - 1];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = col0 + 16 * j + 4 * (lane / 16) + e;
+            sw[j][e] = g.w_scale[n < g.N ? n : g.N - 1];
+        }
+    if constexpr (ACT == kF32) {
+        const bool pieces = g.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int64_t m = row0 + 16 * i + lane % 16;
+            if (m >= g.M) continue;
+            float *C = static_cast<float *>(g.C) + m * g.ldc;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int64_t n = col0 + 16 * j + 4 * (lane / 16);
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
+                if (pieces && n + 4 <= g.N) {
+                    *reinterpret_cast<float4 *>(C + n) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < g.N) C[n + e] = y[e];
+                }
+            }
+        }
+    } else {
+        // through the LDS: each wave writes its tile into one of the stage arrays and
+        // reads it back as whole rows, so that a store writes rows' neighbouring columns.
+        // Chunk c of 16 bytes is at c ^ (row % chunks).
+        constexpr int kCols = 16 * NT, kChunks = kCols / 8;
+        static_assert(16 * MT * kCols * 2 <= (BM < BN ? BM : BN) * BK && kWaves <= 2 * NB, "a wave's tile in a stage array");
+        __builtin_amdgcn_s_waitcnt(0);  // the loads past the last stage
+        __syncthreads();
+        int8_t *stage = w == 0 ? A0 : w == 1 ? A1 : w == 2 ? A2 : w == 3 ? A3 : w == 4 ? W0 : w == 5 ? W1 : w == 6 ? W2 : W3;
+        uint16_t *ob = reinterpret_cast<uint16_t *>(stage);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int row = 16 * i + lane % 16;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int chunk = 2 * j + lane / 32;
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
+                *reinterpret_cast<uint2 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks)) + 4 * (lane / 16 % 2)]) =
+                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            }
+        }
+        uint16_t *C = static_cast<uint16_t *>(g.C) + row0 * g.ldc + col0;
+        if (g.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && col0 + kCols <= g.N) {
+            constexpr int kRows = kWave / kChunks;  // rows of a store
+#pragma unroll
+            for (int t = 0; t < 16 * MT / kRows; ++t) {
+                const int row = kRows * t + lane / kChunks, chunk = lane % kChunks;
+                const uint4 v = *reinterpret_cast<const uint4 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks))]);
+                if (row0 + row < g.M) *reinterpret_cast<uint4 *>(C + (int64_t)row * g.ldc + 8 * chunk) = v;
+            }
+        } else {
+            constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
+            for (int row = lane / kAcross; row < 16 * MT; row += kRows) {
+                if (row0 + row >= g.M) break;
+#pragma unroll
+                for (int c = lane % kAcross; c < kCols; c += kAcross)
+                    if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[row * kCols + 8 * ((c / 8) ^ (row % kChunks)) + c % 8];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ products, few rows
+
+// Up to 16 MT rows: the weights are read once, by waves that each take a share of K of
+// 16 output channels, 8 steps of 64 in flight; the waves' sums join in the LDS.
+template <int ACT, int MT, int W>
+__global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g) {
+    using A = Act<ACT>;
+    constexpr int kSteps = 8;
+    __shared__ i32x4 sums[W][MT][kWave];
+    const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r = lane % 16, c = lane / 16;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + r < g.N ? n0 + r : g.N - 1;
+    const int steps = (int)((g.K + 63) / 64), share = (steps + W - 1) / W;
+    const int first = w * share, last = first + share < steps ? first + share : steps;
+    const int8_t *pw = g.W + n * g.ldw + 16 * c, *pa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = 16 * i + r < g.M ? 16 * i + r : g.M - 1;
+        pa[i] = g.A + m * g.lda + 16 * c;
+    }
+    i32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
+    for (int s = first; s < last; s += kSteps) {
+        uint4 wf[kSteps];
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const int64_t at = 64 * (int64_t)(s + k < last ? s + k : last - 1);
+            wf[k] = *reinterpret_cast<const uint4 *>(pw + at);
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if (s + k >= last) break;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                acc[i] = mfma_i8(wf[k], *reinterpret_cast<const uint4 *>(pa[i] + 64 * (int64_t)(s + k)), acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sums[w][i][lane] = acc[i];
+    __syncthreads();
+    for (int i = w; i < MT; i += W) {
+        i32x4 t = sums[0][i][lane];
+#pragma unroll
+        for (int k = 1; k < W; ++k) t += sums[k][i][lane];
+        const int64_t m = 16 * i + r;
+        if (m >= g.M) continue;
+        const float sa = g.a_scale[m];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t col = n0 + 4 * c + e;
+            if (col < g.N) A::st(static_cast<typename A::T *>(g.C) + m * g.ldc + col, (float)t[e] * sa * g.w_scale[col]);
+        }
+    }
+}
+
+template <int ACT, int MT, int NT, int WGM, int WGN> void launch_tiles(const Int8GemmArgs &g, hipStream_t stream) {
+    constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN;
+    const dim3 grid((unsigned)((g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
+    dense_int8_kernel<ACT, MT, NT, WGM, WGN><<<grid, WGM * WGN * kWave, 0, stream>>>(g);
+}
+
+template <int ACT> void launch_product(const Int8GemmArgs &g, hipStream_t stream) {
+#ifdef FORCE
+    if (FORCE == 1) return launch_tiles<ACT, 4, 8, 4, 2>(g, stream);
+    if (FORCE == 2) return launch_tiles<ACT, 4, 4, 2, 2>(g, stream);
+    if (FORCE == 3) return launch_tiles<ACT, 2, 2, 2, 2>(g, stream);
+#endif
+    const dim3 few((unsigned)((g.N + 15) / 16));
+    if (g.M <= 16) return dense_int8_few_kernel<ACT, 1, 4><<<few, 4 * kWave, 0, stream>>>(g);
+    if (g.M <= 32) return dense_int8_few_kernel<ACT, 2, 4><<<few, 4 * kWave, 0, stream>>>(g);
+    if (g.M <= 64) return dense_int8_few_kernel<ACT, 4, 4><<<few, 4 * kWave, 0, stream>>>(g);
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
+    if (tiles(256, 256) >= 256) return launch_tiles<ACT, 4, 8, 4, 2>(g, stream);
+    if (tiles(128, 128) >= 256) return launch_tiles<ACT, 4, 4, 2, 2>(g, stream);
+    launch_tiles<ACT, 2, 2, 2, 2>(g, stream);
 }
 
 }  // namespace
@@ -97,9 +364,8 @@ hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_dense_int8(const Int8GemmArgs &g, hipStream_t stream) {
-    const dim3 grid((unsigned)((g.M + 15) / 16 * ((g.N + 15) / 16)));
-    if (g.act == kBF16) dense_int8_kernel<kBF16><<<grid, 64, 0, stream>>>(g);
-    else dense_int8_kernel<kF32><<<grid, 64, 0, stream>>>(g);
+    if (g.act == kBF16) launch_product<kBF16>(g, stream);
+    else launch_product<kF32>(g, stream);
     return hipGetLastError();
 }
 

@@ -641,7 +641,7 @@ int places_of(int64_t L, int run) { return L > 0 ? (int)((L + run - 1) / run) : 
 // backward over 8 x 2048 x 2048: 5 us of 80 less), else not, since backward finds there
 // what the prompt has read (6 x 1501 x 1000 float32: 77 us for both against 99).
 bool read_once(const RecurArgs &a, int tensors) {
-    return a.B * a.L * a.D * (a.act == kBF16 ? 2 : 4) * (tensors - (a.q ? 0 : 1)) > (int64_t(256) << 20);
+    return a.B * a.L * a.D * (a.act == kBF16 ? 2 : 4) * (tensors - (a.q ? 0 : 1)) >= (int64_t(256) << 20);
 }
 
 // Pairs of bfloat16 channels a lane (4 bytes, as one float32 channel) where all rows have

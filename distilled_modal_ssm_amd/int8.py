@@ -65,7 +65,8 @@ class Int8Dense:
                 out = self.torch.empty((M, self.N), dtype=x.dtype, device=self.device)
             ldo, otype = self._rows("out", out, M, self.N)
             at = -(-M * self.ld // 256) * 256  # the rows' scales behind the rows
-            ws = hb._scratch(self._ws, at + 4 * M, stream, self.device).data_ptr()
+            scratch = hb._scratch(self._ws, at + 4 * M, stream, self.device)
+            ws = scratch.data_ptr()
             # (straight to the C entry points: a token's call counts in microseconds)
             hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, self.ld,
                                      ws + at, stream), "hyena_quantize_rows")

@@ -38,7 +38,9 @@ class GatedRecurrence:
         self._ws = {}  # scratch memory of each stream; a captured graph has its own
         self._ws_bytes = {}  # of each length
         self._state_shape = (self.B, self.D)
-        self._token, self._desc_ref = hb.load().hyena_recurrence_decode_step, ctypes.byref(self.desc)
+        lib = hb.load()
+        self._prompt, self._token, self._desc_ref = (lib.hyena_recurrence_prefill, lib.hyena_recurrence_decode_step,
+                                                     ctypes.byref(self.desc))
 
     def new_state(self):
         return self.torch.zeros(self._state_shape, dtype=self.torch.float32, device=self.device)
@@ -51,6 +53,8 @@ class GatedRecurrence:
     def _workspace(self, L, stream):
         n = self._ws_bytes.get(L)
         if n is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
             n = self._ws_bytes[L] = hb.hyena_recurrence_workspace(self.desc, L)
         return (hb._scratch(self._ws, n, stream, self.device), n) if n else (None, 0)
 
@@ -59,14 +63,18 @@ class GatedRecurrence:
         if t.dtype != self.tdtype or t.shape != shape or t.device != self.device:
             raise ValueError(f"{name}: need {self.tdtype} {tuple(shape)} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
+        strides = t.stride()
+        ld = strides[-2]
+        if len(shape) == 3 and ld >= self.D and strides == (shape[1] * ld, ld, 1):
+            return ld
         if t.is_contiguous():
             return self.D
         if len(shape) == 3:
             ld = hb._row_stride(t, ())
         else:
-            if self.D > 1 and t.stride(1) != 1:
+            if self.D > 1 and strides[1] != 1:
                 raise ValueError(f"{name}: rows need unit element stride")
-            ld = t.stride(0) if self.B > 1 else self.D
+            ld = ld if self.B > 1 else self.D
         if ld < self.D:
             raise ValueError(f"{name}: rows overlap")
         return ld
@@ -105,8 +113,14 @@ class GatedRecurrence:
             else:
                 self._f32("state_out", state_out, self._state_shape)
             ws, n = self._workspace(L, stream)
-            hb.hyena_recurrence_prefill(self.desc, L, lengths, q, ld_q, g, ld_g, v, ld_v, y, self._rows("y", y, shape),
-                                        state_in, state_out, chunk_states, ws, n, stream)
+            # (straight to the C entry point: a few tokens' call counts in microseconds)
+            hb._check(self._prompt(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
+                                   None if q is None else q.data_ptr(), ld_q, g.data_ptr(), ld_g, v.data_ptr(), ld_v,
+                                   y.data_ptr(), self._rows("y", y, shape),
+                                   None if state_in is None else state_in.data_ptr(), state_out.data_ptr(),
+                                   None if chunk_states is None else chunk_states.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), n, stream),
+                      "hyena_recurrence_prefill")
         return y, state_out
 
     def backward(self, q, g, v, dy, chunk_states, lengths=None, dstate_out=None, out=None, stream=None):
