@@ -79,6 +79,7 @@ EXPORTS = (
     "hyena_recurrence_prefill",
     "hyena_recurrence_backward",
     "hyena_recurrence_decode_step",
+    "hyena_int8_bytes",
     "hyena_quantize_rows",
     "hyena_dense_int8",
     "hyena_draft_verify_workspace",
@@ -219,8 +220,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "hyena_recurrence_backward": ([R, i64, p, p, i64, p, i64, p, i64, p, i64, p, p, p, i64, p, i64, p, i64, p, p,
                                            sz, p], ctypes.c_int),
             "hyena_recurrence_decode_step": ([R, p, i64, p, i64, p, i64, p, i64, p, p, p, p], ctypes.c_int),
-            "hyena_quantize_rows": ([i64, i64, i32, p, i64, i32, f32, p, i64, p, p], ctypes.c_int),
-            "hyena_dense_int8": ([i64, i64, i64, p, i64, p, p, i64, p, i32, p, i64, p], ctypes.c_int),
+            "hyena_int8_bytes": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_quantize_rows": ([i64, i64, i32, p, i64, i32, f32, p, p, p], ctypes.c_int),
+            "hyena_dense_int8": ([i64, i64, i64, p, p, p, p, i32, p, i64, p], ctypes.c_int),
             "hyena_draft_verify_workspace": ([i64, i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
             "hyena_draft_verify": ([i64, i64, i64, i32, p, i64, p, i64, p, p, p, p, p, p, sz, p], ctypes.c_int),
         }
@@ -622,14 +624,19 @@ def hyena_recurrence_decode_step(desc: hm_recurrence_desc, q, ld_q, g, ld_g, v, 
     _check(st, "hyena_recurrence_decode_step")
 
 
-def hyena_quantize_rows(M, K, dtype, x, ldx, rms, eps, q, ldq, scale, stream=None) -> None:
-    st = load().hyena_quantize_rows(M, K, dtype, _ptr(x), ldx, int(rms), eps, _ptr(q), ldq, _ptr(scale),
-                                    _stream(stream))
+def hyena_int8_bytes(M: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_int8_bytes(M, K, ctypes.byref(n)), "hyena_int8_bytes")
+    return n.value
+
+
+def hyena_quantize_rows(M, K, dtype, x, ldx, rms, eps, q, scale, stream=None) -> None:
+    st = load().hyena_quantize_rows(M, K, dtype, _ptr(x), ldx, int(rms), eps, _ptr(q), _ptr(scale), _stream(stream))
     _check(st, "hyena_quantize_rows")
 
 
-def hyena_dense_int8(M, N, K, A, lda, a_scale, W, ldw, w_scale, dtype, C, ldc, stream=None) -> None:
-    st = load().hyena_dense_int8(M, N, K, _ptr(A), lda, _ptr(a_scale), _ptr(W), ldw, _ptr(w_scale), dtype, _ptr(C), ldc,
+def hyena_dense_int8(M, N, K, A, a_scale, W, w_scale, dtype, C, ldc, stream=None) -> None:
+    st = load().hyena_dense_int8(M, N, K, _ptr(A), _ptr(a_scale), _ptr(W), _ptr(w_scale), dtype, _ptr(C), ldc,
                                  _stream(stream))
     _check(st, "hyena_dense_int8")
 

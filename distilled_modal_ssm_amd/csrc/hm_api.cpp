@@ -1145,38 +1145,51 @@ hm_status hyena_recurrence_decode_step(const hm_recurrence_desc *desc, const voi
     return hm::launch_recurrence_decode(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
-hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps,
-                              int8_t *q, int64_t ldq, float *scale, void *stream) {
+// Rows and columns that 8-bit integers are held for.
+static hm_status check_int8(int64_t M, int64_t K) {
     if (M < 0 || K < 1) return HM_ERR_INVALID_ARG;
+    return K > HM_INT8_MAX_K || M >= INT32_MAX - 511 ? HM_ERR_UNSUPPORTED : HM_OK;
+}
+
+hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes) {
+    const hm_status st = check_int8(M, K);
+    if (st != HM_OK) return st;
+    if (!bytes) return HM_ERR_INVALID_ARG;
+    *bytes = (size_t)((M + 15) / 16) * (size_t)((K + 63) / 64) * 1024;
+    return HM_OK;
+}
+
+hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps,
+                              int8_t *q, float *scale, void *stream) {
+    const hm_status st = check_int8(M, K);
+    if (st != HM_OK) return st;
     if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
     if (rms && !(std::isfinite(eps) && eps >= 0.0f)) return HM_ERR_INVALID_ARG;
-    if (K > HM_INT8_MAX_K || M > INT32_MAX) return HM_ERR_UNSUPPORTED;
-    if (ldx < K || ldq < K) return HM_ERR_INVALID_ARG;
-    if (ldq % 64 != 0) return HM_ERR_UNSUPPORTED;
+    if (ldx < K) return HM_ERR_INVALID_ARG;
     if (M == 0) return HM_OK;
     if (!x || !q || !scale) return HM_ERR_INVALID_ARG;
     if (!aligned(x, dtype == HM_BF16 ? 2 : 4) || !aligned(q, 16) || !aligned(scale, 4)) return HM_ERR_UNSUPPORTED;
-    if (M > kMaxElems / ldx || M > kMaxElems / ldq) return HM_ERR_INVALID_ARG;
-    const hm::QuantArgs a{M, K, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, ldq, scale};
+    if (M > kMaxElems / ldx) return HM_ERR_INVALID_ARG;
+    const hm::QuantArgs a{M, K, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, scale};
     return hm::launch_quantize_rows(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
-hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *a_scale,
-                           const int8_t *W, int64_t ldw, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
-                           void *stream) {
-    if (M < 0 || N < 0 || K < 1) return HM_ERR_INVALID_ARG;
+hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, const float *a_scale, const int8_t *W,
+                           const float *w_scale, int32_t dtype, void *C, int64_t ldc, void *stream) {
+    hm_status st = check_int8(M, K);
+    if (st == HM_OK) st = check_int8(N, K);
+    if (st != HM_OK) return st;
     if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
-    if (K > HM_INT8_MAX_K || M >= INT32_MAX - 511 || N >= INT32_MAX - 511) return HM_ERR_UNSUPPORTED;
-    if (lda < K || ldw < K || ldc < N) return HM_ERR_INVALID_ARG;
-    if (lda % 64 != 0 || ldw % 64 != 0) return HM_ERR_UNSUPPORTED;
+    if (ldc < N) return HM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return HM_OK;
-    if ((M + 15) / 16 > INT32_MAX / ((N + 15) / 16)) return HM_ERR_UNSUPPORTED;
+    // fewer than 2^32 threads: 512 for 256 x 256 outputs, or 256 for 16 columns of a few rows
+    if ((M + 255) / 256 >= ((int64_t(1) << 20) + (N + 255) / 256 - 1) / ((N + 255) / 256)) return HM_ERR_UNSUPPORTED;
     if (!A || !a_scale || !W || !w_scale || !C) return HM_ERR_INVALID_ARG;
     if (!aligned(A, 16) || !aligned(W, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
         !aligned(C, dtype == HM_BF16 ? 2 : 4))
         return HM_ERR_UNSUPPORTED;
-    if (M > kMaxElems / lda || N > kMaxElems / ldw || M > kMaxElems / ldc) return HM_ERR_INVALID_ARG;
-    const hm::Int8GemmArgs a{M, N, K, A, lda, a_scale, W, ldw, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
+    if (M > kMaxElems / ldc) return HM_ERR_INVALID_ARG;
+    const hm::Int8GemmArgs a{M, N, K, A, a_scale, W, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
     return hm::launch_dense_int8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 

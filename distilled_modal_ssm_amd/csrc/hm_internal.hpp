@@ -424,16 +424,13 @@ struct QuantArgs {
     bool rms;
     float eps;
     int8_t *q;
-    int64_t ldq;
     float *scale;
 };
 struct Int8GemmArgs {
     int64_t M, N, K;
     const int8_t *A;
-    int64_t lda;
     const float *a_scale;
     const int8_t *W;
-    int64_t ldw;
     const float *w_scale;
     int act;
     void *C;

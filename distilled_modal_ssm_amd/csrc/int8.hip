@@ -15,6 +15,17 @@ __device__ __forceinline__ i32x4 mfma_i8(uint4 a, uint4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
+// Rows are held in blocks of 16 rows by 64 columns, 1024 bytes each.  Place of the
+// 16-byte chunk c of a block's row r: the LDS serves a 16-byte read of a wave 16 lanes at
+// a time, from 0-3, 12-15, 20-23 and 24-27 on; with a fragment's rows l % 16 and chunks
+// l / 16, those and all others that go together fall on all 64 banks.
+__device__ __forceinline__ int place(int r, int c) {
+    const int fours = (r >> 2) & 3;  // 0 1 2 3 -> 0 2 3 1
+    return 64 * r + 16 * (c ^ (((fours << 1) ^ (3 * (fours >> 1))) & 3));
+}
+
+__device__ __forceinline__ int64_t block_of(int64_t row, int64_t K) { return (row >> 4) * ((K + 63) >> 6) * 1024; }
+
 // ------------------------------------------------------------------ rows in 8 bits
 
 // rint(127 x / amax), the integer of the exact quotient: in float32, off by less than
@@ -27,46 +38,143 @@ __device__ __forceinline__ int quantized(float x, float amax, float inverse) {
     return (int)rint((double)x * 127.0 / (double)amax);
 }
 
-// One workgroup a row: the largest magnitude (as bits, where NaN and infinities come
-// last) and the sum of squares, then the row again out of the cache.
-template <int ACT>
+struct RowStat {
+    uint32_t top;  // bits of the largest magnitude; NaN and infinities come last
+    float sum;     // of squares
+};
+
+__device__ __forceinline__ void take(RowStat &s, float x) {
+    const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
+    s.top = bits > s.top ? bits : s.top;
+    s.sum = fmaf(x, x, s.sum);
+}
+
+// The statistics of W waves' row, joined in all of them.
+template <int W> __device__ __forceinline__ RowStat joined(RowStat s) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) {
+        const uint32_t top = __shfl_xor(s.top, m);
+        s.top = top > s.top ? top : s.top;
+        s.sum += __shfl_xor(s.sum, m);
+    }
+    if constexpr (W > 1) {
+        __shared__ RowStat all[W];
+        if (threadIdx.x % kWave == 0) all[threadIdx.x / kWave] = s;
+        __syncthreads();
+        s = all[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            s.top = all[w].top > s.top ? all[w].top : s.top;
+            s.sum += all[w].sum;
+        }
+    }
+    return s;
+}
+
+__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s) {
+    float scale = __uint_as_float(s.top) / 127.0f;
+    if (a.rms) scale = scale / sqrtf(s.sum / (float)a.K + a.eps);
+    return s.top < 0x7f800000u ? scale : __builtin_nanf("");
+}
+
+// E values' integers as bytes.
+template <int E> __device__ __forceinline__ void quantize(const float (&x)[E], float amax, float inverse, int (&n)[E]) {
+    bool sure = amax > 1e-30f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float r = x[e] * inverse, near = rintf(r);
+        n[e] = (int)near;
+        sure = sure && fabsf(r - near) < 0.4999f;
+    }
+    if (!sure) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) n[e] = quantized(x[e], amax, inverse);
+    }
+}
+
+// A row in the registers of W waves, N pieces of 16 bytes a lane, read once.
+template <int ACT, int N, int W>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
+    constexpr int EB = Act<ACT>::kBytes, E = 16 / EB, kLanes = W * kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t m = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    if (m >= a.M) return;
+    const int lane = W > 1 ? (int)threadIdx.x : (int)threadIdx.x % kWave, K = (int)a.K;
+    const auto x = make_region(static_cast<const unsigned char *>(a.x) + m * a.ldx * EB, (uint32_t)K * EB);
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 piece[N];  // what is past the row's end reads as 0
+#pragma unroll
+    for (int k = 0; k < N; ++k) piece[k] = __builtin_amdgcn_raw_buffer_load_b128(x, 16 * (k * kLanes + lane), 0, 0);
+    auto values = [&](int k, float (&v)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if constexpr (ACT == kBF16) v[e] = e % 2 ? bf16_hi(piece[k][e / 2]) : bf16_lo(piece[k][e / 2]);
+            else v[e] = __uint_as_float(piece[k][e]);
+        }
+    };
+    RowStat s{0, 0.0f};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float v[E];
+        values(k, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) take(s, v[e]);
+    }
+    s = joined<W>(s);
+    const bool some = s.top > 0 && s.top < 0x7f800000u;
+    const float amax = __uint_as_float(s.top), inverse = 127.0f / amax;
+    const int end = (K + 63) / 64 * 64;
+    int8_t *q = a.q + block_of(m, K);
+    const int r = (int)(m % 16);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int col = E * (k * kLanes + lane), at = col / 64 * 1024 + place(r, col % 64 / 16) + col % 16;
+        if (col >= end) break;
+        uint32_t out[E / 4] = {};
+        if (some) {
+            float v[E];
+            int n[E];
+            values(k, v);
+            quantize(v, amax, inverse, n);
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[e / 4] |= (uint32_t)(n[e] & 255) << (8 * (e % 4));
+        }
+        if constexpr (E == 8) *reinterpret_cast<uint2 *>(q + at) = make_uint2(out[0], out[1]);
+        else *reinterpret_cast<uint32_t *>(q + at) = out[0];
+    }
+    if (lane == 0) a.scale[m] = row_scale(a, s);
+}
+
+// Rows of any alignment and length: one workgroup a row, which is read twice.
+template <int ACT>
+__global__ __launch_bounds__(256) void quantize_any_rows_kernel(QuantArgs a) {
     using A = Act<ACT>;
-    __shared__ uint32_t most[4];
-    __shared__ float sums[4];
     const int64_t m = blockIdx.x;
     const typename A::T *x = static_cast<const typename A::T *>(a.x) + m * a.ldx;
-    int8_t *q = a.q + m * a.ldq;
-    const int tid = threadIdx.x, K = (int)a.K;
-    uint32_t top = 0;
-    float sum = 0.0f;
-    for (int k = tid; k < K; k += 256) {
-        const float v = A::ld(x + k);
-        const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
-        top = bits > top ? bits : top;
-        sum = fmaf(v, v, sum);
-    }
-    for (int s = 32; s > 0; s >>= 1) {
-        const uint32_t other = __shfl_xor(top, s);
-        top = other > top ? other : top;
-        sum += __shfl_xor(sum, s);
-    }
-    if (tid % 64 == 0) {
-        most[tid / 64] = top;
-        sums[tid / 64] = sum;
-    }
-    __syncthreads();
-    for (int w = 0; w < 4; ++w) top = most[w] > top ? most[w] : top;
-    sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-    const bool whole = top < 0x7f800000u;
-    const float amax = __uint_as_float(top), inverse = 127.0f / amax;
+    int8_t *q = a.q + block_of(m, a.K);
+    const int tid = threadIdx.x, K = (int)a.K, r = (int)(m % 16);
+    RowStat s{0, 0.0f};
+    for (int k = tid; k < K; k += 256) take(s, A::ld(x + k));
+    s = joined<4>(s);
+    const bool some = s.top > 0 && s.top < 0x7f800000u;
+    const float amax = __uint_as_float(s.top), inverse = 127.0f / amax;
     const int end = (K + 63) / 64 * 64;
-    for (int k = tid; k < end; k += 256) q[k] = k < K && whole && top > 0 ? (int8_t)quantized(A::ld(x + k), amax, inverse) : 0;
-    if (tid == 0) {
-        float s = amax / 127.0f;
-        if (a.rms) s = s / sqrtf(sum / (float)K + a.eps);
-        a.scale[m] = whole ? s : __builtin_nanf("");
-    }
+    for (int k = tid; k < end; k += 256)
+        q[k / 64 * 1024 + place(r, k % 64 / 16) + k % 16] = k < K && some ? (int8_t)quantized(A::ld(x + k), amax, inverse) : 0;
+    if (tid == 0) a.scale[m] = row_scale(a, s);
+}
+
+template <int ACT> void launch_quantize(const QuantArgs &a, hipStream_t stream) {
+    constexpr int EB = Act<ACT>::kBytes, E = 16 / EB;
+    const dim3 rows((unsigned)a.M);
+    // (a piece's bounds count 4 bytes)
+    const bool pieces = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * EB % 16 == 0 || a.M == 1) && a.K * EB % 4 == 0;
+    if (!pieces || a.K > 16 * E * 256) return quantize_any_rows_kernel<ACT><<<rows, 256, 0, stream>>>(a);
+    if (a.M >= 1024 && a.K <= 4 * E * kWave)
+        return quantize_rows_kernel<ACT, 4, 1><<<dim3((unsigned)((a.M + 3) / 4)), 256, 0, stream>>>(a);
+    if (a.K <= E * 256) return quantize_rows_kernel<ACT, 1, 4><<<rows, 256, 0, stream>>>(a);
+    if (a.K <= 4 * E * 256) return quantize_rows_kernel<ACT, 4, 4><<<rows, 256, 0, stream>>>(a);
+    quantize_rows_kernel<ACT, 16, 4><<<rows, 256, 0, stream>>>(a);
 }
 
 // ------------------------------------------------------------------ products, tiles
@@ -78,10 +186,6 @@ template <int I, int N, typename F> __device__ __forceinline__ void static_for(F
     }
 }
 
-// Place of the 16-byte chunk c of a 64-byte LDS row r: a fragment read (16 rows, one
-// chunk each) covers all banks in every 8 lanes and in all 16.
-__device__ __forceinline__ int swizzled(int r, int c) { return c ^ (((r >> 1) ^ (r >> 3)) & 3); }
-
 // WGM x WGN waves of MT x NT tiles of 16 x 16: a workgroup's outputs are BM x BN.  K is
 // staged 64 at a time by direct global -> LDS loads into four buffers, each stage's
 // loads issued four stages before its products.  Each buffer is its own array, and the
@@ -90,14 +194,14 @@ __device__ __forceinline__ int swizzled(int r, int c) { return c ^ (((r >> 1) ^ 
 // stage; rows past the last are the last row again.  A stage's A fragments are read
 // behind that barrier, before the products of the stage before; the W fragments of
 // column tile j as soon as the products with the last ones are issued.
-template <int ACT, int MT, int NT, int WGM, int WGN>
-__global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArgs g) {
+template <int ACT, int MT, int NT, int WGM, int WGN, int NB>
+__global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : 2) void dense_int8_kernel(Int8GemmArgs g) {
     using A = Act<ACT>;
-    constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN, BK = 64, NB = 4, kWaves = WGM * WGN;
+    constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN, BK = 64, kWaves = WGM * WGN;
     constexpr int kBlocksA = BM / 16 / kWaves, kBlocksW = BN / 16 / kWaves, kLoads = kBlocksA + kBlocksW;
     static_assert(kBlocksA * 16 * kWaves == BM && kBlocksW * 16 * kWaves == BN, "whole blocks a wave");
-    __shared__ __attribute__((aligned(16))) int8_t A0[BM * BK], A1[BM * BK], A2[BM * BK], A3[BM * BK];
-    __shared__ __attribute__((aligned(16))) int8_t W0[BN * BK], W1[BN * BK], W2[BN * BK], W3[BN * BK];
+    __shared__ __attribute__((aligned(16))) int8_t A0[BM * BK], A1[BM * BK], A2[BM * BK], A3[NB > 3 ? BM * BK : 16];
+    __shared__ __attribute__((aligned(16))) int8_t W0[BN * BK], W1[BN * BK], W2[BN * BK], W3[NB > 3 ? BN * BK : 16];
 
     const int tiles_m = (int)((g.M + BM - 1) / BM), tiles_n = (int)((g.N + BN - 1) / BN);
     const int nwg = tiles_m * tiles_n;
@@ -114,20 +218,18 @@ __global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArg
     const int wm = w % WGM, wn = w / WGM;
     const int stages = (int)((g.K + BK - 1) / BK);
 
-    uint32_t offa[kBlocksA], offw[kBlocksW];
+    // the wave's blocks of 16 rows (the last one again past the end) and the lane's 16 bytes
+    const int8_t *pa[kBlocksA], *pw[kBlocksW];
 #pragma unroll
     for (int h = 0; h < kBlocksA; ++h) {
-        const int lr = 16 * (kBlocksA * w + h) + lane / 4;
-        const int64_t row = m0 + lr < g.M ? lr : g.M - 1 - m0;
-        offa[h] = (uint32_t)(row * g.lda) + 16u * swizzled(lr, lane % 4);
+        const int64_t row = m0 + 16 * (kBlocksA * w + h);
+        pa[h] = g.A + block_of(row < g.M ? row : g.M - 1, g.K);
     }
 #pragma unroll
     for (int h = 0; h < kBlocksW; ++h) {
-        const int lr = 16 * (kBlocksW * w + h) + lane / 4;
-        const int64_t row = n0 + lr < g.N ? lr : g.N - 1 - n0;
-        offw[h] = (uint32_t)(row * g.ldw) + 16u * swizzled(lr, lane % 4);
+        const int64_t row = n0 + 16 * (kBlocksW * w + h);
+        pw[h] = g.W + block_of(row < g.N ? row : g.N - 1, g.K);
     }
-    const int8_t *Ab = g.A + m0 * g.lda, *Wb = g.W + n0 * g.ldw;
     auto bufs = [&](auto bc) {
         constexpr int b = decltype(bc)::value;
         int8_t *a = b == 0 ? A0 : b == 1 ? A1 : b == 2 ? A2 : A3;
@@ -135,20 +237,18 @@ __global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArg
         return std::make_pair(a, ww);
     };
     auto issue = [&](int8_t *as, int8_t *ws, int stage) {
-        const int64_t k0 = (int64_t)(stage < stages ? stage : stages - 1) * BK;
+        const uint32_t at = (uint32_t)(stage < stages ? stage : stages - 1) * 1024u + 16u * lane;
 #pragma unroll
         for (int h = 0; h < kBlocksA; ++h)
-            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(Ab + k0 + offa[h]),
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(pa[h] + at),
                                              &as[16 * (kBlocksA * w + h) * BK], 16, 0, 0);
 #pragma unroll
         for (int h = 0; h < kBlocksW; ++h)
-            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(Wb + k0 + offw[h]),
+            __builtin_amdgcn_global_load_lds(reinterpret_cast<const void *>(pw[h] + at),
                                              &ws[16 * (kBlocksW * w + h) * BK], 16, 0, 0);
     };
-    auto frag = [&](const int8_t *buf, int row0) {
-        const int r = row0 + lane % 16;
-        return *reinterpret_cast<const uint4 *>(&buf[r * BK + 16 * swizzled(r, lane / 16)]);
-    };
+    const int mine = place(lane % 16, lane / 16);
+    auto frag = [&](const int8_t *buf, int row0) { return *reinterpret_cast<const uint4 *>(&buf[row0 * BK + mine]); };
     uint4 af[2][MT], wf[NT];
     i32x4 acc[MT][NT];
 #pragma unroll
@@ -168,7 +268,7 @@ __global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArg
     issue(A0, W0, 0);
     issue(A1, W1, 1);
     issue(A2, W2, 2);
-    issue(A3, W3, 3);
+    if constexpr (NB > 3) issue(A3, W3, 3);
     stage_barrier(std::integral_constant<int, kLoads * (NB - 1)>{});
 #pragma unroll
     for (int i = 0; i < MT; ++i) af[0][i] = frag(A0, 16 * (MT * wm + i));
@@ -176,12 +276,13 @@ __global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArg
     for (int j = 0; j < NT; ++j) wf[j] = frag(W0, 16 * (NT * wn + j));
     // the W fragment is the first operand, so the C tiles are held transposed: lane l
     // holds row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3
-    for (int s0 = 0; s0 < stages; s0 += NB)
-        static_for<0, NB>([&](auto sc) {
+    constexpr int kTurn = NB % 2 ? 2 * NB : NB;
+    for (int s0 = 0; s0 < stages; s0 += kTurn)
+        static_for<0, kTurn>([&](auto sc) {
             constexpr int b = decltype(sc)::value, cur = b % 2, next = (b + 1) % NB;
             if (s0 + b >= stages) return;
             stage_barrier(std::integral_constant<int, kLoads * (NB - 2)>{});
-            const auto here = bufs(sc), ahead = bufs(std::integral_constant<int, next>{});
+            const auto here = bufs(std::integral_constant<int, b % NB>{}), ahead = bufs(std::integral_constant<int, next>{});
             issue(here.first, here.second, s0 + b + NB);
             const int8_t *as = ahead.first, *ws = ahead.second;
 #pragma unroll
@@ -237,41 +338,47 @@ __global__ __launch_bounds__(WGM *WGN *kWave) void dense_int8_kernel(Int8GemmArg
         // through the LDS: each wave writes its tile into one of the stage arrays and
         // reads it back as whole rows, so that a store writes rows' neighbouring columns.
         // Chunk c of 16 bytes is at c ^ (row % chunks).
-        constexpr int kCols = 16 * NT, kChunks = kCols / 8;
-        static_assert(16 * MT * kCols * 2 <= (BM < BN ? BM : BN) * BK && kWaves <= 2 * NB, "a wave's tile in a stage array");
+        constexpr int kCols = 16 * NT, kChunks = kCols / 8, kBytes = (BM < BN ? BM : BN) * BK;
+        constexpr int kPart = MT * 16 * kCols * 2 <= kBytes ? MT : kBytes / (16 * kCols * 2);  // row tiles at once
+        static_assert(kPart > 0 && MT % kPart == 0 && (NB > 3 ? kWaves <= 8 : kWaves <= 4), "a part of a wave's tile in a stage array");
         __builtin_amdgcn_s_waitcnt(0);  // the loads past the last stage
         __syncthreads();
-        int8_t *stage = w == 0 ? A0 : w == 1 ? A1 : w == 2 ? A2 : w == 3 ? A3 : w == 4 ? W0 : w == 5 ? W1 : w == 6 ? W2 : W3;
+        int8_t *stage = w == 0 ? A0 : w == 1 ? A1 : w == 2 ? A2 : w == 3 ? W0 : w == 4 ? W1 : w == 5 ? W2 : w == 6 ? W3 : A3;
         uint16_t *ob = reinterpret_cast<uint16_t *>(stage);
+        const bool pieces = g.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && col0 + kCols <= g.N;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int row = 16 * i + lane % 16;
+        for (int i0 = 0; i0 < MT; i0 += kPart) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int chunk = 2 * j + lane / 32;
-                float y[4];
+            for (int i = i0; i < i0 + kPart; ++i) {
+                const int row = 16 * (i - i0) + lane % 16;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
-                *reinterpret_cast<uint2 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks)) + 4 * (lane / 16 % 2)]) =
-                    make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                for (int j = 0; j < NT; ++j) {
+                    const int chunk = 2 * j + lane / 32;
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
+                    *reinterpret_cast<uint2 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks)) + 4 * (lane / 16 % 2)]) =
+                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                }
             }
-        }
-        uint16_t *C = static_cast<uint16_t *>(g.C) + row0 * g.ldc + col0;
-        if (g.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && col0 + kCols <= g.N) {
-            constexpr int kRows = kWave / kChunks;  // rows of a store
+            const int64_t first = row0 + 16 * i0;
+            uint16_t *C = static_cast<uint16_t *>(g.C) + first * g.ldc + col0;
+            if (pieces) {
+                constexpr int kRows = kWave / kChunks;  // rows of a store
 #pragma unroll
-            for (int t = 0; t < 16 * MT / kRows; ++t) {
-                const int row = kRows * t + lane / kChunks, chunk = lane % kChunks;
-                const uint4 v = *reinterpret_cast<const uint4 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks))]);
-                if (row0 + row < g.M) *reinterpret_cast<uint4 *>(C + (int64_t)row * g.ldc + 8 * chunk) = v;
-            }
-        } else {
-            constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
-            for (int row = lane / kAcross; row < 16 * MT; row += kRows) {
-                if (row0 + row >= g.M) break;
+                for (int t = 0; t < 16 * kPart / kRows; ++t) {
+                    const int row = kRows * t + lane / kChunks, chunk = lane % kChunks;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks))]);
+                    if (first + row < g.M) *reinterpret_cast<uint4 *>(C + (int64_t)row * g.ldc + 8 * chunk) = v;
+                }
+            } else {
+                constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
+                for (int row = lane / kAcross; row < 16 * kPart; row += kRows) {
+                    if (first + row >= g.M) break;
 #pragma unroll
-                for (int c = lane % kAcross; c < kCols; c += kAcross)
-                    if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[row * kCols + 8 * ((c / 8) ^ (row % kChunks)) + c % 8];
+                    for (int c = lane % kAcross; c < kCols; c += kAcross)
+                        if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[row * kCols + 8 * ((c / 8) ^ (row % kChunks)) + c % 8];
+                }
             }
         }
     }
@@ -288,15 +395,13 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
     __shared__ i32x4 sums[W][MT][kWave];
     const int lane = threadIdx.x % kWave, w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane % 16, c = lane / 16;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + r < g.N ? n0 + r : g.N - 1;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int mine = place(r, c);
     const int steps = (int)((g.K + 63) / 64), share = (steps + W - 1) / W;
     const int first = w * share, last = first + share < steps ? first + share : steps;
-    const int8_t *pw = g.W + n * g.ldw + 16 * c, *pa[MT];
+    const int8_t *pw = g.W + block_of(n0, g.K) + mine, *pa[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t m = 16 * i + r < g.M ? 16 * i + r : g.M - 1;
-        pa[i] = g.A + m * g.lda + 16 * c;
-    }
+    for (int i = 0; i < MT; ++i) pa[i] = g.A + block_of(16 * i < g.M ? 16 * i : g.M - 1, g.K) + mine;
     i32x4 acc[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = i32x4{0, 0, 0, 0};
@@ -304,7 +409,7 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
         uint4 wf[kSteps];
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            const int64_t at = 64 * (int64_t)(s + k < last ? s + k : last - 1);
+            const int64_t at = 1024 * (int64_t)(s + k < last ? s + k : last - 1);
             wf[k] = *reinterpret_cast<const uint4 *>(pw + at);
         }
 #pragma unroll
@@ -312,7 +417,7 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
             if (s + k >= last) break;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                acc[i] = mfma_i8(wf[k], *reinterpret_cast<const uint4 *>(pa[i] + 64 * (int64_t)(s + k)), acc[i]);
+                acc[i] = mfma_i8(wf[k], *reinterpret_cast<const uint4 *>(pa[i] + 1024 * (int64_t)(s + k)), acc[i]);
         }
     }
 #pragma unroll
@@ -333,16 +438,20 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
     }
 }
 
-template <int ACT, int MT, int NT, int WGM, int WGN> void launch_tiles(const Int8GemmArgs &g, hipStream_t stream) {
+template <int ACT, int MT, int NT, int WGM, int WGN, int NB = 4> void launch_tiles(const Int8GemmArgs &g, hipStream_t stream) {
     constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN;
     const dim3 grid((unsigned)((g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
-    dense_int8_kernel<ACT, MT, NT, WGM, WGN><<<grid, WGM * WGN * kWave, 0, stream>>>(g);
+    dense_int8_kernel<ACT, MT, NT, WGM, WGN, NB><<<grid, WGM * WGN * kWave, 0, stream>>>(g);
 }
 
 template <int ACT> void launch_product(const Int8GemmArgs &g, hipStream_t stream) {
 #ifdef FORCE
     if (FORCE == 1) return launch_tiles<ACT, 4, 8, 4, 2>(g, stream);
     if (FORCE == 2) return launch_tiles<ACT, 4, 4, 2, 2>(g, stream);
+    if (FORCE == 4) return launch_tiles<ACT, 8, 8, 2, 2>(g, stream);
+    if (FORCE == 5) return launch_tiles<ACT, 8, 4, 2, 4>(g, stream);
+    if (FORCE == 6) return launch_tiles<ACT, 8, 4, 2, 2, 3>(g, stream);
+    if (FORCE == 7) return launch_tiles<ACT, 4, 8, 2, 2, 3>(g, stream);
     if (FORCE == 3) return launch_tiles<ACT, 2, 2, 2, 2>(g, stream);
 #endif
     const dim3 few((unsigned)((g.N + 15) / 16));
@@ -358,8 +467,8 @@ template <int ACT> void launch_product(const Int8GemmArgs &g, hipStream_t stream
 }  // namespace
 
 hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream) {
-    if (a.act == kBF16) quantize_rows_kernel<kBF16><<<dim3((unsigned)a.M), 256, 0, stream>>>(a);
-    else quantize_rows_kernel<kF32><<<dim3((unsigned)a.M), 256, 0, stream>>>(a);
+    if (a.act == kBF16) launch_quantize<kBF16>(a, stream);
+    else launch_quantize<kF32>(a, stream);
     return hipGetLastError();
 }
 

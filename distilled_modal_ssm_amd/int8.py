@@ -14,8 +14,8 @@ class Int8Dense:
     """y = x W^T of a weight W [outputs][inputs] in 8-bit integers.
 
     weight: float32 or bfloat16 rows with unit element stride on the GPU, read
-    here once.  ``weight8`` [outputs][ld] int8 and ``weight_scale`` [outputs]
-    hold it (columns past ``inputs`` are 0).
+    here once, on the given or the current stream.  ``weight8`` (int8, in the
+    library's blocks) and ``weight_scale`` [outputs] hold it.
     """
 
     def __init__(self, weight, stream=None):
@@ -27,17 +27,16 @@ class Int8Dense:
         self.N, self.K = int(weight.shape[0]), int(weight.shape[1])
         if self.K < 1 or self.K > hb.HM_INT8_MAX_K:
             raise ValueError(f"1 to {hb.HM_INT8_MAX_K} inputs, got {self.K}")
-        self.ld = -(-self.K // 64) * 64
+        self._block_row = hb.hyena_int8_bytes(16, self.K)
         self._types = {torch.float32: hb.HM_F32, torch.bfloat16: hb.HM_BF16}
         self._ws = {}  # scratch memory of each stream; a captured graph has its own
         lib = hb.load()
         self._quantize, self._product = lib.hyena_quantize_rows, lib.hyena_dense_int8
         ld, dtype = self._rows("weight", weight, self.N, self.K)
         with hb._On(self.device, stream) as s:
-            self.weight8 = torch.empty((self.N, self.ld), dtype=torch.int8, device=self.device)
+            self.weight8 = torch.empty(hb.hyena_int8_bytes(self.N, self.K), dtype=torch.int8, device=self.device)
             self.weight_scale = torch.empty(self.N, dtype=torch.float32, device=self.device)
-            hb.hyena_quantize_rows(self.N, self.K, dtype, weight, ld, 0, 0.0, self.weight8, self.ld, self.weight_scale,
-                                   s)
+            hb.hyena_quantize_rows(self.N, self.K, dtype, weight, ld, 0, 0.0, self.weight8, self.weight_scale, s)
 
     def _rows(self, name, t, rows, width):
         """Row stride and type of float rows [rows][width]."""
@@ -64,13 +63,13 @@ class Int8Dense:
             if out is None:
                 out = self.torch.empty((M, self.N), dtype=x.dtype, device=self.device)
             ldo, otype = self._rows("out", out, M, self.N)
-            at = -(-M * self.ld // 256) * 256  # the rows' scales behind the rows
+            at = -(-M // 16) * self._block_row  # the rows' scales behind the rows
             scratch = hb._scratch(self._ws, at + 4 * M, stream, self.device)
             ws = scratch.data_ptr()
             # (straight to the C entry points: a token's call counts in microseconds)
-            hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, self.ld,
-                                     ws + at, stream), "hyena_quantize_rows")
-            hb._check(self._product(M, self.N, self.K, ws, self.ld, ws + at, self.weight8.data_ptr(), self.ld,
+            hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, ws + at,
+                                     stream), "hyena_quantize_rows")
+            hb._check(self._product(M, self.N, self.K, ws, ws + at, self.weight8.data_ptr(),
                                     self.weight_scale.data_ptr(), otype, out.data_ptr(), ldo, stream),
                       "hyena_dense_int8")
         return out

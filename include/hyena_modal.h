@@ -771,33 +771,40 @@ hm_status hyena_recurrence_decode_step(const hm_recurrence_desc *desc, const voi
 #define HM_INT8_MAX_K 131072 /* most inputs: sums of products stay below 2^31 */
 
 /*
+ * Bytes of M rows of K 8-bit integers as the two calls below hold them: in blocks of 16
+ * rows by 64 columns, each block 1024 bytes, all columns of 16 rows after each other,
+ * M rounded up to 16 and K to 64.  Row r's columns 16 c .. 16 c + 15 of a block are at
+ * byte 64 r + 16 (c ^ s[r / 4]) of it, s = {0, 2, 3, 1}.  (A block is what a wave loads
+ * at once, and lies in the LDS as in memory.)  Pure host computation.
+ */
+hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes);
+
+/*
  * Rows in 8-bit integers, each with a scale of its own:
  *     amax = max_k |x[m][k]|,  q[m][k] = rint(127 x[m][k] / amax) (ties to even),
  *     scale[m] = amax / 127,  or with rms != 0  amax / 127 / sqrt(mean_k x^2 + eps).
  * The integers are those of the exact quotient.  A row of zeros gets zeros and
  * scale 0; a row with a value that is not finite gets zeros and scale NaN.
- *   x [M][ldx] of dtype (hm_dtype), K columns;  q [M][ldq] bytes, columns K up to
- *   the next multiple of 64 are set to 0 (the products read them);  scale [M].
+ *   x [M][ldx] of dtype (hm_dtype), K columns;  q  hyena_int8_bytes bytes, columns from
+ *   K on set to 0, rows from M on left as they are;  scale [M].
  * Tokens (rows of activations) and output channels (rows of W) alike.
- * 1 <= K <= HM_INT8_MAX_K, ldq a multiple of 64, q 16-byte aligned, M < 2^31
- * (else HM_ERR_UNSUPPORTED).
+ * 1 <= K <= HM_INT8_MAX_K, M < 2^31 - 2^9, q 16-byte aligned (else
+ * HM_ERR_UNSUPPORTED).
  */
 hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx,
-                              int32_t rms, float eps, int8_t *q, int64_t ldq, float *scale,
-                              void *stream);
+                              int32_t rms, float eps, int8_t *q, float *scale, void *stream);
 
 /*
  *     C[m][n] = a_scale[m] w_scale[n] sum_k A[m][k] W[n][k],
  * the sum exact in 32-bit integers, C of dtype (hm_dtype) rounded once from
- * float32.  A [M][lda] and W [N][ldw] bytes as hyena_quantize_rows writes them:
- * lda, ldw multiples of 64, 16-byte aligned, zeros (in one of the two) from K to
- * the next multiple of 64 (else HM_ERR_UNSUPPORTED for what can be checked).
- * C [M][ldc].  K <= HM_INT8_MAX_K; M, N < 2^31 - 2^9, and
- * ceil(M / 16) * ceil(N / 16) < 2^31 (else HM_ERR_UNSUPPORTED).
+ * float32.  A (M rows) and W (N rows) of K columns as hyena_quantize_rows holds them,
+ * 16-byte aligned; what their rows past M and N hold does not matter.  C [M][ldc].
+ * 1 <= K <= HM_INT8_MAX_K; M, N < 2^31 - 2^9, and ceil(M / 256) * ceil(N / 256) < 2^20
+ * (else HM_ERR_UNSUPPORTED).
  */
-hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda,
-                           const float *a_scale, const int8_t *W, int64_t ldw, const float *w_scale,
-                           int32_t dtype, void *C, int64_t ldc, void *stream);
+hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, const float *a_scale,
+                           const int8_t *W, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
+                           void *stream);
 
 /* ------------------------------------------------------------------------
  * Verification of drafted tokens: a small model drafts a few tokens, the target

@@ -119,35 +119,42 @@ def test_recurrence_workspace():
 
 
 def _quantize(**kw):
-    a = dict(M=4, K=100, dtype=hb.HM_F32, x=FAKE, ldx=100, rms=0, eps=0.0, q=FAKE, ldq=128, scale=FAKE, stream=0)
+    a = dict(M=4, K=100, dtype=hb.HM_F32, x=FAKE, ldx=100, rms=0, eps=0.0, q=FAKE, scale=FAKE, stream=0)
     hb.hyena_quantize_rows(**{**a, **kw})
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), BAD), (dict(K=0), BAD), (dict(K=131073, ldx=1 << 18, ldq=1 << 18), NO), (dict(dtype=2), NO),
+    (dict(M=-1), BAD), (dict(K=0), BAD), (dict(K=131073, ldx=1 << 18), NO), (dict(dtype=2), NO),
     (dict(rms=1, eps=-1.0), BAD), (dict(rms=1, eps=math.nan), BAD), (dict(rms=1, eps=math.inf), BAD), (dict(ldx=99), BAD),
-    (dict(ldq=64), BAD), (dict(ldq=120), NO), (dict(x=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD),
+    (dict(x=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD),
     (dict(x=FAKE + 2), NO), (dict(dtype=hb.HM_BF16, x=FAKE + 1), NO), (dict(q=FAKE + 8), NO), (dict(scale=FAKE + 2), NO),
-    (dict(M=1 << 31), NO), (dict(M=1 << 30, ldx=1 << 20), BAD),
+    (dict(M=(1 << 31) - 512), NO), (dict(M=1 << 30, ldx=1 << 20), BAD),
 ])
 def test_quantize_arguments(kw, status):
     _refused(status, _quantize, **kw)
 
 
+def test_int8_bytes():
+    assert hb.hyena_int8_bytes(1, 1) == 1024 and hb.hyena_int8_bytes(33, 65) == 3 * 2 * 1024
+    assert hb.hyena_int8_bytes(0, 5) == 0
+    _refused(BAD, hb.hyena_int8_bytes, -1, 5)
+    _refused(BAD, hb.hyena_int8_bytes, 5, 0)
+    _refused(NO, hb.hyena_int8_bytes, 5, 131073)
+    assert hb.load().hyena_int8_bytes(1, 1, None) == BAD
+
+
 def _dense(**kw):
-    a = dict(M=4, N=50, K=100, A=FAKE, lda=128, a_scale=FAKE, W=FAKE, ldw=128, w_scale=FAKE, dtype=hb.HM_F32, C=FAKE,
-             ldc=50, stream=0)
+    a = dict(M=4, N=50, K=100, A=FAKE, a_scale=FAKE, W=FAKE, w_scale=FAKE, dtype=hb.HM_F32, C=FAKE, ldc=50, stream=0)
     hb.hyena_dense_int8(**{**a, **kw})
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=0), BAD), (dict(K=131073, lda=1 << 18, ldw=1 << 18), NO),
-    (dict(dtype=7), NO), (dict(lda=64), BAD), (dict(ldw=64), BAD), (dict(lda=100), NO), (dict(ldw=144), NO),
-    (dict(ldc=49), BAD), (dict(A=None), BAD), (dict(W=None), BAD), (dict(C=None), BAD), (dict(a_scale=None), BAD),
-    (dict(w_scale=None), BAD), (dict(A=FAKE + 8), NO), (dict(W=FAKE + 4), NO), (dict(C=FAKE + 2), NO),
-    (dict(a_scale=FAKE + 1), NO), (dict(w_scale=FAKE + 2), NO), (dict(M=(1 << 31) - 512), NO),
-    (dict(N=(1 << 31) - 512, ldc=1 << 31), NO), (dict(M=1 << 24, N=1 << 24, ldc=1 << 24), NO),
-    (dict(M=1 << 30, lda=1 << 20), BAD),
+    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=0), BAD), (dict(K=131073), NO),
+    (dict(dtype=7), NO), (dict(ldc=49), BAD), (dict(A=None), BAD), (dict(W=None), BAD), (dict(C=None), BAD),
+    (dict(a_scale=None), BAD), (dict(w_scale=None), BAD), (dict(A=FAKE + 8), NO), (dict(W=FAKE + 4), NO),
+    (dict(C=FAKE + 2), NO), (dict(a_scale=FAKE + 1), NO), (dict(w_scale=FAKE + 2), NO), (dict(M=(1 << 31) - 512), NO),
+    (dict(N=(1 << 31) - 512, ldc=1 << 31), NO), (dict(M=1 << 19, N=1 << 19, ldc=1 << 19), NO),
+    (dict(M=1 << 27, ldc=1 << 22), BAD),
 ])
 def test_dense_int8_arguments(kw, status):
     _refused(status, _dense, **kw)
