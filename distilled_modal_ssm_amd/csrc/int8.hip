@@ -179,23 +179,27 @@ template <int ACT> void launch_quantize(const QuantArgs &a, hipStream_t stream) 
 
 // ------------------------------------------------------------------ products, tiles
 
-template <int I, int N, typename F> __device__ __forceinline__ void static_for(F &&f) {
-    if constexpr (I < N) {
-        f(std::integral_constant<int, I>{});
-        static_for<I + 1, N>(f);
-    }
+// step(B), step(B + 1), .. step(E - 1) until `left` of them are done; whether they are.
+template <int B, int E, typename F> __device__ __forceinline__ bool steps(int left, F &&step) {
+    step(std::integral_constant<int, B>{});
+    if (left == B + 1) return true;
+    if constexpr (B + 1 < E) return steps<B + 1, E>(left, step);
+    return false;
 }
 
 // WGM x WGN waves of MT x NT tiles of 16 x 16: a workgroup's outputs are BM x BN.  K is
-// staged 64 at a time by direct global -> LDS loads into four buffers, each stage's
-// loads issued four stages before its products.  Each buffer is its own array, and the
-// stage barrier a bare s_barrier behind a wait for the next stage's loads only.  Past
-// the last stage the last one is loaded again, so that the waits are the same for every
-// stage; rows past the last are the last row again.  A stage's A fragments are read
-// behind that barrier, before the products of the stage before; the W fragments of
-// column tile j as soon as the products with the last ones are issued.
+// staged 64 at a time by direct global -> LDS loads, a block a wave and load, into NB
+// buffers, each stage's loads issued NB stages before its products.  Each buffer is its
+// own array, and the stage barrier a bare s_barrier behind a wait for the next stage's
+// loads only.  Past the last stage the last one is loaded again, so that the waits are
+// the same for every stage; blocks past the last are the last again.  A stage's A
+// fragments are read behind that barrier, before the products of the stage before; the W
+// fragments of column tile j as soon as the products with the last ones are issued.
+// Bound (32768 x 6144 x 2048, 2240 TOPS, 45 % of the matrix cores' dense rate at the
+// clock they have then) by the stages' barriers and the latency of their loads: two
+// workgroups a CU of 256 x 128, whose stores one hides behind the other's products.
 template <int ACT, int MT, int NT, int WGM, int WGN, int NB>
-__global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : 2) void dense_int8_kernel(Int8GemmArgs g) {
+__global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : MT * NT == 32 ? 2 : 3) void dense_int8_kernel(Int8GemmArgs g) {
     using A = Act<ACT>;
     constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN, BK = 64, kWaves = WGM * WGN;
     constexpr int kBlocksA = BM / 16 / kWaves, kBlocksW = BN / 16 / kWaves, kLoads = kBlocksA + kBlocksW;
@@ -276,27 +280,30 @@ __global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : 2) void dense_int8_k
     for (int j = 0; j < NT; ++j) wf[j] = frag(W0, 16 * (NT * wn + j));
     // the W fragment is the first operand, so the C tiles are held transposed: lane l
     // holds row 16 i + l % 16, columns 16 j + 4 (l / 16) .. + 3
-    constexpr int kTurn = NB % 2 ? 2 * NB : NB;
-    for (int s0 = 0; s0 < stages; s0 += kTurn)
-        static_for<0, kTurn>([&](auto sc) {
+    // (The loop is left right behind the last stage: where that one could be followed by
+    // another turn, the compiler waits for all loads in flight before a stage's reads, as
+    // it still does once a turn.  256 x 128 outputs of 32768 x 6144 x 2048: 454 us with
+    // such waits, 422 with one in two turns of NB stages, 419 in four.)
+    constexpr int kTurn = 4 * NB;
+    for (int s0 = 0;; s0 += kTurn) {
+        const bool done = steps<0, kTurn>(stages - s0, [&](auto sc) {
             constexpr int b = decltype(sc)::value, cur = b % 2, next = (b + 1) % NB;
-            if (s0 + b >= stages) return;
             stage_barrier(std::integral_constant<int, kLoads * (NB - 2)>{});
             const auto here = bufs(std::integral_constant<int, b % NB>{}), ahead = bufs(std::integral_constant<int, next>{});
             issue(here.first, here.second, s0 + b + NB);
             const int8_t *as = ahead.first, *ws = ahead.second;
 #pragma unroll
             for (int i = 0; i < MT; ++i) af[1 - cur][i] = frag(as, 16 * (MT * wm + i));
-            __builtin_amdgcn_s_setprio(1);
-#pragma unroll
+            #pragma unroll
             for (int j = 0; j < NT; ++j) {
 #pragma unroll
                 for (int i = 0; i < MT; ++i) acc[i][j] = mfma_i8(wf[j], af[cur][i], acc[i][j]);
                 wf[j] = frag(ws, 16 * (NT * wn + j));
             }
-            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
         });
+        if (done) break;
+    }
 
     const int64_t row0 = m0 + 16 * MT * wm, col0 = n0 + 16 * NT * wn;
     float sa[MT], sw[NT][4];
@@ -373,8 +380,10 @@ __global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : 2) void dense_int8_k
                 }
             } else {
                 constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
-                for (int row = lane / kAcross; row < 16 * kPart; row += kRows) {
-                    if (first + row >= g.M) break;
+#pragma unroll 8
+                for (int t = 0; t < 16 * kPart / kRows; ++t) {
+                    const int row = kRows * t + lane / kAcross;
+                    if (first + row >= g.M) continue;
 #pragma unroll
                     for (int c = lane % kAcross; c < kCols; c += kAcross)
                         if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[row * kCols + 8 * ((c / 8) ^ (row % kChunks)) + c % 8];
@@ -438,30 +447,27 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
     }
 }
 
-template <int ACT, int MT, int NT, int WGM, int WGN, int NB = 4> void launch_tiles(const Int8GemmArgs &g, hipStream_t stream) {
+template <int ACT, int MT, int NT, int WGM, int WGN, int NB> void launch_tiles(const Int8GemmArgs &g, hipStream_t stream) {
     constexpr int BM = 16 * MT * WGM, BN = 16 * NT * WGN;
     const dim3 grid((unsigned)((g.M + BM - 1) / BM * ((g.N + BN - 1) / BN)));
     dense_int8_kernel<ACT, MT, NT, WGM, WGN, NB><<<grid, WGM * WGN * kWave, 0, stream>>>(g);
 }
 
+// By rows and numbers of tiles, from measurements at 3 x 9 x 17 sizes (K = 512 to 8192):
+// up to 32 rows the weights are streamed (6144 x 2048, 32 rows: 6.9 us, 7.2 in tiles of
+// 64 x 64; 33 rows 9.0, 7.1); then the smallest tiles of which three a CU are enough
+// (320 x 6144 x 2048: 10.2 us with 64 x 64, 12.4 with 128 x 128, 18.6 with 256 x 128;
+// 2048 x 6144 x 2048: 48, 28.7, 29.7), else 256 x 128, or 256 x 256 where K is long
+// (8192 x 8192 x 8192: 404 us against 428, 2720 TOPS; 16384 x 6144 x 512: 90, 78).
 template <int ACT> void launch_product(const Int8GemmArgs &g, hipStream_t stream) {
-#ifdef FORCE
-    if (FORCE == 1) return launch_tiles<ACT, 4, 8, 4, 2>(g, stream);
-    if (FORCE == 2) return launch_tiles<ACT, 4, 4, 2, 2>(g, stream);
-    if (FORCE == 4) return launch_tiles<ACT, 8, 8, 2, 2>(g, stream);
-    if (FORCE == 5) return launch_tiles<ACT, 8, 4, 2, 4>(g, stream);
-    if (FORCE == 6) return launch_tiles<ACT, 8, 4, 2, 2, 3>(g, stream);
-    if (FORCE == 7) return launch_tiles<ACT, 4, 8, 2, 2, 3>(g, stream);
-    if (FORCE == 3) return launch_tiles<ACT, 2, 2, 2, 2>(g, stream);
-#endif
     const dim3 few((unsigned)((g.N + 15) / 16));
     if (g.M <= 16) return dense_int8_few_kernel<ACT, 1, 4><<<few, 4 * kWave, 0, stream>>>(g);
     if (g.M <= 32) return dense_int8_few_kernel<ACT, 2, 4><<<few, 4 * kWave, 0, stream>>>(g);
-    if (g.M <= 64) return dense_int8_few_kernel<ACT, 4, 4><<<few, 4 * kWave, 0, stream>>>(g);
     auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= 256) return launch_tiles<ACT, 4, 8, 4, 2>(g, stream);
-    if (tiles(128, 128) >= 256) return launch_tiles<ACT, 4, 4, 2, 2>(g, stream);
-    launch_tiles<ACT, 2, 2, 2, 2>(g, stream);
+    if (tiles(64, 64) <= 768) return launch_tiles<ACT, 2, 2, 2, 2, 4>(g, stream);
+    if (tiles(128, 128) <= 768) return launch_tiles<ACT, 4, 4, 2, 2, 3>(g, stream);
+    if (g.K >= 4096) return launch_tiles<ACT, 8, 4, 2, 4, 4>(g, stream);
+    launch_tiles<ACT, 8, 4, 2, 2, 3>(g, stream);
 }
 
 }  // namespace

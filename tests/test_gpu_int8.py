@@ -120,6 +120,38 @@ def test_products(act, M, N, K):
     assert (wide[:, :3] == 5).all() and (wide[:, N + 3:] == 5).all()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N", [(70, 90), (1100, 3001), (2100, 6210)])  # tiles of 64 x 64, 128 x 128 and larger
+def test_products_in_tiles(act, M, N):
+    """Numbers of stages of 64 inputs around every turn of the loop, and the long K of the largest tiles."""
+    torch = require_gpu()
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    tol = 5 * 2.0 ** -24 + (2.0 ** -8 if act == "bf16" else 0)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    stages = [*range(1, 19), 64, 65] if M < 1000 else [1, 2, 3, 4, 5, 7, 12, 13, 16, 17, 64, 65]
+    for s in stages:
+        K = 64 * s - (s * 7) % 64
+        log(f"tiles {act} {M} {N} {K}")
+        x, w = (torch.randn(r, K, generator=g, device="cuda").to(dt) for r in (M, N))
+        y = Int8Dense(w)(x).double()
+
+        def quantized(a):
+            a = a.double()
+            top = a.abs().amax(-1, keepdim=True)
+            return torch.round(a * 127 / top), top[:, 0] / 127
+
+        (X, sx), (W, sw) = quantized(x), quantized(w)
+        ref = (X @ W.t()) * sx[:, None] * sw
+        bad = (y - ref).abs() - tol * ref.abs()
+        assert float(bad.max()) <= 0, (K, int(bad.argmax()) // N, int(bad.argmax()) % N)
+        wide = torch.full((M, N + 10), 5.0, dtype=dt, device="cuda")  # rows of even stride, then of whole pieces
+        for at, cols in ((3, N), (8, N // 8 * 8)):
+            part = Int8Dense(w[:cols])(x, out=wide[:, at:at + cols])
+            assert torch.equal(part.double(), y[:, :cols])
+            assert (wide[:, :at] == 5).all() and (wide[:, at + cols:] == 5).all()
+            wide.fill_(5.0)
+
+
 def test_largest_sums():
     """All products 127^2 of 131072 inputs: 2.11e9, below 2^31."""
     torch = require_gpu()
