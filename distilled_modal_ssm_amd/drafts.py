@@ -26,14 +26,14 @@ class DraftVerify:
         self.ws_bytes = hb.hyena_draft_verify_workspace(self.B, self.T, self.V)
         self._ws = {}  # scratch memory of each stream; a captured graph has its own
         self._verify = hb.load().hyena_draft_verify
+        self._p_shape, self._q_shape = (self.B, self.T + 1, self.V), (self.B, self.T, self.V)
+        self._x_shape, self._u_shape, self._rows = (self.B, self.T), (self.B, self.T + 1), (self.B,)
 
-    def _probs(self, name, t, places, dtype):
+    def _probs(self, name, t, shape, dtype):
         """Row stride of probabilities [B][places][V]."""
-        torch, shape = self.torch, (self.B, places, self.V)
-        if t.dtype not in (torch.float32, torch.bfloat16) or t.shape != shape or t.device != self.device or \
-                (dtype is not None and t.dtype != dtype):
-            raise ValueError(f"{name}: need float32 or bfloat16 {shape} on {self.device}, of one type, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
+        if t.dtype != dtype or t.shape != shape or t.device != self.device:
+            raise ValueError(f"{name}: need {dtype} {shape} on {self.device}, got {t.dtype} {tuple(t.shape)} on "
+                             f"{t.device}")
         ld = self.V if t.is_contiguous() else hb._row_stride(t, ())
         if ld < self.V:
             raise ValueError(f"{name}: rows overlap")
@@ -50,23 +50,25 @@ class DraftVerify:
         probabilities, of p's type, or None where it drafts without chance.
         lengths int32 [B]: drafted tokens of each sequence.
         """
-        torch, B, T = self.torch, self.B, self.T
-        ld_p = self._probs("p", p, T + 1, None)
-        ld_q = 0 if q is None else self._probs("q", q, T, p.dtype)
-        hb._expect("tokens", tokens, torch.int32, (B, T), self.device)
-        hb._expect("u", u, torch.float32, (B, T + 1), self.device)
+        torch, dtype = self.torch, p.dtype
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"p: need float32 or bfloat16, got {dtype}")
+        ld_p = self._probs("p", p, self._p_shape, dtype)
+        ld_q = 0 if q is None else self._probs("q", q, self._q_shape, dtype)
+        hb._expect("tokens", tokens, torch.int32, self._x_shape, self.device)
+        hb._expect("u", u, torch.float32, self._u_shape, self.device)
         if lengths is not None:
-            hb._expect("lengths", lengths, torch.int32, (B,), self.device)
+            hb._expect("lengths", lengths, torch.int32, self._rows, self.device)
         with hb._On(self.device, stream) as stream:
             if out is None:
-                out = (torch.empty((B, T + 1), dtype=torch.int32, device=self.device),
-                       torch.empty((B,), dtype=torch.int32, device=self.device))
+                out = (torch.empty(self._u_shape, dtype=torch.int32, device=self.device),
+                       torch.empty(self._rows, dtype=torch.int32, device=self.device))
             else:
-                hb._expect("out tokens", out[0], torch.int32, (B, T + 1), self.device)
-                hb._expect("out accepted", out[1], torch.int32, (B,), self.device)
+                hb._expect("out tokens", out[0], torch.int32, self._u_shape, self.device)
+                hb._expect("out accepted", out[1], torch.int32, self._rows, self.device)
             ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
             # (straight to the C entry point: a step's call counts in microseconds)
-            hb._check(self._verify(B, T, self.V, hb.HM_BF16 if p.dtype == torch.bfloat16 else hb.HM_F32, p.data_ptr(),
+            hb._check(self._verify(self.B, self.T, self.V, hb.HM_BF16 if dtype == torch.bfloat16 else hb.HM_F32, p.data_ptr(),
                                    ld_p, None if q is None else q.data_ptr(), ld_q, tokens.data_ptr(),
                                    None if lengths is None else lengths.data_ptr(), u.data_ptr(), out[0].data_ptr(),
                                    out[1].data_ptr(), ws.data_ptr(), self.ws_bytes, stream), "hyena_draft_verify")
