@@ -690,6 +690,17 @@ class _On:
         return self.guard.__exit__(*exc) if self.guard is not None else None
 
 
+def _call(call, device, stream, *args):
+    """``call(*args, s)`` as inside ``with _On(device, stream) as s``, without a guard where none is needed (1 us of
+    a call of a few tokens)."""
+    if stream is None:
+        import torch
+        if torch.cuda.current_device() == device.index:
+            return call(*args, _current_stream(device))
+    with _On(device, stream) as s:
+        return call(*args, s)
+
+
 def _scratch(kept, n, stream, device):
     """n bytes of scratch memory for a call on the current stream, whose hipStream_t is ``stream``: a
     handle's buffer of that stream, out of its dict ``kept``, or a longer one in its place.

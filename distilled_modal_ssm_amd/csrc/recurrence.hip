@@ -594,22 +594,36 @@ __global__ __launch_bounds__(W *kWave, 4) void recurrence_backward_kernel(RecurA
 
 // ------------------------------------------------------------------ one token
 
-template <int ACT, int GATE, int INPUT>
+// V neighbouring channels a lane: 4 where rows and states are aligned for it (256 rows of
+// 4096 bfloat16 channels through parents' states: 5.1 us, 6.9 with one), else one.
+template <int ACT, int GATE, int INPUT, int V>
 __global__ __launch_bounds__(256) void recurrence_token_kernel(RecurArgs a) {
     using A = Act<ACT>;
     using T = typename A::T;
-    const int64_t tiles = (a.D + 255) / 256, b = blockIdx.x / tiles, c = blockIdx.x % tiles * 256 + threadIdx.x;
+    struct alignas(V * sizeof(T)) Values { T x[V]; };
+    struct alignas(V * 4) States { float h[V]; };
+    const int64_t tiles = (a.D + 256 * V - 1) / (256 * V), b = blockIdx.x / tiles;
+    const int64_t c = blockIdx.x % tiles * (256 * V) + threadIdx.x * V;
     if (c >= a.D) return;
     int64_t from = b;
     if (a.src_rows) {
         const int64_t r = a.src_rows[b];
         if (r >= 0 && r < a.B) from = r;
     }
-    float f, i;
-    gate_of<GATE, INPUT>(A::ld(static_cast<const T *>(a.g) + b * a.ld_g + c), f, i);
-    const float h = fmaf(f, a.state_in[from * a.D + c], i * A::ld(static_cast<const T *>(a.v) + b * a.ld_v + c));
-    a.state_out[b * a.D + c] = h;
-    A::st(static_cast<T *>(a.y) + b * a.ld_y + c, a.q ? h * A::ld(static_cast<const T *>(a.q) + b * a.ld_q + c) : h);
+    const Values g = *reinterpret_cast<const Values *>(static_cast<const T *>(a.g) + b * a.ld_g + c);
+    const Values v = *reinterpret_cast<const Values *>(static_cast<const T *>(a.v) + b * a.ld_v + c);
+    Values q{}, y;
+    if (a.q) q = *reinterpret_cast<const Values *>(static_cast<const T *>(a.q) + b * a.ld_q + c);
+    States s = *reinterpret_cast<const States *>(a.state_in + from * a.D + c);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        float f, i;
+        gate_of<GATE, INPUT>(A::ld(&g.x[e]), f, i);
+        s.h[e] = fmaf(f, s.h[e], i * A::ld(&v.x[e]));
+        A::st(&y.x[e], a.q ? s.h[e] * A::ld(&q.x[e]) : s.h[e]);
+    }
+    *reinterpret_cast<States *>(a.state_out + b * a.D + c) = s;
+    *reinterpret_cast<Values *>(static_cast<T *>(a.y) + b * a.ld_y + c) = y;
 }
 
 // A launch of the kernel for the call's types.
@@ -722,9 +736,14 @@ hipError_t launch_recurrence_backward(const RecurArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_recurrence_decode(const RecurArgs &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.B * ((a.D + 255) / 256)));
+    const uintptr_t e = a.act == kBF16 ? 8 : 16;
+    auto ok = [&](const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % e == 0 && (ld % 4 == 0 || a.B == 1); };
+    const bool four = a.D % 4 == 0 && ok(a.q, a.ld_q) && ok(a.g, a.ld_g) && ok(a.v, a.ld_v) && ok(a.y, a.ld_y) &&
+                      reinterpret_cast<uintptr_t>(a.state_in) % 16 == 0 && reinterpret_cast<uintptr_t>(a.state_out) % 16 == 0;
     return for_types(a, [&](auto act, auto gate, auto input) {
-        recurrence_token_kernel<decltype(act)::value, decltype(gate)::value, decltype(input)::value><<<grid, 256, 0, stream>>>(a);
+        constexpr int C = decltype(act)::value, G = decltype(gate)::value, I = decltype(input)::value;
+        if (four) recurrence_token_kernel<C, G, I, 4><<<dim3((unsigned)(a.B * ((a.D + 1023) / 1024))), 256, 0, stream>>>(a);
+        else recurrence_token_kernel<C, G, I, 1><<<dim3((unsigned)(a.B * ((a.D + 255) / 256))), 256, 0, stream>>>(a);
     });
 }
 

@@ -59,17 +59,20 @@ class DraftVerify:
         hb._expect("u", u, torch.float32, self._u_shape, self.device)
         if lengths is not None:
             hb._expect("lengths", lengths, torch.int32, self._rows, self.device)
-        with hb._On(self.device, stream) as stream:
-            if out is None:
-                out = (torch.empty(self._u_shape, dtype=torch.int32, device=self.device),
-                       torch.empty(self._rows, dtype=torch.int32, device=self.device))
-            else:
-                hb._expect("out tokens", out[0], torch.int32, self._u_shape, self.device)
-                hb._expect("out accepted", out[1], torch.int32, self._rows, self.device)
-            ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
-            # (straight to the C entry point: a step's call counts in microseconds)
-            hb._check(self._verify(self.B, self.T, self.V, hb.HM_BF16 if dtype == torch.bfloat16 else hb.HM_F32, p.data_ptr(),
-                                   ld_p, None if q is None else q.data_ptr(), ld_q, tokens.data_ptr(),
-                                   None if lengths is None else lengths.data_ptr(), u.data_ptr(), out[0].data_ptr(),
-                                   out[1].data_ptr(), ws.data_ptr(), self.ws_bytes, stream), "hyena_draft_verify")
+        if out is not None:
+            hb._expect("out tokens", out[0], torch.int32, self._u_shape, self.device)
+            hb._expect("out accepted", out[1], torch.int32, self._rows, self.device)
+        return hb._call(self._run, self.device, stream, p, ld_p, q, ld_q, tokens, lengths, u, out)
+
+    def _run(self, p, ld_p, q, ld_q, tokens, lengths, u, out, stream):
+        torch = self.torch
+        if out is None:
+            out = (torch.empty(self._u_shape, dtype=torch.int32, device=self.device),
+                   torch.empty(self._rows, dtype=torch.int32, device=self.device))
+        ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
+        # (straight to the C entry point: a step's call counts in microseconds)
+        hb._check(self._verify(self.B, self.T, self.V, hb.HM_BF16 if p.dtype == torch.bfloat16 else hb.HM_F32, p.data_ptr(),
+                               ld_p, None if q is None else q.data_ptr(), ld_q, tokens.data_ptr(),
+                               None if lengths is None else lengths.data_ptr(), u.data_ptr(), out[0].data_ptr(),
+                               out[1].data_ptr(), ws.data_ptr(), self.ws_bytes, stream), "hyena_draft_verify")
         return out

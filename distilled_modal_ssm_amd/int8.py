@@ -59,17 +59,18 @@ class Int8Dense:
         """
         M = int(x.shape[0]) if x.dim() == 2 else -1
         ld, dtype = self._rows("x", x, M, self.K)
-        with hb._On(self.device, stream) as stream:
-            if out is None:
-                out = self.torch.empty((M, self.N), dtype=x.dtype, device=self.device)
-            ldo, otype = self._rows("out", out, M, self.N)
-            at = -(-M // 16) * self._block_row  # the rows' scales behind the rows
-            scratch = hb._scratch(self._ws, at + 4 * M, stream, self.device)
-            ws = scratch.data_ptr()
-            # (straight to the C entry points: a token's call counts in microseconds)
-            hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, ws + at,
-                                     stream), "hyena_quantize_rows")
-            hb._check(self._product(M, self.N, self.K, ws, ws + at, self.weight8.data_ptr(),
-                                    self.weight_scale.data_ptr(), otype, out.data_ptr(), ldo, stream),
-                      "hyena_dense_int8")
+        ldo, otype = (self.N, dtype) if out is None else self._rows("out", out, M, self.N)
+        return hb._call(self._run, self.device, stream, x, M, ld, dtype, rms_eps, out, ldo, otype)
+
+    def _run(self, x, M, ld, dtype, rms_eps, out, ldo, otype, stream):
+        if out is None:
+            out = self.torch.empty((M, self.N), dtype=x.dtype, device=self.device)
+        at = -(-M // 16) * self._block_row  # the rows' scales behind the rows
+        scratch = hb._scratch(self._ws, at + 4 * M, stream, self.device)
+        ws = scratch.data_ptr()
+        # (straight to the C entry points: a token's call counts in microseconds)
+        hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, ws + at,
+                                 stream), "hyena_quantize_rows")
+        hb._check(self._product(M, self.N, self.K, ws, ws + at, self.weight8.data_ptr(), self.weight_scale.data_ptr(),
+                                otype, out.data_ptr(), ldo, stream), "hyena_dense_int8")
         return out

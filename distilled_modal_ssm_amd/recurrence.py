@@ -99,28 +99,30 @@ class GatedRecurrence:
         chunk_states: memory as ``new_chunk_states`` gives it, which a backward
         pass reads.
         """
-        shape, (ld_q, ld_g, ld_v) = self._inputs(q, g, v, lengths)
-        L = shape[1]
+        shape, lds = self._inputs(q, g, v, lengths)
         if state_in is not None:
             self._f32("state_in", state_in, self._state_shape)
+        if state_out is not None:
+            self._f32("state_out", state_out, self._state_shape)
         if chunk_states is not None:
-            self._f32("chunk_states", chunk_states, (self.B, -(-L // hb.HM_RECURRENCE_CHUNK), self.D))
-        with hb._On(self.device, stream) as stream:
-            if y is None:
-                y = self.torch.empty(shape, dtype=self.tdtype, device=self.device)
-            if state_out is None:
-                state_out = self.torch.empty(self._state_shape, dtype=self.torch.float32, device=self.device)
-            else:
-                self._f32("state_out", state_out, self._state_shape)
-            ws, n = self._workspace(L, stream)
-            # (straight to the C entry point: a few tokens' call counts in microseconds)
-            hb._check(self._prompt(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
-                                   None if q is None else q.data_ptr(), ld_q, g.data_ptr(), ld_g, v.data_ptr(), ld_v,
-                                   y.data_ptr(), self._rows("y", y, shape),
-                                   None if state_in is None else state_in.data_ptr(), state_out.data_ptr(),
-                                   None if chunk_states is None else chunk_states.data_ptr(),
-                                   None if ws is None else ws.data_ptr(), n, stream),
-                      "hyena_recurrence_prefill")
+            self._f32("chunk_states", chunk_states, (self.B, -(-shape[1] // hb.HM_RECURRENCE_CHUNK), self.D))
+        ld_y = self.D if y is None else self._rows("y", y, shape)
+        return hb._call(self._run_prompt, self.device, stream, shape, q, g, v, lds, lengths, y, ld_y, state_in, state_out,
+                        chunk_states)
+
+    def _run_prompt(self, shape, q, g, v, lds, lengths, y, ld_y, state_in, state_out, chunk_states, stream):
+        torch, L = self.torch, shape[1]
+        if y is None:
+            y = torch.empty(shape, dtype=self.tdtype, device=self.device)
+        if state_out is None:
+            state_out = torch.empty(self._state_shape, dtype=torch.float32, device=self.device)
+        ws, n = self._workspace(L, stream)
+        # (straight to the C entry point: a few tokens' call counts in microseconds)
+        hb._check(self._prompt(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
+                               None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
+                               y.data_ptr(), ld_y, None if state_in is None else state_in.data_ptr(),
+                               state_out.data_ptr(), None if chunk_states is None else chunk_states.data_ptr(),
+                               None if ws is None else ws.data_ptr(), n, stream), "hyena_recurrence_prefill")
         return y, state_out
 
     def backward(self, q, g, v, dy, chunk_states, lengths=None, dstate_out=None, out=None, stream=None):
@@ -173,12 +175,15 @@ class GatedRecurrence:
             state_out = state
         else:
             self._f32("state_out", state_out, shape)
-        with hb._On(self.device, stream) as stream:
-            if y is None:
-                y = self.torch.empty(shape, dtype=self.tdtype, device=self.device)
-            # (straight to the C entry point: a token's call counts in microseconds)
-            hb._check(self._token(self._desc_ref, None if q is None else q.data_ptr(), ld_q, g.data_ptr(), ld_g,
-                                  v.data_ptr(), ld_v, y.data_ptr(), self._rows("y", y, shape), state.data_ptr(),
-                                  None if rows is None else rows.data_ptr(), state_out.data_ptr(), stream),
-                      "hyena_recurrence_decode_step")
+        ld_y = self.D if y is None else self._rows("y", y, shape)
+        return hb._call(self._run_token, self.device, stream, q, ld_q, g, ld_g, v, ld_v, y, ld_y, state, rows, state_out)
+
+    def _run_token(self, q, ld_q, g, ld_g, v, ld_v, y, ld_y, state, rows, state_out, stream):
+        if y is None:
+            y = self.torch.empty(self._state_shape, dtype=self.tdtype, device=self.device)
+        # (straight to the C entry point: a token's call counts in microseconds)
+        hb._check(self._token(self._desc_ref, None if q is None else q.data_ptr(), ld_q, g.data_ptr(), ld_g,
+                              v.data_ptr(), ld_v, y.data_ptr(), ld_y, state.data_ptr(),
+                              None if rows is None else rows.data_ptr(), state_out.data_ptr(), stream),
+                  "hyena_recurrence_decode_step")
         return y
