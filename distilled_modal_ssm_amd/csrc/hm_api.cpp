@@ -1164,6 +1164,7 @@ hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x
     const hm_status st = check_int8(M, K);
     if (st != HM_OK) return st;
     if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
+    if (M >= int64_t(1) << 24) return HM_ERR_UNSUPPORTED;  // a workgroup of 256 threads a row: fewer than 2^32
     if (rms && !(std::isfinite(eps) && eps >= 0.0f)) return HM_ERR_INVALID_ARG;
     if (ldx < K) return HM_ERR_INVALID_ARG;
     if (M == 0) return HM_OK;

@@ -14,8 +14,9 @@ class Int8Dense:
     """y = x W^T of a weight W [outputs][inputs] in 8-bit integers.
 
     weight: float32 or bfloat16 rows with unit element stride on the GPU, read
-    here once, on the given or the current stream.  ``weight8`` (int8, in the
-    library's blocks) and ``weight_scale`` [outputs] hold it.
+    here once, on the given or the current stream, which calls on other streams
+    have to wait for.  ``weight8`` (int8, in the library's blocks) and
+    ``weight_scale`` [outputs] hold it.
     """
 
     def __init__(self, weight, stream=None):

@@ -788,8 +788,7 @@ hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes);
  *   x [M][ldx] of dtype (hm_dtype), K columns;  q  hyena_int8_bytes bytes, columns from
  *   K on set to 0, rows from M on left as they are;  scale [M].
  * Tokens (rows of activations) and output channels (rows of W) alike.
- * 1 <= K <= HM_INT8_MAX_K, M < 2^31 - 2^9, q 16-byte aligned (else
- * HM_ERR_UNSUPPORTED).
+ * 1 <= K <= HM_INT8_MAX_K, M < 2^24, q 16-byte aligned (else HM_ERR_UNSUPPORTED).
  */
 hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx,
                               int32_t rms, float eps, int8_t *q, float *scale, void *stream);

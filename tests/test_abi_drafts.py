@@ -128,7 +128,7 @@ def _quantize(**kw):
     (dict(rms=1, eps=-1.0), BAD), (dict(rms=1, eps=math.nan), BAD), (dict(rms=1, eps=math.inf), BAD), (dict(ldx=99), BAD),
     (dict(x=None), BAD), (dict(q=None), BAD), (dict(scale=None), BAD),
     (dict(x=FAKE + 2), NO), (dict(dtype=hb.HM_BF16, x=FAKE + 1), NO), (dict(q=FAKE + 8), NO), (dict(scale=FAKE + 2), NO),
-    (dict(M=(1 << 31) - 512), NO), (dict(M=1 << 30, ldx=1 << 20), BAD),
+    (dict(M=1 << 24), NO), (dict(M=1 << 23, ldx=1 << 24), BAD),
 ])
 def test_quantize_arguments(kw, status):
     _refused(status, _quantize, **kw)
@@ -190,3 +190,76 @@ def test_empty_problems_need_no_gpu():
     _verify(batch=0, p=None, q=None, tokens=None, u=None, out_tokens=None, out_accepted=None, workspace=None, ws_bytes=0)
     assert hb.hyena_draft_verify_workspace(0, 4, 1000) == 0
     assert hb.load().hyena_draft_verify_workspace(1, 4, 1000, None) == BAD
+
+
+def _scratch_users(monkeypatch):
+    """Calls that use scratch memory on stream 1, in place of the library's: each returns the address it was given."""
+    import torch
+    from distilled_modal_ssm_amd import DraftVerify, GatedRecurrence, Int8Dense
+    seen = []
+    monkeypatch.setattr(hb, "_call", lambda call, device, stream, *args: call(*args, 1))
+    rec = GatedRecurrence(1, 16, "f32", device="cpu")
+    rec._prompt = lambda *a: seen.append((a[-3], a[-2])) or hb.HM_OK
+
+    def prompt(n):
+        x = torch.zeros(1, n, 16)
+        rec.prefill(x, x, x)
+        return seen[-1]
+
+    verify = DraftVerify(2, 3, 5000, device="cpu")
+    verify._verify = lambda *a: seen.append((a[-3], a[-2])) or hb.HM_OK
+
+    def check(_):
+        verify.verify(torch.zeros(2, 4, 5000), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 4))
+        return seen[-1]
+
+    class OnHost:
+        def __init__(self, *a):
+            pass
+
+        def __enter__(self):
+            return 1
+
+        def __exit__(self, *exc):
+            return None
+
+    monkeypatch.setattr(hb, "_On", OnHost)
+    monkeypatch.setattr(hb, "hyena_quantize_rows", lambda *a: None)
+    dense = Int8Dense(torch.zeros(30, 100))
+    dense._quantize = lambda *a: seen.append((a[-3], a[-2] - a[-3])) or hb.HM_OK
+    dense._product = lambda *a: hb.HM_OK
+
+    def product(n):
+        dense(torch.zeros(n, 100))
+        return seen[-1]
+
+    return {"prompt": (rec, prompt), "verify": (verify, check), "dense": (dense, product)}
+
+
+@pytest.mark.parametrize("user", ["prompt", "verify", "dense"])
+def test_captured_calls_have_scratch_of_their_own(monkeypatch, user):
+    """As for the other handles: a graph's addresses are not a buffer that a later call replaces or uses."""
+    import torch
+    handle, call = _scratch_users(monkeypatch)[user]
+    capturing = [1]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(capturing))
+    at, n = call(5000)
+    assert at and n > 0 and not handle._ws
+    capturing.clear()
+    eager = call(5000)[0]
+    assert call(5000)[0] == eager and len(handle._ws) == 1
+    capturing.append(1)
+    assert call(5000)[0] != eager
+    capturing.clear()
+    assert call(5000)[0] == eager and len(handle._ws) == 1
+
+
+def test_recurrence_workspaces_of_short_and_long_prompts():
+    """A workgroup's tokens (8, 64 or 128) need none; more are joined through words of 8 bytes a channel and place,
+    the backward pass's of 64 tokens the most."""
+    d = _desc(batch=3, channels=100)
+    assert [hb.hyena_recurrence_workspace(d, L) for L in (0, 1, 8, 9, 64)] == [0] * 5
+    assert hb.hyena_recurrence_workspace(d, 65) == 3 * 2 * 128 + 3 * 128 * (2 + 1 + 1) * 8
+    places = -(-100000 // 64)
+    groups = -(-places // 8)
+    assert hb.hyena_recurrence_workspace(d, 100000) == 3 * 2 * 128 + 3 * 128 * (places + groups + -(-groups // 8)) * 8

@@ -215,6 +215,17 @@ def test_prompt_and_backward(kw, act):
     p.check_grads(*p.backward(chunks))
 
 
+@pytest.mark.parametrize("act,lengths", [("f32", None), ("bf16", [20011, 9500])])
+def test_long_prompts_and_backward(act, lengths):
+    """More than twice 64 places of 128 tokens, and four times backward: several links of the chain between them."""
+    torch = require_gpu()
+    log(f"long {act}")
+    p = Problem(torch, 1 if lengths is None else 2, 20011, 70, act, lengths=lengths, resume=True, train=True)
+    chunks = p.op.new_chunk_states(p.L)
+    p.check(*p.prefill(chunk_states=chunks))
+    p.check_grads(*p.backward(chunks))
+
+
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("gate", ["log", "sigmoid"])
 @pytest.mark.parametrize("input", ["free", "convex", "norm"])
