@@ -82,6 +82,8 @@ EXPORTS = (
     "hyena_int8_bytes",
     "hyena_quantize_rows",
     "hyena_dense_int8",
+    "hyena_dense_int8_rows_workspace",
+    "hyena_dense_int8_rows",
     "hyena_draft_verify_workspace",
     "hyena_draft_verify",
 )
@@ -223,6 +225,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "hyena_int8_bytes": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
             "hyena_quantize_rows": ([i64, i64, i32, p, i64, i32, f32, p, p, p], ctypes.c_int),
             "hyena_dense_int8": ([i64, i64, i64, p, p, p, p, i32, p, i64, p], ctypes.c_int),
+            "hyena_dense_int8_rows_workspace": ([i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
+            "hyena_dense_int8_rows": ([i64, i64, i64, i32, p, i64, i32, f32, p, p, i32, p, i64, p, sz, p], ctypes.c_int),
             "hyena_draft_verify_workspace": ([i64, i64, i64, ctypes.POINTER(sz)], ctypes.c_int),
             "hyena_draft_verify": ([i64, i64, i64, i32, p, i64, p, i64, p, p, p, p, p, p, sz, p], ctypes.c_int),
         }
@@ -639,6 +643,19 @@ def hyena_dense_int8(M, N, K, A, a_scale, W, w_scale, dtype, C, ldc, stream=None
     st = load().hyena_dense_int8(M, N, K, _ptr(A), _ptr(a_scale), _ptr(W), _ptr(w_scale), dtype, _ptr(C), ldc,
                                  _stream(stream))
     _check(st, "hyena_dense_int8")
+
+
+def hyena_dense_int8_rows_workspace(M: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().hyena_dense_int8_rows_workspace(M, K, ctypes.byref(n)), "hyena_dense_int8_rows_workspace")
+    return n.value
+
+
+def hyena_dense_int8_rows(M, N, K, x_dtype, x, ldx, rms, eps, W, w_scale, dtype, C, ldc, workspace, ws_bytes=None,
+                          stream=None) -> None:
+    st = load().hyena_dense_int8_rows(M, N, K, x_dtype, _ptr(x), ldx, int(rms), eps, _ptr(W), _ptr(w_scale), dtype, _ptr(C),
+                                      ldc, _ptr(workspace), _ws_bytes(workspace, ws_bytes), _stream(stream))
+    _check(st, "hyena_dense_int8_rows")
 
 
 def hyena_draft_verify_workspace(batch: int, drafts: int, vocab: int) -> int:

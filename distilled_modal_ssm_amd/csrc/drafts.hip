@@ -7,6 +7,10 @@
 // A row of weights is cut into parts of 1024.  The first kernel, a wave a part, finds the
 // place and sums the part in float64; the second, one workgroup a sequence, finds the
 // part that the number falls on from the sums, reads it again and finds the token in it.
+// Vocabularies of up to four parts take one kernel that does both (4000 tokens: 6.5 us for
+// one sequence and 7.2 for 256, 7.6 and 9.2 in two; of 8 parts, by 16 waves: 9.9, 8.1).
+// What bounds it: launches and memory latency; a large batch's first kernel, HBM (64 x
+// 131072 float32 with q: 12.2 us, 5 TB/s).
 // Sums are in float64 because which token a number falls on is a matter of the last
 // digits, and in a fixed order.
 #include "hm_internal.hpp"
@@ -15,7 +19,7 @@ namespace hm {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
-constexpr int kPart = 1024, kEach = kPart / kWave, kMine = kPart / kThreads;
+constexpr int kPart = 1024, kEach = kPart / kWave;
 
 // Probabilities that are none count as 0.
 __device__ __forceinline__ float weighed(float p) { return p > 0.0f && p < __builtin_inff() ? p : 0.0f; }
@@ -92,13 +96,10 @@ template <int ACT, bool PAIRS> __device__ __forceinline__ void load_part(const v
     }
 }
 
+// Sums over a part by a wave: of max(p - q, 0) and of p, in every lane.
 template <int ACT, bool PAIRS>
-__global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a, int64_t parts) {
-    const int64_t groups = (parts + kWaves - 1) / kWaves, b = blockIdx.x / groups;
-    const int64_t part = blockIdx.x % groups * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (part >= parts) return;
-    const int lane = threadIdx.x % kWave, state = place_of<ACT>(a, b);
-    const Weights<ACT> w(a, b, state);
+__device__ __forceinline__ double2 sum_part(const VerifyArgs &a, const Weights<ACT> &w, int64_t part) {
+    const int lane = threadIdx.x % kWave;
     const int64_t v0 = part * kPart;
     const int count = a.V - v0 < kPart ? (int)(a.V - v0) : kPart;
     float p[kEach], q[kEach];
@@ -116,10 +117,20 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a, int
         left += __shfl_xor(left, s);
         all += __shfl_xor(all, s);
     }
-    if (lane == 0) {
+    return make_double2(left, all);
+}
+
+template <int ACT, bool PAIRS>
+__global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a, int64_t parts) {
+    const int64_t groups = (parts + kWaves - 1) / kWaves, b = blockIdx.x / groups;
+    const int64_t part = blockIdx.x % groups * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (part >= parts) return;
+    const int state = place_of<ACT>(a, b);
+    const double2 sums = sum_part<ACT, PAIRS>(a, Weights<ACT>(a, b, state), part);
+    if (threadIdx.x % kWave == 0) {
         const Work work = work_of(a, parts);
-        work.left[b * parts + part] = left;
-        work.all[b * parts + part] = all;
+        work.left[b * parts + part] = sums.x;
+        work.all[b * parts + part] = sums.y;
         if (part == 0) work.place[b] = state;
     }
 }
@@ -155,7 +166,7 @@ __device__ __forceinline__ double before_in_block(double x, double *sh, double &
 // took 10 us.)
 struct Found {
     int64_t over[kWaves], last[kWaves];  // of a wave, -1 where it has none
-    double over_before[kWaves], last_before[kWaves];
+    double over_before[kWaves], last_before[kWaves], sums[kWaves];
 };
 
 template <typename F>
@@ -203,29 +214,26 @@ __device__ __forceinline__ int64_t find(int64_t first, int64_t n, F weight, doub
     return found;
 }
 
+// The token of sequence b from its parts' sums, and its outputs.
 template <int ACT>
-__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int64_t parts) {
+__device__ __forceinline__ void draw(const VerifyArgs &a, int64_t b, int state, const Weights<ACT> &w, const double *left,
+                                     const double *all, int64_t parts, Found &sh) {
     using A = Act<ACT>;
-    __shared__ double sums[kWaves];
-    __shared__ Found sh;
-    const int64_t b = blockIdx.x;
-    const int tid = threadIdx.x;
-    const Work work = work_of(a, parts);
-    const int state = work.place[b], place = state % kRefused;
-    const Weights<ACT> w(a, b, state);
+    constexpr int kMine = kPart / kThreads;
+    const int tid = threadIdx.x, place = state % kRefused;
     // the part; a thread has `each` neighbours
     const int64_t each = (parts + kThreads - 1) / kThreads, first = tid * each;
     const int64_t mine = first >= parts ? 0 : parts - first < each ? parts - first : each;
     bool rest = true;  // max(p - q, 0); p where that is 0 all over
-    const double *part = work.left + b * parts;
+    const double *part = left;
     double whole, before;
     for (;;) {
         double sum = 0.0;
         for (int64_t i = 0; i < mine; ++i) sum += part[first + i];
-        before = before_in_block(sum, sums, whole);
+        before = before_in_block(sum, sh.sums, whole);
         if (whole > 0.0 || !rest) break;
         rest = false;
-        part = work.all + b * parts;
+        part = all;
     }
     int64_t token = -1;
     if (whole > 0.0) {
@@ -246,12 +254,49 @@ __global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int
             sum += x[e];
         }
         double ignored;
-        before = so_far + before_in_block(sum, sums, ignored);
+        before = so_far + before_in_block(sum, sh.sums, ignored);
         token = find(v0, kMine, [&](int64_t i) { return x[i]; }, at, before, sh);
     }
     if (tid <= a.T)
         a.out_tokens[b * (a.T + 1) + tid] = tid < place ? a.tokens[b * a.T + tid] : tid == place ? (int)token : -1;
     if (tid == 0) a.out_accepted[b] = place;
+}
+
+template <int ACT>
+__global__ __launch_bounds__(kThreads) void verify_draw_kernel(VerifyArgs a, int64_t parts) {
+    __shared__ Found sh;
+    const int64_t b = blockIdx.x;
+    const Work work = work_of(a, parts);
+    const int state = work.place[b];
+    draw<ACT>(a, b, state, Weights<ACT>(a, b, state), work.left + b * parts, work.all + b * parts, parts, sh);
+}
+
+template <int ACT, bool PAIRS> __global__ __launch_bounds__(kThreads) void verify_whole_kernel(VerifyArgs a, int parts) {
+    __shared__ Found sh;
+    __shared__ double left[kWaves], all[kWaves];
+    const int64_t b = blockIdx.x;
+    const int state = place_of<ACT>(a, b), part = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Weights<ACT> w(a, b, state);
+    if (part < parts) {
+        const double2 sums = sum_part<ACT, PAIRS>(a, w, part);
+        if (threadIdx.x % kWave == 0) {
+            left[part] = sums.x;
+            all[part] = sums.y;
+        }
+    }
+    __syncthreads();
+    draw<ACT>(a, b, state, w, left, all, parts, sh);
+}
+
+template <int ACT, bool PAIRS> void launch(const VerifyArgs &a, hipStream_t stream) {
+    const int64_t parts = parts_of(a.V);
+    const dim3 grid((unsigned)(a.B * ((parts + kWaves - 1) / kWaves))), rows((unsigned)a.B);
+    if (parts <= kWaves) {
+        verify_whole_kernel<ACT, PAIRS><<<rows, kThreads, 0, stream>>>(a, (int)parts);
+    } else {
+        verify_sums_kernel<ACT, PAIRS><<<grid, kThreads, 0, stream>>>(a, parts);
+        verify_draw_kernel<ACT><<<rows, kThreads, 0, stream>>>(a, parts);
+    }
 }
 
 }  // namespace
@@ -261,19 +306,10 @@ size_t draft_verify_workspace(int64_t B, int64_t V) {
 }
 
 hipError_t launch_draft_verify(const VerifyArgs &a, hipStream_t stream) {
-    const int64_t parts = parts_of(a.V);
-    const dim3 grid((unsigned)(a.B * ((parts + kWaves - 1) / kWaves))), rows((unsigned)a.B);
     auto pairs = [&](const void *p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0; };
-    if (a.act == kF32) {
-        verify_sums_kernel<kF32, false><<<grid, kThreads, 0, stream>>>(a, parts);
-        verify_draw_kernel<kF32><<<rows, kThreads, 0, stream>>>(a, parts);
-    } else {
-        if (a.V % 2 == 0 && pairs(a.p, a.ld_p) && (!a.q || pairs(a.q, a.ld_q)))
-            verify_sums_kernel<kBF16, true><<<grid, kThreads, 0, stream>>>(a, parts);
-        else
-            verify_sums_kernel<kBF16, false><<<grid, kThreads, 0, stream>>>(a, parts);
-        verify_draw_kernel<kBF16><<<rows, kThreads, 0, stream>>>(a, parts);
-    }
+    if (a.act == kF32) launch<kF32, false>(a, stream);
+    else if (a.V % 2 == 0 && pairs(a.p, a.ld_p) && (!a.q || pairs(a.q, a.ld_q))) launch<kBF16, true>(a, stream);
+    else launch<kBF16, false>(a, stream);
     return hipGetLastError();
 }
 

@@ -1159,24 +1159,30 @@ hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes) {
     return HM_OK;
 }
 
-hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps,
-                              int8_t *q, float *scale, void *stream) {
-    const hm_status st = check_int8(M, K);
-    if (st != HM_OK) return st;
+// Rows to bring to 8 bits (M > 0), but for where they go.
+static hm_status check_quantize(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps) {
     if (dtype != HM_F32 && dtype != HM_BF16) return HM_ERR_UNSUPPORTED;
     if (M >= int64_t(1) << 24) return HM_ERR_UNSUPPORTED;  // a workgroup of 256 threads a row: fewer than 2^32
     if (rms && !(std::isfinite(eps) && eps >= 0.0f)) return HM_ERR_INVALID_ARG;
     if (ldx < K) return HM_ERR_INVALID_ARG;
+    return M > 0 ? check_rows(x, ldx, K, M, dtype == HM_BF16 ? 2 : 4) : HM_OK;
+}
+
+hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx, int32_t rms, float eps,
+                              int8_t *q, float *scale, void *stream) {
+    hm_status st = check_int8(M, K);
+    if (st == HM_OK) st = check_quantize(M, K, dtype, x, ldx, rms, eps);
+    if (st != HM_OK) return st;
     if (M == 0) return HM_OK;
-    if (!x || !q || !scale) return HM_ERR_INVALID_ARG;
-    if (!aligned(x, dtype == HM_BF16 ? 2 : 4) || !aligned(q, 16) || !aligned(scale, 4)) return HM_ERR_UNSUPPORTED;
-    if (M > kMaxElems / ldx) return HM_ERR_INVALID_ARG;
+    if (!q || !scale) return HM_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(scale, 4)) return HM_ERR_UNSUPPORTED;
     const hm::QuantArgs a{M, K, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, scale};
     return hm::launch_quantize_rows(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
-hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, const float *a_scale, const int8_t *W,
-                           const float *w_scale, int32_t dtype, void *C, int64_t ldc, void *stream) {
+// A product's sizes, weights and outputs.
+static hm_status check_product(int64_t M, int64_t N, int64_t K, const int8_t *W, const float *w_scale, int32_t dtype,
+                               const void *C, int64_t ldc) {
     hm_status st = check_int8(M, K);
     if (st == HM_OK) st = check_int8(N, K);
     if (st != HM_OK) return st;
@@ -1185,13 +1191,48 @@ hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, con
     if (M == 0 || N == 0) return HM_OK;
     // fewer than 2^32 threads: 512 for 256 x 256 outputs, or 256 for 16 columns of a few rows
     if ((M + 255) / 256 >= ((int64_t(1) << 20) + (N + 255) / 256 - 1) / ((N + 255) / 256)) return HM_ERR_UNSUPPORTED;
-    if (!A || !a_scale || !W || !w_scale || !C) return HM_ERR_INVALID_ARG;
-    if (!aligned(A, 16) || !aligned(W, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
-        !aligned(C, dtype == HM_BF16 ? 2 : 4))
-        return HM_ERR_UNSUPPORTED;
-    if (M > kMaxElems / ldc) return HM_ERR_INVALID_ARG;
+    if (!W || !w_scale || !C) return HM_ERR_INVALID_ARG;
+    if (!aligned(W, 16) || !aligned(w_scale, 4) || !aligned(C, dtype == HM_BF16 ? 2 : 4)) return HM_ERR_UNSUPPORTED;
+    return M > kMaxElems / ldc ? HM_ERR_INVALID_ARG : HM_OK;
+}
+
+hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, const float *a_scale, const int8_t *W,
+                           const float *w_scale, int32_t dtype, void *C, int64_t ldc, void *stream) {
+    const hm_status st = check_product(M, N, K, W, w_scale, dtype, C, ldc);
+    if (st != HM_OK) return st;
+    if (M == 0 || N == 0) return HM_OK;
+    if (!A || !a_scale) return HM_ERR_INVALID_ARG;
+    if (!aligned(A, 16) || !aligned(a_scale, 4)) return HM_ERR_UNSUPPORTED;
     const hm::Int8GemmArgs a{M, N, K, A, a_scale, W, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
     return hm::launch_dense_int8(a, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+}
+
+// The rows, then their scales.
+static size_t int8_rows_bytes(int64_t M, int64_t K) {
+    return (size_t)((M + 15) / 16) * (size_t)((K + 63) / 64) * 1024 + ((size_t)M * sizeof(float) + 255) / 256 * 256;
+}
+
+hm_status hyena_dense_int8_rows_workspace(int64_t M, int64_t K, size_t *bytes) {
+    const hm_status st = check_int8(M, K);
+    if (st != HM_OK) return st;
+    if (!bytes) return HM_ERR_INVALID_ARG;
+    *bytes = int8_rows_bytes(M, K);
+    return HM_OK;
+}
+
+hm_status hyena_dense_int8_rows(int64_t M, int64_t N, int64_t K, int32_t x_dtype, const void *x, int64_t ldx, int32_t rms,
+                                float eps, const int8_t *W, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
+                                void *workspace, size_t ws_bytes, void *stream) {
+    hm_status st = check_product(M, N, K, W, w_scale, dtype, C, ldc);
+    if (st == HM_OK) st = check_quantize(M, K, x_dtype, x, ldx, rms, eps);
+    if (st != HM_OK) return st;
+    if (M == 0 || N == 0) return HM_OK;
+    if ((st = check_workspace(workspace, ws_bytes, int8_rows_bytes(M, K))) != HM_OK) return st;
+    int8_t *q = static_cast<int8_t *>(workspace);
+    float *scale = reinterpret_cast<float *>(q + (M + 15) / 16 * ((K + 63) / 64) * 1024);
+    const hm::QuantArgs a{M, K, x_dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, scale};
+    const hm::Int8GemmArgs g{M, N, K, q, scale, W, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
+    return hm::launch_dense_int8_rows(a, g, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
 static hm_status check_drafts(int64_t batch, int64_t drafts, int64_t vocab) {

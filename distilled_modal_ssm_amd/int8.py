@@ -28,11 +28,10 @@ class Int8Dense:
         self.N, self.K = int(weight.shape[0]), int(weight.shape[1])
         if self.K < 1 or self.K > hb.HM_INT8_MAX_K:
             raise ValueError(f"1 to {hb.HM_INT8_MAX_K} inputs, got {self.K}")
-        self._block_row = hb.hyena_int8_bytes(16, self.K)
+        self._ws_bytes = {}  # of each number of rows
         self._types = {torch.float32: hb.HM_F32, torch.bfloat16: hb.HM_BF16}
         self._ws = {}  # scratch memory of each stream; a captured graph has its own
-        lib = hb.load()
-        self._quantize, self._product = lib.hyena_quantize_rows, lib.hyena_dense_int8
+        self._product = hb.load().hyena_dense_int8_rows
         ld, dtype = self._rows("weight", weight, self.N, self.K)
         with hb._On(self.device, stream) as s:
             self.weight8 = torch.empty(hb.hyena_int8_bytes(self.N, self.K), dtype=torch.int8, device=self.device)
@@ -66,12 +65,14 @@ class Int8Dense:
     def _run(self, x, M, ld, dtype, rms_eps, out, ldo, otype, stream):
         if out is None:
             out = self.torch.empty((M, self.N), dtype=x.dtype, device=self.device)
-        at = -(-M // 16) * self._block_row  # the rows' scales behind the rows
-        scratch = hb._scratch(self._ws, at + 4 * M, stream, self.device)
-        ws = scratch.data_ptr()
-        # (straight to the C entry points: a token's call counts in microseconds)
-        hb._check(self._quantize(M, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0, ws, ws + at,
-                                 stream), "hyena_quantize_rows")
-        hb._check(self._product(M, self.N, self.K, ws, ws + at, self.weight8.data_ptr(), self.weight_scale.data_ptr(),
-                                otype, out.data_ptr(), ldo, stream), "hyena_dense_int8")
+        n = self._ws_bytes.get(M)
+        if n is None:
+            if len(self._ws_bytes) >= 1024:
+                self._ws_bytes.clear()
+            n = self._ws_bytes[M] = hb.hyena_dense_int8_rows_workspace(M, self.K)
+        ws = hb._scratch(self._ws, n, stream, self.device)
+        # (straight to the C entry point: a token's call counts in microseconds)
+        hb._check(self._product(M, self.N, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0,
+                                self.weight8.data_ptr(), self.weight_scale.data_ptr(), otype, out.data_ptr(), ldo,
+                                ws.data_ptr(), n, stream), "hyena_dense_int8_rows")
         return out

@@ -805,6 +805,18 @@ hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, con
                            const int8_t *W, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
                            void *stream);
 
+/*
+ * Both for rows of float32 or bfloat16: hyena_quantize_rows of x, and the products with
+ * W.  workspace: hyena_dense_int8_rows_workspace bytes, 256-byte aligned, scratch.  (A few
+ * short rows take one launch, else two.)
+ */
+hm_status hyena_dense_int8_rows_workspace(int64_t M, int64_t K, size_t *bytes);
+
+hm_status hyena_dense_int8_rows(int64_t M, int64_t N, int64_t K, int32_t x_dtype, const void *x,
+                                int64_t ldx, int32_t rms, float eps, const int8_t *W,
+                                const float *w_scale, int32_t dtype, void *C, int64_t ldc,
+                                void *workspace, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------------
  * Verification of drafted tokens: a small model drafts a few tokens, the target
  * model reads them all at once, and what is kept of them and drawn behind them

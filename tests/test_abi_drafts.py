@@ -160,6 +160,30 @@ def test_dense_int8_arguments(kw, status):
     _refused(status, _dense, **kw)
 
 
+def _dense_rows(**kw):
+    a = dict(M=4, N=50, K=100, x_dtype=hb.HM_F32, x=FAKE, ldx=100, rms=0, eps=0.0, W=FAKE, w_scale=FAKE, dtype=hb.HM_BF16,
+             C=FAKE, ldc=50, workspace=FAKE, ws_bytes=1 << 30, stream=0)
+    hb.hyena_dense_int8_rows(**{**a, **kw})
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), BAD), (dict(N=-1), BAD), (dict(K=0), BAD), (dict(K=131073, ldx=1 << 18), NO), (dict(dtype=7), NO),
+    (dict(x_dtype=7), NO), (dict(ldc=49), BAD), (dict(ldx=99), BAD), (dict(x=None), BAD), (dict(W=None), BAD),
+    (dict(C=None), BAD), (dict(w_scale=None), BAD), (dict(x=FAKE + 2), NO), (dict(W=FAKE + 4), NO), (dict(C=FAKE + 1), NO),
+    (dict(w_scale=FAKE + 2), NO), (dict(rms=1, eps=-1.0), BAD), (dict(M=1 << 24), NO), (dict(workspace=None), WS),
+    (dict(ws_bytes=2048), WS), (dict(workspace=FAKE + 64), NO), (dict(M=1 << 23, ldx=1 << 24), BAD),
+])
+def test_dense_int8_rows_arguments(kw, status):
+    _refused(status, _dense_rows, **kw)
+
+
+def test_dense_int8_rows_workspace():
+    assert hb.hyena_dense_int8_rows_workspace(33, 65) == 3 * 2 * 1024 + 256
+    assert hb.hyena_dense_int8_rows_workspace(0, 65) == 0
+    _refused(BAD, hb.hyena_dense_int8_rows_workspace, 1, 0)
+    assert hb.load().hyena_dense_int8_rows_workspace(1, 1, None) == BAD
+
+
 def _verify(**kw):
     a = dict(batch=3, drafts=4, vocab=1000, dtype=hb.HM_F32, p=FAKE, ld_p=1000, q=FAKE, ld_q=1000, tokens=FAKE,
              lengths=None, u=FAKE, out_tokens=FAKE, out_accepted=FAKE, workspace=FAKE, ws_bytes=1 << 30, stream=0)
@@ -187,6 +211,8 @@ def test_empty_problems_need_no_gpu():
     _quantize(M=0, x=None, q=None, scale=None)
     _dense(M=0, A=None, a_scale=None, C=None)
     _dense(N=0, W=None, w_scale=None, C=None)
+    _dense_rows(M=0, x=None, C=None, workspace=None, ws_bytes=0)
+    _dense_rows(N=0, W=None, w_scale=None, C=None, workspace=None, ws_bytes=0)
     _verify(batch=0, p=None, q=None, tokens=None, u=None, out_tokens=None, out_accepted=None, workspace=None, ws_bytes=0)
     assert hb.hyena_draft_verify_workspace(0, 4, 1000) == 0
     assert hb.load().hyena_draft_verify_workspace(1, 4, 1000, None) == BAD
@@ -226,8 +252,7 @@ def _scratch_users(monkeypatch):
     monkeypatch.setattr(hb, "_On", OnHost)
     monkeypatch.setattr(hb, "hyena_quantize_rows", lambda *a: None)
     dense = Int8Dense(torch.zeros(30, 100))
-    dense._quantize = lambda *a: seen.append((a[-3], a[-2] - a[-3])) or hb.HM_OK
-    dense._product = lambda *a: hb.HM_OK
+    dense._product = lambda *a: seen.append((a[-3], a[-2])) or hb.HM_OK
 
     def product(n):
         dense(torch.zeros(n, 100))

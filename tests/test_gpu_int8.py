@@ -152,6 +152,37 @@ def test_products_in_tiles(act, M, N):
             wide.fill_(5.0)
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("K", [4, 64, 130, 512, 1000, 2048, 2050])
+def test_few_rows_in_one_launch(act, M, K):
+    """Up to 8 rows of up to 2048 inputs are brought to 8 bits by the product itself: as the two calls do."""
+    torch = require_gpu()
+    log(f"few {act} {M} {K}")
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    dt = torch.bfloat16 if act == "bf16" else torch.float32
+    x = (torch.randn(M, K, generator=g, device="cuda") * torch.exp(torch.randn(M, 1, generator=g, device="cuda"))).to(dt)
+    if M > 2:
+        x[1] = 0
+        x[2, K // 2] = float("inf") if M == 4 else 3.0
+    op = Int8Dense(torch.randn(77, K, generator=g, device="cuda").to(dt))
+    for eps in (None, 1e-6):
+        q = torch.empty(hb.hyena_int8_bytes(M, K), dtype=torch.int8, device="cuda")
+        s = torch.empty(M, device="cuda")
+        hb.hyena_quantize_rows(M, K, hb.HM_BF16 if act == "bf16" else hb.HM_F32, x, K, eps is not None, eps or 0.0, q, s)
+        for ot in (torch.float32, torch.bfloat16):
+            want = torch.empty(M, 77, dtype=ot, device="cuda")
+            hb.hyena_dense_int8(M, 77, K, q, s, op.weight8, op.weight_scale, hb.HM_BF16 if ot == torch.bfloat16 else hb.HM_F32,
+                                want, 77)
+            got = op(x, out=torch.empty_like(want), rms_eps=eps)
+            # (a row's sum of squares may be added in another order: K / 256 + 18 roundings of the scale)
+            tol = 0 if eps is None else (K / 256 + 18) * 2.0 ** -24 + (2.0 ** -7 if ot == torch.bfloat16 else 0)
+            a, b = got.double(), want.double()
+            assert torch.equal(torch.isnan(a), torch.isnan(b)) and (M < 3 or bool(torch.isnan(a[2]).all()) == (M == 4))
+            a, b = torch.nan_to_num(a), torch.nan_to_num(b)
+            assert bool(((a - b).abs() <= tol * b.abs()).all())
+
+
 def test_largest_sums():
     """All products 127^2 of 131072 inputs: 2.11e9, below 2^31."""
     torch = require_gpu()
