@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kGroup = 8;          // workgroups that join one by one
 constexpr uint64_t kMark = ~0ull;  // a word that is not there yet
+constexpr int kPatience = 1 << 20; // looks at a word
 
 // ------------------------------------------------------------------ gates
 
@@ -177,10 +178,12 @@ __device__ __forceinline__ void put_word(uint64_t *p, float A, float H) {
     __hip_atomic_store(p, (uint64_t)bits << 32 | __float_as_uint(H), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// A lane's V words at p, as soon as they are there.
+// A lane's V words at p, as soon as they are there.  (A word that never comes, in a
+// workspace that another call writes to at the same time, is taken as the mark, a NaN,
+// after about a second.)
 template <int V> __device__ __forceinline__ void wait_words(const uint64_t *p, float2 *out) {
     uint64_t word[V];
-    for (;;) {
+    for (int turn = 0; turn < kPatience; ++turn) {
         bool there = true;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -285,6 +288,7 @@ __global__ __launch_bounds__(W *kWave, 4) void recurrence_kernel(RecurArgs a, in
     const uint32_t tiles = (uint32_t)((a.D + kWave * V - 1) / (kWave * V)), row_tiles = (uint32_t)a.B * tiles;
     const uint32_t row_tile = blockIdx.x % row_tiles, tile = row_tile % tiles;
     const int place = draw_place(a, row_tile, places);
+    if (place >= places) return;  // (no counter of this call's says so)
     const int64_t b = row_tile / tiles, c0 = (int64_t)tile * (kWave * V);
     const bool mine = c0 + lane * V < a.D;
     // lanes past the last channel read their neighbours' states and write nothing
@@ -420,6 +424,7 @@ __global__ __launch_bounds__(W *kWave, 4) void recurrence_backward_kernel(RecurA
     const uint32_t tiles = (uint32_t)((a.D + kWave * V - 1) / (kWave * V)), row_tiles = (uint32_t)a.B * tiles;
     const uint32_t row_tile = blockIdx.x % row_tiles, tile = row_tile % tiles;
     const int run = places - 1 - draw_place(a, row_tile, places);  // the last ones first
+    if (run < 0) return;
     const int64_t b = row_tile / tiles, c0 = (int64_t)tile * (kWave * V);
     const bool mine = c0 + lane * V < a.D;
     const int64_t at = mine ? lane * V : a.D - V - c0;
