@@ -288,3 +288,24 @@ def test_recurrence_workspaces_of_short_and_long_prompts():
     places = -(-100000 // 64)
     groups = -(-places // 8)
     assert hb.hyena_recurrence_workspace(d, 100000) == 3 * 2 * 128 + 3 * 128 * (places + groups + -(-groups // 8)) * 8
+
+
+def test_tensors_of_the_host_are_refused(monkeypatch):
+    """Before any call of the library: its pointers are device pointers."""
+    import torch
+    from distilled_modal_ssm_amd import DraftVerify, GatedRecurrence, Int8Dense
+
+    def never(*a):
+        raise AssertionError("called")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    rec, verify = GatedRecurrence(1, 16, "f32", device="cpu"), DraftVerify(1, 1, 9, device="cpu")
+    rec._prompt = rec._token = verify._verify = never
+    monkeypatch.setattr(hb, "hyena_recurrence_backward", never)
+    monkeypatch.setattr(hb, "hyena_quantize_rows", never)
+    x = torch.zeros(1, 3, 16)
+    for call in (lambda: rec.prefill(x, x, x), lambda: rec.decode_step(x[:, 0], x[:, 0], x[:, 0], torch.zeros(1, 16)),
+                 lambda: rec.backward(x, x, x, x, torch.zeros(1, 1, 16)), lambda: Int8Dense(torch.zeros(4, 4)),
+                 lambda: verify.verify(torch.zeros(1, 2, 9), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2))):
+        with pytest.raises(ValueError):
+            call()
