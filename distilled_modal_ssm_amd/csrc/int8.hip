@@ -323,75 +323,56 @@ __global__ __launch_bounds__(WGM *WGN *kWave, NB == 4 ? 1 : MT * NT == 32 ? 2 : 
             const int64_t n = col0 + 16 * j + 4 * (lane / 16) + e;
             sw[j][e] = g.w_scale[n < g.N ? n : g.N - 1];
         }
-    if constexpr (ACT == kF32) {
-        const bool pieces = g.ldc % 4 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0;
+    // Through the LDS: each wave writes its tile, a part at a time, into one of the stage
+    // arrays and reads it back as whole rows, so that a store writes rows' neighbouring
+    // columns.  Chunk c of 16 bytes is at c ^ (row % chunks).  (Stored from the registers,
+    // float32 rows of odd length took 36 us of 419 x 23331 x 266, now 22.)
+    constexpr int kCols = 16 * NT, EB = A::kBytes, E = 16 / EB, kChunks = kCols / E, kStage = (BM < BN ? BM : BN) * BK;
+    constexpr int kPart = MT * 16 * kCols * EB <= kStage ? MT : kStage / (16 * kCols * EB);  // row tiles at once
+    static_assert(kPart > 0 && MT % kPart == 0 && (NB > 3 ? kWaves <= 8 : kWaves <= 4), "a part of a wave's tile in a stage array");
+    using T = typename A::T;
+    __builtin_amdgcn_s_waitcnt(0);  // the loads past the last stage
+    __syncthreads();
+    int8_t *stage = w == 0 ? A0 : w == 1 ? A1 : w == 2 ? A2 : w == 3 ? W0 : w == 4 ? W1 : w == 5 ? W2 : w == 6 ? W3 : A3;
+    T *ob = reinterpret_cast<T *>(stage);
+    auto place_in = [&](int row, int c) { return row * kCols + E * (c ^ (row % kChunks)); };
+    const bool pieces = g.ldc % E == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && col0 + kCols <= g.N;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int64_t m = row0 + 16 * i + lane % 16;
-            if (m >= g.M) continue;
-            float *C = static_cast<float *>(g.C) + m * g.ldc;
+    for (int i0 = 0; i0 < MT; i0 += kPart) {
+#pragma unroll
+        for (int i = i0; i < i0 + kPart; ++i) {
+            const int row = 16 * (i - i0) + lane % 16;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const int64_t n = col0 + 16 * j + 4 * (lane / 16);
                 float y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
-                if (pieces && n + 4 <= g.N) {
-                    *reinterpret_cast<float4 *>(C + n) = make_float4(y[0], y[1], y[2], y[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < g.N) C[n + e] = y[e];
-                }
+                if constexpr (ACT == kF32)
+                    *reinterpret_cast<float4 *>(&ob[place_in(row, 4 * j + lane / 16)]) = make_float4(y[0], y[1], y[2], y[3]);
+                else
+                    *reinterpret_cast<uint2 *>(&ob[place_in(row, 2 * j + lane / 32) + 4 * (lane / 16 % 2)]) =
+                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
             }
         }
-    } else {
-        // through the LDS: each wave writes its tile into one of the stage arrays and
-        // reads it back as whole rows, so that a store writes rows' neighbouring columns.
-        // Chunk c of 16 bytes is at c ^ (row % chunks).
-        constexpr int kCols = 16 * NT, kChunks = kCols / 8, kBytes = (BM < BN ? BM : BN) * BK;
-        constexpr int kPart = MT * 16 * kCols * 2 <= kBytes ? MT : kBytes / (16 * kCols * 2);  // row tiles at once
-        static_assert(kPart > 0 && MT % kPart == 0 && (NB > 3 ? kWaves <= 8 : kWaves <= 4), "a part of a wave's tile in a stage array");
-        __builtin_amdgcn_s_waitcnt(0);  // the loads past the last stage
-        __syncthreads();
-        int8_t *stage = w == 0 ? A0 : w == 1 ? A1 : w == 2 ? A2 : w == 3 ? W0 : w == 4 ? W1 : w == 5 ? W2 : w == 6 ? W3 : A3;
-        uint16_t *ob = reinterpret_cast<uint16_t *>(stage);
-        const bool pieces = g.ldc % 8 == 0 && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && col0 + kCols <= g.N;
+        const int64_t first = row0 + 16 * i0;
+        T *C = static_cast<T *>(g.C) + first * g.ldc + col0;
+        if (pieces) {
+            constexpr int kRows = kWave / kChunks;  // rows of a store
 #pragma unroll
-        for (int i0 = 0; i0 < MT; i0 += kPart) {
-#pragma unroll
-            for (int i = i0; i < i0 + kPart; ++i) {
-                const int row = 16 * (i - i0) + lane % 16;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int chunk = 2 * j + lane / 32;
-                    float y[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = (float)acc[i][j][e] * sa[i] * sw[j][e];
-                    *reinterpret_cast<uint2 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks)) + 4 * (lane / 16 % 2)]) =
-                        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-                }
+            for (int t = 0; t < 16 * kPart / kRows; ++t) {
+                const int row = kRows * t + lane / kChunks, chunk = lane % kChunks;
+                const uint4 v = *reinterpret_cast<const uint4 *>(&ob[place_in(row, chunk)]);
+                if (first + row < g.M) *reinterpret_cast<uint4 *>(C + (int64_t)row * g.ldc + E * chunk) = v;
             }
-            const int64_t first = row0 + 16 * i0;
-            uint16_t *C = static_cast<uint16_t *>(g.C) + first * g.ldc + col0;
-            if (pieces) {
-                constexpr int kRows = kWave / kChunks;  // rows of a store
-#pragma unroll
-                for (int t = 0; t < 16 * kPart / kRows; ++t) {
-                    const int row = kRows * t + lane / kChunks, chunk = lane % kChunks;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(&ob[row * kCols + 8 * (chunk ^ (row % kChunks))]);
-                    if (first + row < g.M) *reinterpret_cast<uint4 *>(C + (int64_t)row * g.ldc + 8 * chunk) = v;
-                }
-            } else {
-                constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
+        } else {
+            constexpr int kAcross = kCols < kWave ? kCols : kWave, kRows = kWave / kAcross;
 #pragma unroll 8
-                for (int t = 0; t < 16 * kPart / kRows; ++t) {
-                    const int row = kRows * t + lane / kAcross;
-                    if (first + row >= g.M) continue;
+            for (int t = 0; t < 16 * kPart / kRows; ++t) {
+                const int row = kRows * t + lane / kAcross;
+                if (first + row >= g.M) continue;
 #pragma unroll
-                    for (int c = lane % kAcross; c < kCols; c += kAcross)
-                        if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[row * kCols + 8 * ((c / 8) ^ (row % kChunks)) + c % 8];
-                }
+                for (int c = lane % kAcross; c < kCols; c += kAcross)
+                    if (col0 + c < g.N) C[(int64_t)row * g.ldc + c] = ob[place_in(row, c / E) + c % E];
             }
         }
     }

@@ -39,8 +39,9 @@ class GatedRecurrence:
         self._ws_bytes = {}  # of each length
         self._state_shape = (self.B, self.D)
         lib = hb.load()
-        self._prompt, self._token, self._desc_ref = (lib.hyena_recurrence_prefill, lib.hyena_recurrence_decode_step,
-                                                     ctypes.byref(self.desc))
+        self._prompt, self._grads, self._token = (lib.hyena_recurrence_prefill, lib.hyena_recurrence_backward,
+                                                  lib.hyena_recurrence_decode_step)
+        self._desc_ref = ctypes.byref(self.desc)
 
     def new_state(self):
         return self.torch.zeros(self._state_shape, dtype=self.torch.float32, device=self.device)
@@ -133,26 +134,37 @@ class GatedRecurrence:
         state after the prompt, or None.  out: the four tensors to write (None
         for dq without q) instead of new ones.
         """
-        shape, (ld_q, ld_g, ld_v) = self._inputs(q, g, v, lengths)
-        L = shape[1]
+        shape, lds = self._inputs(q, g, v, lengths)
         ld_dy = self._rows("dy", dy, shape)
-        self._f32("chunk_states", chunk_states, (self.B, -(-L // hb.HM_RECURRENCE_CHUNK), self.D))
+        self._f32("chunk_states", chunk_states, (self.B, -(-shape[1] // hb.HM_RECURRENCE_CHUNK), self.D))
         if dstate_out is not None:
             self._f32("dstate_out", dstate_out, self._state_shape)
-        with hb._On(self.device, stream) as stream:
-            if out is None:
-                new = lambda: self.torch.empty(shape, dtype=self.tdtype, device=self.device)  # noqa: E731
-                out = (None if q is None else new(), new(), new(),
-                       self.torch.empty(self._state_shape, dtype=self.torch.float32, device=self.device))
-            dq, dg, dv, dstate_in = out
-            if (dq is None) != (q is None):
+        if out is not None:
+            if (out[0] is None) != (q is None):
                 raise ValueError("dq goes with q")
-            self._f32("dstate_in", dstate_in, self._state_shape)
-            ws, n = self._workspace(L, stream)
-            hb.hyena_recurrence_backward(self.desc, L, lengths, q, ld_q, g, ld_g, v, ld_v, dy, ld_dy, chunk_states,
-                                         dstate_out, dq, 0 if dq is None else self._rows("dq", dq, shape), dg,
-                                         self._rows("dg", dg, shape), dv, self._rows("dv", dv, shape), dstate_in, ws, n,
-                                         stream)
+            self._f32("dstate_in", out[3], self._state_shape)
+            ld_out = [0 if t is None else self._rows(name, t, shape) for name, t in zip(("dq", "dg", "dv"), out)]
+        else:
+            ld_out = (self.D, self.D, self.D)
+        return hb._call(self._run_backward, self.device, stream, shape, q, g, v, lds, dy, ld_dy, chunk_states, lengths,
+                        dstate_out, out, ld_out)
+
+    def _run_backward(self, shape, q, g, v, lds, dy, ld_dy, chunk_states, lengths, dstate_out, out, ld_out, stream):
+        torch, L = self.torch, shape[1]
+        if out is None:
+            n = 2 if q is None else 3
+            grads = torch.empty((n, *shape), dtype=self.tdtype, device=self.device).unbind(0)  # one allocation
+            out = (*(() if n == 3 else (None,)), *grads,
+                   torch.empty(self._state_shape, dtype=torch.float32, device=self.device))
+        dq, dg, dv, dstate_in = out
+        ws, n = self._workspace(L, stream)
+        hb._check(self._grads(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
+                              None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
+                              dy.data_ptr(), ld_dy, chunk_states.data_ptr(),
+                              None if dstate_out is None else dstate_out.data_ptr(),
+                              None if dq is None else dq.data_ptr(), ld_out[0], dg.data_ptr(), ld_out[1], dv.data_ptr(),
+                              ld_out[2], dstate_in.data_ptr(), None if ws is None else ws.data_ptr(), n, stream),
+                  "hyena_recurrence_backward")
         return out
 
     def decode_step(self, q, g, v, state, y=None, rows=None, state_out=None, stream=None):

@@ -300,8 +300,7 @@ def test_tensors_of_the_host_are_refused(monkeypatch):
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     rec, verify = GatedRecurrence(1, 16, "f32", device="cpu"), DraftVerify(1, 1, 9, device="cpu")
-    rec._prompt = rec._token = verify._verify = never
-    monkeypatch.setattr(hb, "hyena_recurrence_backward", never)
+    rec._prompt = rec._token = rec._grads = verify._verify = never
     monkeypatch.setattr(hb, "hyena_quantize_rows", never)
     x = torch.zeros(1, 3, 16)
     for call in (lambda: rec.prefill(x, x, x), lambda: rec.decode_step(x[:, 0], x[:, 0], x[:, 0], torch.zeros(1, 16)),
