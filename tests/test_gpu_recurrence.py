@@ -267,6 +267,29 @@ def test_prompt_in_pieces_is_the_prompt(act):
     p.check(torch.cat(ys, 1), state)
 
 
+@pytest.mark.parametrize("L", [7, 60, 700])
+@pytest.mark.parametrize("D", [2, 3, 127, 129, 131, 255, 257])
+def test_odd_numbers_of_channels_and_states_in_place(D, L):
+    """Rows that begin between words, two lanes with one channel, states and their gradients replaced."""
+    torch = require_gpu()
+    log(f"odd {D} {L}")
+    p = Problem(torch, 2, L, D, "bf16", lengths=[L, L - 3], resume=True, train=True, shift=1, pad=1)
+    chunks = p.op.new_chunk_states(L)
+    state = p.state.clone()
+    y, last = p.prefill(state_out=state, chunk_states=chunks)
+    assert last is state
+    p.check(y, last)
+    p.state.copy_(state)  # where the prompt left it
+    again = p.op.prefill(p.q, p.g, p.v, lengths=p.lengths, state_in=p.state)
+    at = p.op.prefill(p.q, p.g, p.v, lengths=p.lengths, state_in=p.state, state_out=p.state)
+    assert torch.equal(again[0], at[0]) and torch.equal(again[1], at[1])
+    grads = p.backward(chunks)
+    p.check_grads(*grads)
+    out = (*(torch.empty_like(t) for t in grads[:3]), p.dlast)
+    for a, b in zip(p.backward(chunks, out=out), grads):
+        assert torch.equal(a, b)
+
+
 def test_values_that_are_not_finite_stay_in_their_channel():
     torch = require_gpu()
     log("not finite")
