@@ -92,6 +92,27 @@ template <int E> __device__ __forceinline__ void quantize(const float (&x)[E], f
     }
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A row's 16 bytes `at`, `at` + lanes, .. as they lie, at any alignment; what is past the
+// row's end reads as 0.  (Bounds count 4 bytes: the last of an odd number of bfloat16
+// values comes by itself.)
+template <int ACT, int N>
+__device__ __forceinline__ void load_row(const void *row, int K, int at, int lanes, u32x4 (&piece)[N]) {
+    const auto x = make_region(row, (uint32_t)K * Act<ACT>::kBytes & ~3u);
+#pragma unroll
+    for (int k = 0; k < N; ++k) piece[k] = __builtin_amdgcn_raw_buffer_load_b128(x, 16 * (k * lanes + at), 0, 0);
+    if constexpr (ACT == kBF16) {
+        if (K % 2 == 0) return;
+        const uint32_t last = static_cast<const uint16_t *>(row)[K - 1];
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (8 * (k * lanes + at) + 2 * e == K - 1) piece[k][e] = last;
+    }
+}
+
 // A row in the registers of W waves, N pieces of 16 bytes a lane, read once.
 template <int ACT, int N, int W>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
@@ -100,11 +121,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     const int64_t m = W > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
     if (m >= a.M) return;
     const int lane = W > 1 ? (int)threadIdx.x : (int)threadIdx.x % kWave, K = (int)a.K;
-    const auto x = make_region(static_cast<const unsigned char *>(a.x) + m * a.ldx * EB, (uint32_t)K * EB);
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 piece[N];  // what is past the row's end reads as 0
-#pragma unroll
-    for (int k = 0; k < N; ++k) piece[k] = __builtin_amdgcn_raw_buffer_load_b128(x, 16 * (k * kLanes + lane), 0, 0);
+    u32x4 piece[N];
+    load_row<ACT>(static_cast<const unsigned char *>(a.x) + m * a.ldx * EB, K, lane, kLanes, piece);
     auto values = [&](int k, float (&v)[E]) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -145,9 +163,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     if (lane == 0) a.scale[m] = row_scale(a, s);
 }
 
-// Rows of any alignment and length: one workgroup a row, which is read twice.
+// Longer rows than registers hold: one workgroup a row, which is read twice.
 template <int ACT>
-__global__ __launch_bounds__(256) void quantize_any_rows_kernel(QuantArgs a) {
+__global__ __launch_bounds__(256) void quantize_long_rows_kernel(QuantArgs a) {
     using A = Act<ACT>;
     const int64_t m = blockIdx.x;
     const typename A::T *x = static_cast<const typename A::T *>(a.x) + m * a.ldx;
@@ -164,16 +182,10 @@ __global__ __launch_bounds__(256) void quantize_any_rows_kernel(QuantArgs a) {
     if (tid == 0) a.scale[m] = row_scale(a, s);
 }
 
-// Rows that are read 16 bytes at a time (whose bounds count 4).
-bool in_pieces(const QuantArgs &a) {
-    const int eb = a.act == kBF16 ? 2 : 4;
-    return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ldx * eb % 16 == 0 || a.M == 1) && a.K * eb % 4 == 0;
-}
-
 template <int ACT> void launch_quantize(const QuantArgs &a, hipStream_t stream) {
     constexpr int EB = Act<ACT>::kBytes, E = 16 / EB;
     const dim3 rows((unsigned)a.M);
-    if (!in_pieces(a) || a.K > 16 * E * 256) return quantize_any_rows_kernel<ACT><<<rows, 256, 0, stream>>>(a);
+    if (a.K > 16 * E * 256) return quantize_long_rows_kernel<ACT><<<rows, 256, 0, stream>>>(a);
     if (a.M >= 1024 && a.K <= 4 * E * kWave)
         return quantize_rows_kernel<ACT, 4, 1><<<dim3((unsigned)((a.M + 3) / 4)), 256, 0, stream>>>(a);
     if (a.K <= E * 256) return quantize_rows_kernel<ACT, 1, 4><<<rows, 256, 0, stream>>>(a);
@@ -456,14 +468,11 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
 #pragma unroll
     for (int k = 0; k < kSteps; ++k)  // (past the share: the last step's, not used)
         wf[k] = *reinterpret_cast<const uint4 *>(pw + 1024 * (int64_t)(first + k < steps ? first + k : steps - 1));
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    u32x4 piece[kTurns][N];  // what is past the row's end, or the last row, reads as 0
+    u32x4 piece[kTurns][N];
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
         const int m = w + W * t;
-        const auto x = make_region(static_cast<const unsigned char *>(a.x) + (m < M ? m * a.ldx * EB : 0), m < M ? (uint32_t)K * EB : 0u);
-#pragma unroll
-        for (int k = 0; k < N; ++k) piece[t][k] = __builtin_amdgcn_raw_buffer_load_b128(x, 16 * (k * kWave + lane), 0, 0);
+        load_row<ACT>(static_cast<const unsigned char *>(a.x) + (m < M ? m * a.ldx * EB : 0), m < M ? K : 0, lane, kWave, piece[t]);
     }
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
@@ -556,7 +565,7 @@ hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, hipStream_t stream) {
-    if (g.M <= kFusedRows && g.K <= kFusedK && in_pieces(a)) {
+    if (g.M <= kFusedRows && g.K <= kFusedK) {
         const dim3 grid((unsigned)((g.N + 15) / 16));
         if (a.act == kBF16 && g.act == kBF16) dense_int8_fused_kernel<kBF16, kBF16><<<grid, 256, 0, stream>>>(a, g);
         else if (a.act == kBF16) dense_int8_fused_kernel<kBF16, kF32><<<grid, 256, 0, stream>>>(a, g);
