@@ -65,6 +65,23 @@ def test_rows(act, M, K, pad):
         assert (abs(s.cpu().numpy() - want) <= (2 if eps is None else K / 256 + 18) * 2.0 ** -24 * want).all()
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K", [(2, 32771), (3, 16387), (1, 40961), (5, 7), (1030, 1023)])
+def test_rows_between_words(act, M, K):
+    """Odd rows that begin anywhere, the largest value the last one, and NaN right before and behind them."""
+    torch = require_gpu()
+    log(f"rows between words {act} {M} {K}")
+    g = torch.Generator().manual_seed(M + K)
+    x = torch.full((M, K + 2), float("nan"))
+    x[:, 1:K + 1] = torch.randn(M, K, generator=g)
+    x[:, K] = 9.0
+    x = x.to(torch.bfloat16 if act == "bf16" else torch.float32).cuda()[:, 1:K + 1]
+    ref, scale = quantized64(x.double().cpu().numpy())
+    q, s = _quantize(torch, x)
+    assert (q[:, :K] == ref).all() and (q[:, K:] == 0).all()
+    assert (abs(s.cpu().numpy() - scale) <= 2 * 2.0 ** -24 * scale).all()
+
+
 def test_rows_at_borders():
     """Ties, values next to them, the smallest and largest numbers, rows of zeros and rows that are not finite."""
     torch = require_gpu()
