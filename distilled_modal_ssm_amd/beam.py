@@ -30,7 +30,7 @@ class BeamSearch:
         self.n = self.beams if select is None else int(select)
         self.end_token = -1 if end_token is None else int(end_token)
         self.ws_bytes = hb.hyena_beam_select_workspace(self.groups, self.beams, self.vocab, self.n)
-        self._ws = {}  # scratch memory of each stream; a captured graph has its own
+        self._ws = hb._Scratch()  # a captured graph has its own
         self._select = hb.load().hyena_beam_select
         # outputs are made like these: scores, tokens and parents in one allocation
         self._like = (torch.empty((3, self.groups, self.n), dtype=torch.int32, device=self.device),
@@ -68,14 +68,15 @@ class BeamSearch:
                 for name, x, t in zip(("scores", "tokens", "parents", "finished"), out,
                                       (torch.float32, torch.int32, torch.int32, torch.uint8)):
                     hb._expect("out " + name, x, t, (self.groups, self.n), self.device)
-            ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
-            # (straight to the C entry point: a step's call counts in microseconds)
-            hb._check(self._select(self.groups, self.beams, V, self.n,
-                                   hb.HM_BF16 if dtype == torch.bfloat16 else hb.HM_F32, logits.data_ptr(),
-                                   logits.stride(0) if rows > 1 else V, scores.data_ptr(),
-                                   None if finished is None else finished.data_ptr(), self.end_token,
-                                   out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                                   ws.data_ptr(), self.ws_bytes, stream), "hyena_beam_select")
+            with self._ws.order(stream):
+                ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
+                # (straight to the C entry point: a step's call counts in microseconds)
+                hb._check(self._select(self.groups, self.beams, V, self.n,
+                                       hb.HM_BF16 if dtype == torch.bfloat16 else hb.HM_F32, logits.data_ptr(),
+                                       logits.stride(0) if rows > 1 else V, scores.data_ptr(),
+                                       None if finished is None else finished.data_ptr(), self.end_token,
+                                       out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                                       ws.data_ptr(), self.ws_bytes, stream), "hyena_beam_select")
         return out
 
     def rows(self, parents):

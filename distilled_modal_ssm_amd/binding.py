@@ -718,9 +718,24 @@ def _call(call, device, stream, *args):
         return call(*args, s)
 
 
+class _Scratch(dict):
+    """A handle's scratch memory, a buffer a stream.
+
+    ``with scratch.order(stream):`` around the lookup and the library's call: its kernels hand values on
+    through the buffer, and another thread's call on the same stream must not queue its own in between
+    (ctypes lets other threads run during a call)."""
+
+    def __init__(self):
+        super().__init__()
+        self._locks = {}
+
+    def order(self, stream):
+        return self._locks.get(stream) or self._locks.setdefault(stream, threading.Lock())
+
+
 def _scratch(kept, n, stream, device):
     """n bytes of scratch memory for a call on the current stream, whose hipStream_t is ``stream``: a
-    handle's buffer of that stream, out of its dict ``kept``, or a longer one in its place.
+    handle's buffer of that stream, out of its _Scratch ``kept``, or a longer one in its place.
 
     A graph's replays write to the addresses that its capture saw, so a call that torch captures has
     memory of that graph's own, which lives as long as the graph and which no other call is given."""

@@ -24,7 +24,7 @@ class DraftVerify:
         self.device = torch.empty(0, device=device).device  # with its index
         self.B, self.T, self.V = int(batch), int(drafts), int(vocab)
         self.ws_bytes = hb.hyena_draft_verify_workspace(self.B, self.T, self.V)
-        self._ws = {}  # scratch memory of each stream; a captured graph has its own
+        self._ws = hb._Scratch()  # a captured graph has its own
         self._verify = hb.load().hyena_draft_verify
         self._p_shape, self._q_shape = (self.B, self.T + 1, self.V), (self.B, self.T, self.V)
         self._x_shape, self._u_shape, self._rows = (self.B, self.T), (self.B, self.T + 1), (self.B,)
@@ -69,10 +69,11 @@ class DraftVerify:
         if out is None:
             out = (torch.empty(self._u_shape, dtype=torch.int32, device=self.device),
                    torch.empty(self._rows, dtype=torch.int32, device=self.device))
-        ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
-        # (straight to the C entry point: a step's call counts in microseconds)
-        hb._check(self._verify(self.B, self.T, self.V, hb.HM_BF16 if p.dtype == torch.bfloat16 else hb.HM_F32, p.data_ptr(),
-                               ld_p, None if q is None else q.data_ptr(), ld_q, tokens.data_ptr(),
-                               None if lengths is None else lengths.data_ptr(), u.data_ptr(), out[0].data_ptr(),
-                               out[1].data_ptr(), ws.data_ptr(), self.ws_bytes, stream), "hyena_draft_verify")
+        with self._ws.order(stream):
+            ws = hb._scratch(self._ws, self.ws_bytes, stream, self.device)
+            # (straight to the C entry point: a step's call counts in microseconds)
+            hb._check(self._verify(self.B, self.T, self.V, hb.HM_BF16 if p.dtype == torch.bfloat16 else hb.HM_F32,
+                                   p.data_ptr(), ld_p, None if q is None else q.data_ptr(), ld_q, tokens.data_ptr(),
+                                   None if lengths is None else lengths.data_ptr(), u.data_ptr(), out[0].data_ptr(),
+                                   out[1].data_ptr(), ws.data_ptr(), self.ws_bytes, stream), "hyena_draft_verify")
         return out

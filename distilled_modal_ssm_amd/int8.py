@@ -30,7 +30,7 @@ class Int8Dense:
             raise ValueError(f"1 to {hb.HM_INT8_MAX_K} inputs, got {self.K}")
         self._ws_bytes = {}  # of each number of rows
         self._types = {torch.float32: hb.HM_F32, torch.bfloat16: hb.HM_BF16}
-        self._ws = {}  # scratch memory of each stream; a captured graph has its own
+        self._ws = hb._Scratch()  # a captured graph has its own
         self._product = hb.load().hyena_dense_int8_rows
         ld, dtype = self._rows("weight", weight, self.N, self.K)
         with hb._On(self.device, stream) as s:
@@ -70,9 +70,10 @@ class Int8Dense:
             if len(self._ws_bytes) >= 1024:
                 self._ws_bytes.clear()
             n = self._ws_bytes[M] = hb.hyena_dense_int8_rows_workspace(M, self.K)
-        ws = hb._scratch(self._ws, n, stream, self.device)
-        # (straight to the C entry point: a token's call counts in microseconds)
-        hb._check(self._product(M, self.N, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0,
-                                self.weight8.data_ptr(), self.weight_scale.data_ptr(), otype, out.data_ptr(), ldo,
-                                ws.data_ptr(), n, stream), "hyena_dense_int8_rows")
+        with self._ws.order(stream):
+            ws = hb._scratch(self._ws, n, stream, self.device)
+            # (straight to the C entry point: a token's call counts in microseconds)
+            hb._check(self._product(M, self.N, self.K, dtype, x.data_ptr(), ld, rms_eps is not None, rms_eps or 0.0,
+                                    self.weight8.data_ptr(), self.weight_scale.data_ptr(), otype, out.data_ptr(), ldo,
+                                    ws.data_ptr(), n, stream), "hyena_dense_int8_rows")
         return out

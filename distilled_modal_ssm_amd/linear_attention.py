@@ -36,7 +36,7 @@ class LinearAttention:
         self.desc = hb.make_linattn_desc(self.B, self.H, self.dk, self.dv, hb.HM_BF16 if act == "bf16" else hb.HM_F32,
                                          self.scale, self.q_heads, self.k_heads, self.v_heads)
         hb.hyena_linattn_prefill_workspace(self.desc, 0)  # raises for sizes that the library refuses
-        self._ws = {}  # scratch memory of each stream; a captured graph has its own
+        self._ws = hb._Scratch()  # a captured graph has its own
         self._state_shape = (self.B, self.H, self.dk, self.dv)
         self._token_shapes = ((self.B, self.q_heads * self.dk), (self.B, self.k_heads * self.dk),
                               (self.B, self.v_heads * self.dv), (self.B, self.H * self.dv))
@@ -101,10 +101,11 @@ class LinearAttention:
                 state_out = self.torch.empty(self._state_shape, dtype=self.torch.float32, device=self.device)
             else:
                 self._state("state_out", state_out)
-            ws, n = self._workspace(L, stream)
-            hb.hyena_linattn_prefill(self.desc, L, lengths, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
-                                     self._rows("y", y, (*lead, self.H * self.dv), dt), state_in, state_out, ws, n,
-                                     stream)
+            with self._ws.order(stream):
+                ws, n = self._workspace(L, stream)
+                hb.hyena_linattn_prefill(self.desc, L, lengths, q, ld_q, k, ld_k, v, ld_v, log_decay, ld_a, y,
+                                         self._rows("y", y, (*lead, self.H * self.dv), dt), state_in, state_out, ws, n,
+                                         stream)
         return y, state_out
 
     def decode_step(self, q, k, v, state, log_decay=None, y=None, rows=None, state_out=None, stream=None):

@@ -35,7 +35,7 @@ class GatedRecurrence:
         self.desc = hb.make_recurrence_desc(self.B, self.D, hb.HM_BF16 if act == "bf16" else hb.HM_F32, hb.GATES[gate],
                                             hb.GATE_INPUTS[input])
         hb.hyena_recurrence_workspace(self.desc, 0)  # raises for sizes that the library refuses
-        self._ws = {}  # scratch memory of each stream; a captured graph has its own
+        self._ws = hb._Scratch()  # a captured graph has its own
         self._ws_bytes = {}  # of each length
         self._state_shape = (self.B, self.D)
         lib = hb.load()
@@ -117,13 +117,14 @@ class GatedRecurrence:
             y = torch.empty(shape, dtype=self.tdtype, device=self.device)
         if state_out is None:
             state_out = torch.empty(self._state_shape, dtype=torch.float32, device=self.device)
-        ws, n = self._workspace(L, stream)
-        # (straight to the C entry point: a few tokens' call counts in microseconds)
-        hb._check(self._prompt(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
-                               None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
-                               y.data_ptr(), ld_y, None if state_in is None else state_in.data_ptr(),
-                               state_out.data_ptr(), None if chunk_states is None else chunk_states.data_ptr(),
-                               None if ws is None else ws.data_ptr(), n, stream), "hyena_recurrence_prefill")
+        with self._ws.order(stream):
+            ws, n = self._workspace(L, stream)
+            # (straight to the C entry point: a few tokens' call counts in microseconds)
+            hb._check(self._prompt(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
+                                   None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
+                                   y.data_ptr(), ld_y, None if state_in is None else state_in.data_ptr(),
+                                   state_out.data_ptr(), None if chunk_states is None else chunk_states.data_ptr(),
+                                   None if ws is None else ws.data_ptr(), n, stream), "hyena_recurrence_prefill")
         return y, state_out
 
     def backward(self, q, g, v, dy, chunk_states, lengths=None, dstate_out=None, out=None, stream=None):
@@ -157,14 +158,15 @@ class GatedRecurrence:
             out = (*(() if n == 3 else (None,)), *grads,
                    torch.empty(self._state_shape, dtype=torch.float32, device=self.device))
         dq, dg, dv, dstate_in = out
-        ws, n = self._workspace(L, stream)
-        hb._check(self._grads(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
-                              None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
-                              dy.data_ptr(), ld_dy, chunk_states.data_ptr(),
-                              None if dstate_out is None else dstate_out.data_ptr(),
-                              None if dq is None else dq.data_ptr(), ld_out[0], dg.data_ptr(), ld_out[1], dv.data_ptr(),
-                              ld_out[2], dstate_in.data_ptr(), None if ws is None else ws.data_ptr(), n, stream),
-                  "hyena_recurrence_backward")
+        with self._ws.order(stream):
+            ws, n = self._workspace(L, stream)
+            hb._check(self._grads(self._desc_ref, L, None if lengths is None else lengths.data_ptr(),
+                                  None if q is None else q.data_ptr(), lds[0], g.data_ptr(), lds[1], v.data_ptr(), lds[2],
+                                  dy.data_ptr(), ld_dy, chunk_states.data_ptr(),
+                                  None if dstate_out is None else dstate_out.data_ptr(),
+                                  None if dq is None else dq.data_ptr(), ld_out[0], dg.data_ptr(), ld_out[1],
+                                  dv.data_ptr(), ld_out[2], dstate_in.data_ptr(), None if ws is None else ws.data_ptr(), n,
+                                  stream), "hyena_recurrence_backward")
         return out
 
     def decode_step(self, q, g, v, state, y=None, rows=None, state_out=None, stream=None):

@@ -39,6 +39,11 @@
  *  - Errors are returned as hm_status, never thrown.  Arguments are validated on
  *    the host before any HIP call; on a validation error nothing is enqueued.
  *    HM_ERR_HIP reports a failed kernel launch (hipGetLastError after launch).
+ *  - Workspaces are scratch memory through which the kernels of one call hand values
+ *    on.  A workspace may be given to another call once the first has returned, for
+ *    the same stream, or once its kernels have run.  Two host threads must not give
+ *    one workspace to two calls at the same time, on one stream either: the kernels
+ *    of one could be queued between the other's, and both would return HM_OK.
  *  - Alignment: every pointer must be aligned to its element (2 bytes for
  *    bfloat16, 4 for float32, 8 for the complex state); otherwise
  *    HM_ERR_UNSUPPORTED.  Wider vector paths are chosen automatically when
