@@ -781,7 +781,7 @@ class ModalHyena:
     def __init__(self, poles, residues, skip, batch: int, channels: int, act: str, device="cuda"):
         import torch
         self.torch = torch
-        self.device = torch.device(device)
+        self.device = torch.empty(0, device=device).device  # with its index
         t = lambda a: torch.as_tensor(a, dtype=torch.float32).contiguous().to(self.device)
         self.poles, self.residues, self.skip = t(poles), t(residues), t(skip)
         self.H, self.d = int(self.poles.shape[0]), int(self.poles.shape[1])
@@ -791,19 +791,20 @@ class ModalHyena:
         self.tdtype = torch.bfloat16 if act == "bf16" else torch.float32
         self.desc = make_desc(self.B, self.D, self.H, self.d, HM_BF16 if act == "bf16" else HM_F32,
                               self.poles, self.residues, self.skip)
-        self._ws = None
+        self._buffers = _Scratch()
 
     def new_state(self):
         return self.torch.zeros((self.B, self.H, self.d, self.P, 2), dtype=self.torch.float32,
                                 device=self.device)
 
-    def workspace(self, L: int, chunk: int = 0, algo="auto"):
+    @property
+    def _ws(self):
+        return self._buffers or None  # (None before the first)
+
+    def workspace(self, L: int, chunk: int = 0, algo="auto", stream: int = 0):
+        """Scratch memory of a prompt on the current stream, whose hipStream_t is ``stream``, and its bytes."""
         n = hyena_modal_prefill_workspace(self.desc, L, chunk, algo)
-        if self.torch.cuda.is_current_stream_capturing():  # as in _scratch: the graph's own
-            return self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device), n
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device)
-        return self._ws, n
+        return _scratch(self._buffers, max(n, 256), stream, self.device), n
 
     def plan(self, L: int, chunk: int = 0, algo="auto") -> dict:
         return hyena_modal_prefill_plan(self.desc, L, chunk, algo)
@@ -815,15 +816,17 @@ class ModalHyena:
         algo: "auto", "scan" (vector-ALU modal scan) or "mfma" (matrix-core sub-blocks).
         """
         B, L = q.shape[0], q.shape[1]
-        if y is None:
-            y = self.torch.empty((B, L, self.D), dtype=self.tdtype, device=self.device)
-        if state_out is None:
-            state_out = self.new_state()
         ld_in = _row_stride(q, (k, v))
-        ld_y = _row_stride(y, ())
-        ws, n = self.workspace(L, chunk, algo)
-        hyena_modal_prefill(self.desc, L, q, k, v, ld_in, y, ld_y, state_in, state_out, ws, n,
-                            stream, chunk, algo)
+        with _On(self.device, stream) as stream:
+            if y is None:
+                y = self.torch.empty((B, L, self.D), dtype=self.tdtype, device=self.device)
+            if state_out is None:
+                state_out = self.new_state()
+            ld_y = _row_stride(y, ())
+            with self._buffers.order(stream):
+                ws, n = self.workspace(L, chunk, algo, stream)
+                hyena_modal_prefill(self.desc, L, q, k, v, ld_in, y, ld_y, state_in, state_out, ws, n,
+                                    stream, chunk, algo)
         return y, state_out
 
     def fft_prefill(self, q, k, v, y=None, stream=None):

@@ -93,7 +93,7 @@ def _users(torch, monkeypatch, library):
     }
 
 
-USERS = ["recurrence", "gradients", "verify", "dense", "attention", "beams"]
+USERS = ["recurrence", "gradients", "verify", "dense", "attention", "beams", "modal"]
 
 
 @pytest.mark.parametrize("user", USERS)
@@ -114,6 +114,19 @@ def test_threads_on_one_stream(monkeypatch, user):
     for t in threads:
         t.join()
     library.check(2 * calls)
+
+
+@pytest.mark.parametrize("user", USERS)
+def test_streams_have_buffers_of_their_own(monkeypatch, user):
+    """Their kernels run at the same time; a stream's next call finds its own again."""
+    import torch
+    library = _Library()
+    call = _users(torch, monkeypatch, library)[user]
+    for stream in (1, 2, None, 1, 2, None):
+        call(stream)
+    assert [s for s, _, _ in library.queue[::2]] == [1, 2, 0, 1, 2, 0]
+    at = [ws for _, ws, _ in library.queue[::2]]
+    assert at[:3] == at[3:] and len(set(at)) == 3
 
 
 @pytest.mark.parametrize("user", USERS)
