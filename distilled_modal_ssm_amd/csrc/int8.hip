@@ -71,10 +71,38 @@ template <int W> __device__ __forceinline__ RowStat joined(RowStat s) {
     return s;
 }
 
-__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s) {
-    float scale = __uint_as_float(s.top) / 127.0f;
-    if (a.rms) scale = scale / sqrtf(s.sum / (float)a.K + a.eps);
-    return s.top < 0x7f800000u ? scale : __builtin_nanf("");
+// Whether the row's squares have to be summed again, in float64: where float32's sum has
+// left its range, or where squares below 2^-149 could count, of rows below 2^-50 (K of
+// them are less than 2^-132, and the largest square is 2^-100 at least) without an eps
+// that is larger than any of them.
+__device__ __forceinline__ bool sum_again(const QuantArgs &a, const RowStat &s) {
+    if (!a.rms || s.top == 0 || s.top >= 0x7f800000u) return false;
+    return !(s.sum < __builtin_inff()) || (__uint_as_float(s.top) < 0x1p-50f && a.eps < 0x1p-100f);
+}
+
+// That sum of W waves' row, in all of them.
+template <int W> __device__ __forceinline__ double joined(double sum) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    if constexpr (W > 1) {
+        __shared__ double all[W];
+        if (threadIdx.x % kWave == 0) all[threadIdx.x / kWave] = sum;
+        __syncthreads();
+        sum = all[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += all[w];
+    }
+    return sum;
+}
+
+// squares: where sum_again says so.  Rows whose amax / 127 would be subnormal, and lose
+// digits that the root gives back, are scaled in float64 too.
+__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s, double squares) {
+    const float amax = __uint_as_float(s.top);
+    if (s.top >= 0x7f800000u) return __builtin_nanf("");
+    if (!a.rms || s.top == 0) return amax / 127.0f;
+    if (sum_again(a, s) || amax < 0x1p-118f) return (float)(amax / 127.0 / sqrt(squares / (double)a.K + (double)a.eps));
+    return amax / 127.0f / sqrtf(s.sum / (float)a.K + a.eps);
 }
 
 // E values' integers as bytes.
@@ -133,6 +161,19 @@ template <int ACT, int N> __device__ __forceinline__ void take_row(RowStat &s, c
     }
 }
 
+template <int ACT, int N> __device__ __forceinline__ double squares_of(const u32x4 (&piece)[N]) {
+    constexpr int E = 16 / Act<ACT>::kBytes;
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float v[E];
+        piece_values<ACT>(piece, k, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum = fma((double)v[e], (double)v[e], sum);
+    }
+    return sum;
+}
+
 // The integers of load_row's values, to row r of blocks that have `end` columns.
 template <int ACT, int N>
 __device__ __forceinline__ void put_row(int8_t *blocks, int r, int end, int at, int lanes, const u32x4 (&piece)[N], const RowStat &s) {
@@ -172,7 +213,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     take_row<ACT>(s, piece);
     s = joined<W>(s);
     put_row<ACT>(a.q + block_of(m, K), (int)(m % 16), (K + 63) / 64 * 64, lane, kLanes, piece, s);
-    if (lane == 0) a.scale[m] = row_scale(a, s);
+    const double squares = sum_again(a, s) ? joined<W>(squares_of<ACT>(piece)) : 0.0;
+    if (lane == 0) a.scale[m] = row_scale(a, s, squares);
 }
 
 // Longer rows: one workgroup a row, which is read twice, the second time from the caches
@@ -195,7 +237,15 @@ __global__ __launch_bounds__(256) void quantize_long_rows_kernel(QuantArgs a) {
         load_row<ACT>(x + (int64_t)k * EB, K - k < kTurn ? K - k : kTurn, tid, 256, piece);
         put_row<ACT>(q + (int64_t)k / 64 * 1024, (int)(m % 16), end - k, tid, 256, piece, s);
     }
-    if (tid == 0) a.scale[m] = row_scale(a, s);
+    double squares = 0.0;
+    if (sum_again(a, s)) {
+        for (int k = 0; k < K; k += kTurn) {
+            load_row<ACT>(x + (int64_t)k * EB, K - k < kTurn ? K - k : kTurn, tid, 256, piece);
+            squares += squares_of<ACT>(piece);
+        }
+        squares = joined<4>(squares);
+    }
+    if (tid == 0) a.scale[m] = row_scale(a, s, squares);
 }
 
 template <int ACT> void launch_quantize(const QuantArgs &a, hipStream_t stream) {
@@ -498,7 +548,8 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
         take_row<ACT>(s, piece[t]);
         s = joined<1>(s);
         put_row<ACT>(rows, m, 64 * steps, lane, kWave, piece[t], s);
-        if (lane == 0) scales[m] = row_scale(a, s);
+        const double squares = sum_again(a, s) ? joined<1>(squares_of<ACT>(piece[t])) : 0.0;
+        if (lane == 0) scales[m] = row_scale(a, s, squares);
     }
     __syncthreads();
     i32x4 acc = {0, 0, 0, 0};  // (rows that are none hold anything, and are not stored)

@@ -789,7 +789,8 @@ hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes);
  *     amax = max_k |x[m][k]|,  q[m][k] = rint(127 x[m][k] / amax) (ties to even),
  *     scale[m] = amax / 127,  or with rms != 0  amax / 127 / sqrt(mean_k x^2 + eps).
  * The integers are those of the exact quotient.  A row of zeros gets zeros and
- * scale 0; a row with a value that is not finite gets zeros and scale NaN.
+ * scale 0, with eps = 0 too; a row with a value that is not finite gets zeros and
+ * scale NaN.  The mean counts squares beyond float32's range at their value.
  *   x [M][ldx] of dtype (hm_dtype), K columns;  q  hyena_int8_bytes bytes, columns from
  *   K on set to 0, rows from M on left as they are;  scale [M].
  * Tokens (rows of activations) and output channels (rows of W) alike.

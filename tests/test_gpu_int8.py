@@ -251,3 +251,37 @@ def test_captured_products_replay():
         torch.cuda.synchronize()
         op(torch.randn(90, 300, generator=g, device="cuda"))
         assert torch.equal(got, op(x, rms_eps=1e-6))
+
+
+SIZES = [0.0, 1.0, 1e-12, 1e-19, 1e-25, 1e-40, 1e18, 1e20, 1e37]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-37, 1e-6])
+@pytest.mark.parametrize("M,K", [(9, 33), (9, 515), (9, 4001), (9, 16385), (9, 40000), (1026, 513)])
+def test_root_mean_squares_of_any_size(act, eps, M, K):
+    """Rows whose squares leave float32's range at either end, rows of zeros without eps, a large value among small
+    ones; in every kernel that brings rows to 8 bits.  A scale formed in float64 is rounded once (a subnormal one to
+    2^-150), others as in the module's text."""
+    torch = require_gpu()
+    log(f"rms {act} {eps} {M} {K}")
+    g = torch.Generator().manual_seed(K)
+    size = torch.tensor([SIZES[m % 9] for m in range(M)], dtype=torch.float64)
+    x = torch.randn(M, K, generator=g).double() * size[:, None]
+    x[5, K // 2], x[6, K - 1] = 1.0, 3e38
+    x = x.to(torch.bfloat16 if act == "bf16" else torch.float32).cuda()
+    x64 = x.double().cpu().numpy()
+    ref, scale = quantized64(x64)
+    with np.errstate(invalid="ignore"):
+        want = np.nan_to_num(scale / np.sqrt((x64 ** 2).mean(-1) + float(np.float32(eps))))
+    q, s = _quantize(torch, x, eps)
+    assert (q[:, :K] == ref).all()
+    tol = (K / 256 + 18) * 2.0 ** -24 * want + 2.0 ** -150
+    assert (abs(s.cpu().numpy() - want) <= tol).all(), (s, want)
+    op = Int8Dense(torch.randn(50, K, generator=g).cuda())
+    for rows in (slice(0, 8), slice(0, M)):  # in one launch where K is short, and in two
+        y = op(x[rows], rms_eps=eps, out=torch.empty(len(want[rows]), 50, device="cuda"))
+        sums = (torch.from_numpy(ref[rows]) @ torch.from_numpy(_rows_of(op.weight8, 50, K)[:, :K].astype(np.float64)).t()).numpy()
+        exact = sums * want[rows, None] * op.weight_scale.double().cpu().numpy()
+        bad = abs(y.double().cpu().numpy() - exact) - (K / 256 + 20) * 2.0 ** -24 * abs(exact) - 2.0 ** -126
+        assert bad.max() <= 0, np.unravel_index(bad.argmax(), bad.shape)
