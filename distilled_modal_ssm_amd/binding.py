@@ -153,6 +153,17 @@ _lock = threading.Lock()
 _lib = None
 
 
+def _torch_runtime():
+    """Loads the HIP runtime that torch brings along, where it is not loaded yet: the library would bring the
+    system's, torch its own afterwards, and one process must not run two of them."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    for folder in (spec.submodule_search_locations or ()) if spec is not None else ():
+        path = os.path.join(folder, "lib", "libamdhip64.so")
+        if os.path.exists(path):
+            ctypes.CDLL(path)
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library once (raises LibraryMissing if it was not built)."""
     global _lib
@@ -165,6 +176,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             raise LibraryMissing(
                 f"{path} not found: build it with `python -m distilled_modal_ssm_amd.build` "
                 "(or __graft_entry__.build()); there is no CPU fallback")
+        _torch_runtime()
         lib = ctypes.CDLL(path)
         i64, p, sz, f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
         D, A, R = ctypes.POINTER(hm_desc), ctypes.POINTER(hm_linattn_desc), ctypes.POINTER(hm_recurrence_desc)

@@ -6,6 +6,8 @@ same for all) must not queue theirs in between.
 """
 
 import os
+import subprocess
+import sys
 import threading
 import time
 
@@ -20,6 +22,21 @@ def lib():
         from distilled_modal_ssm_amd import build
         build.build()
     return hb.load()
+
+
+@pytest.mark.parametrize("first", ["torch", "library"])
+def test_one_hip_runtime_in_a_process(first):
+    """Whichever of torch and the library is loaded first: torch brings a runtime of its own."""
+    pytest.importorskip("torch")
+    if not os.path.exists("/proc/self/maps"):
+        pytest.skip("no list of mapped files")
+    both = ["import torch", "from distilled_modal_ssm_amd import binding; binding.load()"]
+    code = both if first == "torch" else both[::-1]
+    code += ["print(*sorted({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))"]
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", "\n".join(code)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr
+    assert len(out.stdout.split()) == 1, out.stdout
 
 
 class _Library:
