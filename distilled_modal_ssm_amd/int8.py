@@ -7,7 +7,15 @@ in integers and scales the sums.
 
 from __future__ import annotations
 
+import threading
+import weakref
+
 from . import binding as hb
+
+# A device's scratch memory, as long as a handle is there.  (A model has two handles a
+# layer, and prompts' rows in 8 bits are as large as a layer's weights: one buffer each
+# would take what the weights save.)
+_shared, _sharing = weakref.WeakValueDictionary(), threading.Lock()
 
 
 class Int8Dense:
@@ -30,7 +38,10 @@ class Int8Dense:
             raise ValueError(f"1 to {hb.HM_INT8_MAX_K} inputs, got {self.K}")
         self._ws_bytes = {}  # of each number of rows
         self._types = {torch.float32: hb.HM_F32, torch.bfloat16: hb.HM_BF16}
-        self._ws = hb._Scratch()  # a captured graph has its own
+        with _sharing:
+            self._ws = _shared.get(self.device)
+            if self._ws is None:
+                self._ws = _shared[self.device] = hb._Scratch()  # a captured graph has its own
         self._product = hb.load().hyena_dense_int8_rows
         ld, dtype = self._rows("weight", weight, self.N, self.K)
         with hb._On(self.device, stream) as s:

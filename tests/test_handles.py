@@ -5,6 +5,7 @@ lets other threads run meanwhile.  Two threads on one stream (the default stream
 same for all) must not queue theirs in between.
 """
 
+import gc
 import os
 import subprocess
 import sys
@@ -164,3 +165,25 @@ def test_a_refused_call_lets_the_next_one_in(monkeypatch, user):
     done.join(10)
     assert not done.is_alive()
     library.check(1)
+
+
+def test_a_models_products_share_their_scratch(monkeypatch):
+    """One buffer a device and stream, as long as the longest rows need, given back with the last handle."""
+    import torch
+    from distilled_modal_ssm_amd import Int8Dense
+    library = _Library()
+    _users(torch, monkeypatch, library)
+    layers = [Int8Dense(torch.zeros(30, K)) for K in (100, 400, 200)]
+    for layer in layers:
+        layer._product = library
+    for layer in (layers[1], layers[0], layers[2], layers[1]):
+        layer(torch.zeros(50, layer.K), stream=1)
+    assert len({ws for _, ws, _ in library.queue}) == 1
+    layers[0](torch.zeros(9, 100), stream=2)
+    assert len({ws for _, ws, _ in library.queue}) == 2
+    pool = layers[0]._ws
+    assert all(layer._ws is pool for layer in layers) and len(pool) == 2
+    del pool, layer, layers
+    gc.collect()
+    again = Int8Dense(torch.zeros(30, 100))
+    assert not again._ws
