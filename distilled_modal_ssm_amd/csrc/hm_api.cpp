@@ -1220,6 +1220,16 @@ hm_status hyena_dense_int8_rows_workspace(int64_t M, int64_t K, size_t *bytes) {
     return HM_OK;
 }
 
+// Whether M rows of `width` bytes, `pitch` apart, and M others share no byte.
+static bool rows_apart(const void *a, int64_t pitch_a, int64_t width_a, const void *b, int64_t pitch_b, int64_t width_b,
+                       int64_t M) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    if (p + (uintptr_t)((M - 1) * pitch_a + width_a) <= q || q + (uintptr_t)((M - 1) * pitch_b + width_b) <= p) return true;
+    if (pitch_a != pitch_b) return false;
+    const int64_t off = (int64_t)(q - p) % pitch_a, at = off < 0 ? off + pitch_a : off;  // columns of wider rows
+    return at >= width_a && at + width_b <= pitch_a;
+}
+
 hm_status hyena_dense_int8_rows(int64_t M, int64_t N, int64_t K, int32_t x_dtype, const void *x, int64_t ldx, int32_t rms,
                                 float eps, const int8_t *W, const float *w_scale, int32_t dtype, void *C, int64_t ldc,
                                 void *workspace, size_t ws_bytes, void *stream) {
@@ -1232,7 +1242,9 @@ hm_status hyena_dense_int8_rows(int64_t M, int64_t N, int64_t K, int32_t x_dtype
     float *scale = reinterpret_cast<float *>(q + (M + 15) / 16 * ((K + 63) / 64) * 1024);
     const hm::QuantArgs a{M, K, x_dtype == HM_BF16 ? hm::kBF16 : hm::kF32, x, ldx, rms != 0, eps, q, scale};
     const hm::Int8GemmArgs g{M, N, K, q, scale, W, w_scale, dtype == HM_BF16 ? hm::kBF16 : hm::kF32, C, ldc};
-    return hm::launch_dense_int8_rows(a, g, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
+    const int64_t ex = x_dtype == HM_BF16 ? 2 : 4, ec = dtype == HM_BF16 ? 2 : 4;
+    const bool apart = rows_apart(x, ldx * ex, K * ex, C, ldc * ec, N * ec, M);
+    return hm::launch_dense_int8_rows(a, g, apart, static_cast<hipStream_t>(stream)) == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
 static hm_status check_drafts(int64_t batch, int64_t drafts, int64_t vocab) {

@@ -438,8 +438,8 @@ struct Int8GemmArgs {
 };
 hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream);
 hipError_t launch_dense_int8(const Int8GemmArgs &a, hipStream_t stream);
-// a's rows, brought to a.q and a.scale or not, and their products
-hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, hipStream_t stream);
+// a's rows, brought to a.q and a.scale or not, and their products; apart: these share no memory with the rows
+hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, bool apart, hipStream_t stream);
 
 // Verification of drafted tokens.
 struct VerifyArgs {

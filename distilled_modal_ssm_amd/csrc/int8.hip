@@ -510,8 +510,8 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
     }
 }
 
-// The same for up to kFusedRows rows of up to kFusedK inputs, which every workgroup brings
-// to 8 bits itself while its weights are on their way: wave w takes rows w and w + 4 into
+// The same for up to kFusedRows rows of up to kFusedK inputs that the outputs do not
+// overwrite, which every workgroup brings to 8 bits itself while its weights are on their way: wave w takes rows w and w + 4 into
 // the LDS.  (5 x 6144 x 2048: a call of 8.4 us, 12.0 in two launches.)
 constexpr int kFusedRows = 8, kFusedK = 2048;
 
@@ -600,8 +600,8 @@ hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, hipStream_t stream) {
-    if (g.M <= kFusedRows && g.K <= kFusedK) {
+hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, bool apart, hipStream_t stream) {
+    if (apart && g.M <= kFusedRows && g.K <= kFusedK) {
         const dim3 grid((unsigned)((g.N + 15) / 16));
         if (a.act == kBF16 && g.act == kBF16) dense_int8_fused_kernel<kBF16, kBF16><<<grid, 256, 0, stream>>>(a, g);
         else if (a.act == kBF16) dense_int8_fused_kernel<kBF16, kF32><<<grid, 256, 0, stream>>>(a, g);

@@ -64,7 +64,7 @@ class Int8Dense:
 
     def __call__(self, x, out=None, rms_eps=None, stream=None):
         """y [rows][outputs] of x [rows][inputs], float32 or bfloat16 rows with unit element stride;
-        y of x's type, or ``out`` of either.
+        y of x's type, or ``out`` of either, which may share memory with x.
 
         rms_eps: also scales each row of x by its inverse root mean square, 1 / sqrt(mean x^2 + eps).
         """

@@ -285,3 +285,22 @@ def test_root_mean_squares_of_any_size(act, eps, M, K):
         exact = sums * want[rows, None] * op.weight_scale.double().cpu().numpy()
         bad = abs(y.double().cpu().numpy() - exact) - (K / 256 + 20) * 2.0 ** -24 * abs(exact) - 2.0 ** -126
         assert bad.max() <= 0, np.unravel_index(bad.argmax(), bad.shape)
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 20])
+def test_outputs_that_take_the_inputs_place(M):
+    """x and the outputs in one memory: the same rows, columns of wider rows that meet or not, rows of another width."""
+    torch = require_gpu()
+    log(f"in place {M}")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    for K, N, width, at, to in ((512, 512, 512, 0, 0), (300, 9000, 9000, 100, 0), (300, 500, 800, 0, 300),
+                                (300, 500, 800, 500, 0), (300, 500, 799, 290, 299)):
+        op = Int8Dense(torch.randn(N, K, generator=g, device="cuda"))
+        buf = torch.randn(M, width, generator=g, device="cuda")
+        want = op(buf[:, at:at + K].clone())
+        y = op(buf[:, at:at + K], out=buf[:, to:to + N])
+        assert torch.equal(y, want) and y.data_ptr() == buf[:, to:].data_ptr()
+    op = Int8Dense(torch.randn(200, 600, generator=g, device="cuda"))  # bfloat16 outputs at the front of float32 rows
+    x = torch.randn(M, 600, generator=g, device="cuda")
+    want = op(x.clone(), out=torch.empty(M, 200, dtype=torch.bfloat16, device="cuda"))
+    assert torch.equal(op(x, out=x.view(torch.bfloat16).view(-1)[:200 * M].view(M, 200)), want)
