@@ -989,8 +989,6 @@ static hm_status check_rows(const void *p, int64_t ld, int64_t width, int64_t ro
     return rows > kMaxElems / ld ? HM_ERR_INVALID_ARG : HM_OK;
 }
 
-constexpr int64_t kMostStride = int64_t(1) << 22;
-
 // Sizes of a call over L tokens, and its inputs' rows.
 static hm_status recurrence_args(const hm_recurrence_desc *d, int64_t L, const void *q, int64_t ld_q, const void *g,
                                  int64_t ld_g, const void *v, int64_t ld_v, hm::RecurArgs *a) {
@@ -1002,9 +1000,8 @@ static hm_status recurrence_args(const hm_recurrence_desc *d, int64_t L, const v
             (st = check_rows(g, ld_g, d->channels, rows, e)) != HM_OK ||
             (st = check_rows(v, ld_v, d->channels, rows, e)) != HM_OK)
             return st;
-        // up to 128 rows are addressed by 32-bit byte offsets
         for (int64_t ld : {q ? ld_q : 0, ld_g, ld_v})
-            if (L > 1 && ld >= kMostStride) return HM_ERR_UNSUPPORTED;
+            if (L > 1 && ld >= hm::kRecurMostStride) return HM_ERR_UNSUPPORTED;
     }
     *a = hm::RecurArgs{};
     a->B = d->batch;
@@ -1064,7 +1061,7 @@ hm_status hyena_recurrence_prefill(const hm_recurrence_desc *desc, int64_t L, co
     if ((st = recurrence_args(desc, L, q, ld_q, g, ld_g, v, ld_v, &a)) != HM_OK) return st;
     if (L > 0 && (st = check_rows(y, ld_y, desc->channels, desc->batch * L, desc->act_dtype == HM_BF16 ? 2 : 4)) != HM_OK)
         return st;
-    if (L > 1 && ld_y >= kMostStride) return HM_ERR_UNSUPPORTED;
+    if (L > 1 && ld_y >= hm::kRecurMostStride) return HM_ERR_UNSUPPORTED;
     if (!state_out) return HM_ERR_INVALID_ARG;
     if (!aligned(state_out, 4) || !aligned(state_in, 4) || !aligned(chunk_states, 4) || !aligned(lengths, 4))
         return HM_ERR_UNSUPPORTED;
@@ -1100,7 +1097,7 @@ hm_status hyena_recurrence_backward(const hm_recurrence_desc *desc, int64_t L, c
             (st = check_rows(dv, ld_dv, desc->channels, rows, e)) != HM_OK)
             return st;
         for (int64_t ld : {ld_dy, dq ? ld_dq : 0, ld_dg, ld_dv})
-            if (L > 1 && ld >= kMostStride) return HM_ERR_UNSUPPORTED;
+            if (L > 1 && ld >= hm::kRecurMostStride) return HM_ERR_UNSUPPORTED;
         if (!chunk_states) return HM_ERR_INVALID_ARG;
     }
     if (!aligned(chunk_states, 4) || !aligned(dstate_out, 4) || !aligned(dstate_in, 4) || !aligned(lengths, 4))

@@ -389,6 +389,9 @@ hipError_t launch_beam_reorder(int64_t groups, int64_t beams, const int32_t *par
 enum RecurGate : int { kGateLog = 0, kGateSigmoid = 1 };
 enum RecurInput : int { kInputFree = 0, kInputConvex = 1, kInputNorm = 2 };
 constexpr int kRecurChunk = 64;  // tokens between two kept states
+constexpr int kRecurRows = 16;   // rows of a wave, at most, which it addresses by 32-bit byte offsets
+constexpr int64_t kRecurMostStride = int64_t(1) << 22;  // strides of several rows stay below it
+static_assert(kRecurRows * kRecurMostStride * 4 < int64_t(1) << 31, "an offset past the last row is not read as none");
 struct RecurArgs {
     int64_t B, D, L;
     int act, gate, input;

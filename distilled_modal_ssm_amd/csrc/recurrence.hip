@@ -139,10 +139,9 @@ template <typename R> __device__ __forceinline__ void opaque(R &x) { asm volatil
 
 // `rows` rows of activations of a tile of channels from row `first` on, none where
 // there is no memory: what lies behind the last one reads as 0 and is not written, nor
-// is a lane past the last channel.  Offsets stay below 2^31: at most 16 rows of fewer
-// than 2^22 elements.
+// is a lane past the last channel.  Offsets stay below 2^31, by kRecurRows and
+// kRecurMostStride.
 constexpr uint32_t kNowhere = 0x80000000u;
-constexpr int64_t kMostStride = int64_t(1) << 22;
 template <int ACT, int V> struct Rows {
     using L = Lane<ACT, V>;
     using R = typename L::R;
@@ -154,7 +153,7 @@ template <int ACT, int V> struct Rows {
         const bool any = p && rows > 0;
         region = make_region(static_cast<const typename Act<ACT>::T *>(p) + (any ? first * ld + c0 : 0),
                              any ? (uint32_t)((rows - 1) * ld + width) * kBytes : 0u);
-        step = (uint32_t)(ld < kMostStride ? ld : kMostStride) * kBytes;  // (larger ones come with one row)
+        step = (uint32_t)(ld < kRecurMostStride ? ld : kRecurMostStride) * kBytes;  // (larger ones come with one row)
         at = lane * V < width ? lane * V * kBytes : kNowhere;
     }
     // ALL: every row is there, and its offset need not count for the bounds
@@ -654,6 +653,7 @@ template <typename F> hipError_t for_types(const RecurArgs &a, F launch) {
 }
 
 constexpr int kWaves = 8, kLong = 16, kShort = 8;  // waves, and tokens of a wave
+static_assert(kLong <= kRecurRows && kShort <= kRecurRows, "rows of a wave");
 
 // Tokens of a workgroup.  A prompt: up to 8 in one wave, else 8 a wave where 64 are
 // enough, else 16.  Backward 8 a wave, whose registers hold twice as much a token.

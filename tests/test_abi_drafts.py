@@ -99,6 +99,16 @@ def test_recurrence_own_arguments():
     assert hb.load().hyena_recurrence_workspace(ctypes.byref(_desc()), 10, None) == BAD
 
 
+@pytest.mark.parametrize("ld", [1 << 22, 1 << 30])
+def test_recurrence_strides(ld):
+    """Rows too far apart for a wave's 32-bit offsets: of every tensor, where there are several."""
+    d = _desc(batch=1)
+    for name in ("q", "g", "v", "y"):
+        _refused(NO, _prompt, d, L=2, **{"ld_" + name: ld})
+    for name in ("q", "g", "v", "dy", "dq", "dg", "dv"):
+        _refused(NO, _backward, d, L=2, **{"ld_" + name: ld})
+
+
 @pytest.mark.parametrize("B,D,L", [(1 << 23, 1, 1), (1 << 20, 512, 1), (1 << 9, 64, 1 << 20), (1, 1 << 29, 1)])
 def test_recurrence_sizes_of_a_launch(B, D, L):
     """Batch rows, channel tiles and chunks that a launch has no threads for are refused; half as many are not."""
