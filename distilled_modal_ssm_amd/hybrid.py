@@ -189,7 +189,7 @@ class HybridLM:
 
     def generate_drafted(self, prompts, draft, steps: int, drafts=4, temperature=1.0, generator=None):
         """``steps`` tokens drawn behind every prompt [B][L], distributed as this model's at the given
-        temperature, with the help of ``draft``, a HybridLM of the same vocabulary.
+        temperature (one below 2^-126 counts as that), with the help of ``draft``, a HybridLM of the same vocabulary.
 
         Returns (tokens [B][steps], rate of drafted tokens that were kept).
         """
@@ -199,7 +199,12 @@ class HybridLM:
         if T < 1 or steps < 1 or not temperature > 0:
             raise ValueError("need at least one draft and one step, and a temperature above 0")
         B = prompts.shape[0]
-        probs = lambda logits: torch.softmax(logits.float() / temperature, -1)  # noqa: E731
+        cold = max(float(temperature), 2.0 ** -126)  # (1 / cold is a float32 too)
+
+        def probs(logits):
+            logits = logits.float()
+            return torch.softmax((logits - logits.amax(-1, keepdim=True)) / cold, -1)  # (at most 0: none is infinite)
+
         rand = lambda n: torch.rand((B, n), generator=generator, device=self.device)  # noqa: E731
         one = DraftVerify(B, 0, self.vocab, device=self.device)
         several = DraftVerify(B, T, self.vocab, device=self.device)

@@ -1,0 +1,93 @@
+"""The loop of drafted generation without a GPU: models whose logits are a table of the last token, and the
+verification by its definition in place of the library's."""
+
+import pytest
+
+from distilled_modal_ssm_amd import hybrid
+
+
+class _Verify:
+    """DraftVerify on the host; probabilities that are none count as 0, and rows without any draw -1."""
+
+    def __init__(self, batch, drafts, vocab, device=None):
+        self.T = drafts
+
+    def verify(self, p, tokens, u, q=None):
+        import torch
+        clean = lambda x: torch.where(torch.isfinite(x) & (x > 0), x, 0.0 * torch.ones_like(x)).double()  # noqa: E731
+        p, q = clean(p), None if q is None else clean(q)
+        out, counts = torch.full((p.shape[0], self.T + 1), -1, dtype=torch.int32), []
+        for b in range(p.shape[0]):
+            n = 0
+            while n < self.T and 0 <= (x := int(tokens[b, n])) and float(u[b, n]) * float(q[b, n, x]) < float(p[b, n, x]):
+                out[b, n] = x
+                n += 1
+            w = p[b, n]
+            if n < self.T:
+                left = (w - q[b, n]).clamp(min=0)
+                w = left if float(left.sum()) > 0 else w
+            over = torch.nonzero(w.cumsum(0) > float(u[b, self.T]) * float(w.sum()))
+            out[b, n] = int(over[0]) if len(over) else -1
+            counts.append(n)
+        return out, torch.tensor(counts, dtype=torch.int32)
+
+
+class _Table(hybrid.HybridLM):
+    """Its state is a count of the tokens read; logits of a row: table[last token], or change(count, logits)."""
+
+    def __init__(self, table, change=None):
+        import torch
+        super().__init__([], torch.zeros(table.shape[0], 4), None, device="cpu")
+        self.table, self.change = table, change
+
+    def _logits(self, count, tokens):
+        logits = self.table[tokens.long()].clone()
+        return self.change(count, logits) if self.change else logits
+
+    def _operators(self, rows):
+        return []
+
+    def prefill(self, tokens, last=False):
+        import torch
+        count = torch.full((tokens.shape[0],), tokens.shape[1])
+        return self._logits(count, tokens[:, -1]), [count]
+
+    def _step(self, ops, states, tokens):
+        states[0] += 1
+        return self._logits(states[0], tokens)
+
+    def _extend(self, ops, states, tokens, head=True):
+        import torch
+        logits = [self._logits(states[0] + 1 + t, tokens[:, t]) for t in range(tokens.shape[1])]
+        return torch.stack(logits, 1), None
+
+    def _commit(self, ops, states, seen, lengths):
+        states[0] += lengths
+
+
+@pytest.fixture
+def verified(monkeypatch):
+    monkeypatch.setattr(hybrid, "DraftVerify", _Verify)
+
+
+def _models(torch, change=None, draft_change=None, V=40):
+    g = torch.Generator().manual_seed(3)
+    return _Table(4 * torch.randn(V, V, generator=g), change), _Table(4 * torch.randn(V, V, generator=g), draft_change)
+
+
+def _greedy(table, prompts, steps):
+    out, x = [], prompts[:, -1]
+    for _ in range(steps):
+        x = table[x].argmax(-1)
+        out.append(x)
+    return out
+
+
+@pytest.mark.parametrize("temperature", [1e-4, 1e-30, 1e-38, 1e-42, 5e-324])
+def test_any_temperature_above_zero(verified, temperature):
+    """The coldest ones are greedy: no logit leaves float32's range on the way."""
+    import torch
+    model, draft = _models(torch)
+    prompts = torch.arange(12).view(6, 2)
+    tokens, rate = model.generate_drafted(prompts, draft, 9, drafts=3, temperature=temperature)
+    assert torch.equal(tokens.long(), torch.stack(_greedy(model.table, prompts, 9), 1)) and 0 <= rate < 1
