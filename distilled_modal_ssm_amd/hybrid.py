@@ -191,7 +191,8 @@ class HybridLM:
         """``steps`` tokens drawn behind every prompt [B][L], distributed as this model's at the given
         temperature (one below 2^-126 counts as that), with the help of ``draft``, a HybridLM of the same vocabulary.
 
-        Returns (tokens [B][steps], rate of drafted tokens that were kept).
+        Returns (tokens [B][steps], rate of drafted tokens that were kept).  Raises ValueError where this
+        model's logits for one of them give no probabilities; a draft's that do not are refused.
         """
         torch, T = self.torch, int(drafts)
         if draft.vocab != self.vocab:
@@ -220,7 +221,16 @@ class HybridLM:
         done = torch.ones((B, 1), dtype=torch.int64, device=self.device)
         place = torch.arange(T + 1, device=self.device)
         kept = asked = 0
-        while int(done.min()) < steps:
+
+        def progress(accepted):
+            """The fewest tokens a row has, and drafts that were kept; what is returned holds no -1."""
+            least, lowest, n = torch.stack([done.min(), out[:, :steps].min().long(), accepted.sum()]).tolist()
+            if lowest < 0:
+                raise ValueError("a prompt's logits give no probabilities (NaN or infinite)")
+            return least, n
+
+        least, _ = progress(done)
+        while least < steps:
             trial, x, tokens, q = [s.clone() for s in draft_states], last, [last], []
             for _ in range(T):
                 q.append(probs(draft._step(draft_ops, trial, x.view(B))))
@@ -237,6 +247,7 @@ class HybridLM:
             # rows that have their steps write on behind them, in the same places again
             at = done.clamp(max=steps) + place
             out.scatter_(1, at, torch.where(place <= accepted[:, None], next_, out.gather(1, at)))
-            kept, asked = kept + int(accepted.sum()), asked + B * T
             done += lengths[:, None]
+            least, n = progress(accepted)
+            kept, asked = kept + n, asked + B * T
         return out[:, :steps], kept / max(asked, 1)

@@ -91,3 +91,36 @@ def test_any_temperature_above_zero(verified, temperature):
     prompts = torch.arange(12).view(6, 2)
     tokens, rate = model.generate_drafted(prompts, draft, 9, drafts=3, temperature=temperature)
     assert torch.equal(tokens.long(), torch.stack(_greedy(model.table, prompts, 9), 1)) and 0 <= rate < 1
+
+
+@pytest.mark.parametrize("at", [2, 3, 5, 10])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_logits_that_give_no_probabilities(verified, at, value):
+    """Behind ``at`` tokens one row has none: an error, not tokens of -1, once they are to be returned."""
+    import torch
+
+    def change(count, logits):
+        logits[3][count[3] == at] = value
+        return logits
+
+    model, draft = _models(torch, change)
+    prompts = torch.arange(12).view(6, 2)
+    with pytest.raises(ValueError):
+        model.generate_drafted(prompts, draft, 9, drafts=3, temperature=1e-4)
+    if at > 2:  # read, if at all, for tokens behind the last one asked for
+        tokens, _ = model.generate_drafted(prompts, draft, at - 2, drafts=3, temperature=1e-4)
+        assert torch.equal(tokens.long(), torch.stack(_greedy(model.table, prompts, at - 2), 1))
+
+
+def test_a_draft_without_probabilities_is_refused(verified):
+    """The target's tokens do not depend on it."""
+    import torch
+
+    def change(count, logits):
+        logits[2][count[2] >= 4] = float("nan")
+        return logits
+
+    model, draft = _models(torch, None, change)
+    prompts = torch.arange(12).view(6, 2)
+    tokens, _ = model.generate_drafted(prompts, draft, 9, drafts=3, temperature=1e-4)
+    assert torch.equal(tokens.long(), torch.stack(_greedy(model.table, prompts, 9), 1))
