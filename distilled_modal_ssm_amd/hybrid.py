@@ -26,6 +26,8 @@ no lengths, step through the pass token by token and keep the state of each.
 
 from __future__ import annotations
 
+import functools
+
 from . import binding as hb
 from .beam import BeamSearch
 from .drafts import DraftVerify
@@ -34,6 +36,15 @@ from .linear_attention import LinearAttention
 from .recurrence import GatedRecurrence
 
 RMS_EPS = 1e-6
+
+
+def _on_device(method):
+    """``method`` with the model's device current: the library works on the current device's memory."""
+    @functools.wraps(method)
+    def call(self, *args, **kw):
+        with hb._On(self.device, None):
+            return method(self, *args, **kw)
+    return call
 
 
 class HybridLM:
@@ -47,7 +58,7 @@ class HybridLM:
     def __init__(self, layers, embedding, head, device="cuda"):
         import torch
         self.torch = torch
-        self.device = torch.device(device)
+        self.device = torch.empty(0, device=device).device  # with its index
         self.layers = layers
         self.embedding, self.head = embedding, head
         self.vocab, self.D = int(embedding.shape[0]), int(embedding.shape[1])
@@ -84,6 +95,7 @@ class HybridLM:
     def _new(self, *shape):
         return self.torch.empty(shape, dtype=self.torch.bfloat16, device=self.device)
 
+    @_on_device
     def prefill(self, tokens, last=False):
         """tokens [B][L] -> (logits [B * L][vocab], or [B][vocab] of each prompt's ``last`` position
         alone, and the layers' states)."""
@@ -100,6 +112,7 @@ class HybridLM:
             x = x.view(B, L, D)[:, -1].contiguous()
         return self._dense(x, self.head, self._new(x.shape[0], self.vocab)), states
 
+    @_on_device
     def generate(self, prompts, beams: int, steps: int, end_token=None):
         """The best ``beams`` continuations of every prompt [G][L]: (tokens [G][beams][steps],
         scores [G][beams]), best first.  Past its end a sequence repeats end_token."""
@@ -187,6 +200,7 @@ class HybridLM:
                 op.prefill(*kept, *((p,) if kind == "attention" else ()), lengths=lengths, state_in=state,
                            state_out=state)
 
+    @_on_device
     def generate_drafted(self, prompts, draft, steps: int, drafts=4, temperature=1.0, generator=None):
         """``steps`` tokens drawn behind every prompt [B][L], distributed as this model's at the given
         temperature (one below 2^-126 counts as that), with the help of ``draft``, a HybridLM of the same vocabulary.
@@ -195,8 +209,8 @@ class HybridLM:
         model's logits for one of them give no probabilities; a draft's that do not are refused.
         """
         torch, T = self.torch, int(drafts)
-        if draft.vocab != self.vocab:
-            raise ValueError("the drafting model needs the same vocabulary")
+        if draft.vocab != self.vocab or draft.device != self.device:
+            raise ValueError("the drafting model needs the same vocabulary and device")
         if T < 1 or steps < 1 or not temperature > 0:
             raise ValueError("need at least one draft and one step, and a temperature above 0")
         B = prompts.shape[0]

@@ -3,6 +3,7 @@ verification by its definition in place of the library's."""
 
 import pytest
 
+from distilled_modal_ssm_amd import binding as hb
 from distilled_modal_ssm_amd import hybrid
 
 
@@ -65,9 +66,25 @@ class _Table(hybrid.HybridLM):
         states[0] += lengths
 
 
+class _On:
+    """Stands in for the binding's: the devices that are current, one inside the other."""
+
+    current = []
+
+    def __init__(self, device, stream):
+        self.device = device
+
+    def __enter__(self):
+        self.current.append(self.device)
+
+    def __exit__(self, *exc):
+        self.current.pop()
+
+
 @pytest.fixture
 def verified(monkeypatch):
     monkeypatch.setattr(hybrid, "DraftVerify", _Verify)
+    monkeypatch.setattr(hb, "_On", _On)
 
 
 def _models(torch, change=None, draft_change=None, V=40):
@@ -124,3 +141,36 @@ def test_a_draft_without_probabilities_is_refused(verified):
     prompts = torch.arange(12).view(6, 2)
     tokens, _ = model.generate_drafted(prompts, draft, 9, drafts=3, temperature=1e-4)
     assert torch.equal(tokens.long(), torch.stack(_greedy(model.table, prompts, 9), 1))
+
+
+@pytest.mark.parametrize("call", ["prefill", "generate", "generate_drafted"])
+def test_the_models_device_is_current(monkeypatch, call):
+    """At the library's calls, whichever device is current for the caller."""
+    import torch
+
+    class Reached(Exception):
+        pass
+
+    def library(*args):
+        assert _On.current and all(d == model.device for d in _On.current)
+        raise Reached
+
+    monkeypatch.setattr(hb, "_On", _On)
+    monkeypatch.setattr(hybrid, "DraftVerify", _Verify)
+    monkeypatch.setattr(hb, "hyena_dense_bf16", library)
+    # (the prompt's logits would make it current for themselves alone)
+    inner = hybrid.HybridLM.prefill
+    monkeypatch.setattr(hybrid.HybridLM, "prefill", getattr(inner, "__wrapped__", inner) if call != "prefill" else inner)
+    model = hybrid.HybridLM([], torch.zeros(50, 64), torch.zeros(50, 64), device="cpu")
+    prompts = torch.zeros(2, 3, dtype=torch.int64)
+    args = {"prefill": (prompts,), "generate": (prompts, 2, 3), "generate_drafted": (prompts, model, 3)}
+    with pytest.raises(Reached):
+        getattr(model, call)(*args[call])
+
+
+def test_a_draft_on_another_device_is_refused(verified):
+    import torch
+    model, draft = _models(torch)
+    draft.device = torch.device("meta")
+    with pytest.raises(ValueError):
+        model.generate_drafted(torch.zeros(1, 2, dtype=torch.int64), draft, 3)
