@@ -71,16 +71,31 @@ template <int W> __device__ __forceinline__ RowStat joined(RowStat s) {
     return s;
 }
 
-// Whether the row's squares have to be summed again, in float64: where float32's sum has
-// left its range, or where squares below 2^-149 could count, of rows below 2^-50 (K of
-// them are less than 2^-132, and the largest square is 2^-100 at least) without an eps
-// that is larger than any of them.
-__device__ __forceinline__ bool sum_again(const QuantArgs &a, const RowStat &s) {
-    if (!a.rms || s.top == 0 || s.top >= 0x7f800000u) return false;
-    return !(s.sum < __builtin_inff()) || (__uint_as_float(s.top) < 0x1p-50f && a.eps < 0x1p-100f);
+// The row's scale; 0 of a row of zeros, without eps too.
+__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s) {
+    float scale = __uint_as_float(s.top) / 127.0f;
+    if (a.rms && s.top > 0) scale = scale / sqrtf(s.sum / (float)a.K + a.eps);
+    return s.top < 0x7f800000u ? scale : __builtin_nanf("");
 }
 
-// That sum of W waves' row, in all of them.
+// Whether the row's squares have to be summed again, in float64, and its scale formed
+// there: where float32's sum has left its range; where amax / 127 is subnormal, and loses
+// digits that the root gives back; where squares below 2^-149 could count, of rows below
+// 2^-50 (K of them are less than 2^-132, and the largest square is 2^-100 at least)
+// without an eps that is larger than any of them.  (Behind everything else, as one branch
+// of the wave: with the two scales side by side, 5 x 6144 x 2048 took 0.4 us of 8.7 more.)
+__device__ __forceinline__ bool sum_again(const QuantArgs &a, const RowStat &s) {
+    if (!a.rms) return false;
+    const uint32_t low = __float_as_uint(a.eps < 0x1p-100f ? 0x1p-50f : 0x1p-118f);
+    return __builtin_amdgcn_readfirstlane((int)(s.top - 1 < low - 1 || !(s.sum < __builtin_inff())));
+}
+
+__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s, double squares) {
+    if (s.top >= 0x7f800000u) return __builtin_nanf("");
+    return (float)(__uint_as_float(s.top) / 127.0 / sqrt(squares / (double)a.K + (double)a.eps));
+}
+
+// The sum of W waves' row, in all of them.
 template <int W> __device__ __forceinline__ double joined(double sum) {
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
@@ -93,16 +108,6 @@ template <int W> __device__ __forceinline__ double joined(double sum) {
         for (int w = 1; w < W; ++w) sum += all[w];
     }
     return sum;
-}
-
-// squares: where sum_again says so.  Rows whose amax / 127 would be subnormal, and lose
-// digits that the root gives back, are scaled in float64 too.
-__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s, double squares) {
-    const float amax = __uint_as_float(s.top);
-    if (s.top >= 0x7f800000u) return __builtin_nanf("");
-    if (!a.rms || s.top == 0) return amax / 127.0f;
-    if (sum_again(a, s) || amax < 0x1p-118f) return (float)(amax / 127.0 / sqrt(squares / (double)a.K + (double)a.eps));
-    return amax / 127.0f / sqrtf(s.sum / (float)a.K + a.eps);
 }
 
 // E values' integers as bytes.
@@ -213,8 +218,11 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     take_row<ACT>(s, piece);
     s = joined<W>(s);
     put_row<ACT>(a.q + block_of(m, K), (int)(m % 16), (K + 63) / 64 * 64, lane, kLanes, piece, s);
-    const double squares = sum_again(a, s) ? joined<W>(squares_of<ACT>(piece)) : 0.0;
-    if (lane == 0) a.scale[m] = row_scale(a, s, squares);
+    if (lane == 0) a.scale[m] = row_scale(a, s);
+    if (__builtin_expect(sum_again(a, s), 0)) {
+        const double squares = joined<W>(squares_of<ACT>(piece));
+        if (lane == 0) a.scale[m] = row_scale(a, s, squares);
+    }
 }
 
 // Longer rows: one workgroup a row, which is read twice, the second time from the caches
@@ -237,15 +245,16 @@ __global__ __launch_bounds__(256) void quantize_long_rows_kernel(QuantArgs a) {
         load_row<ACT>(x + (int64_t)k * EB, K - k < kTurn ? K - k : kTurn, tid, 256, piece);
         put_row<ACT>(q + (int64_t)k / 64 * 1024, (int)(m % 16), end - k, tid, 256, piece, s);
     }
-    double squares = 0.0;
-    if (sum_again(a, s)) {
+    if (tid == 0) a.scale[m] = row_scale(a, s);
+    if (__builtin_expect(sum_again(a, s), 0)) {
+        double squares = 0.0;
         for (int k = 0; k < K; k += kTurn) {
             load_row<ACT>(x + (int64_t)k * EB, K - k < kTurn ? K - k : kTurn, tid, 256, piece);
             squares += squares_of<ACT>(piece);
         }
         squares = joined<4>(squares);
+        if (tid == 0) a.scale[m] = row_scale(a, s, squares);
     }
-    if (tid == 0) a.scale[m] = row_scale(a, s, squares);
 }
 
 template <int ACT> void launch_quantize(const QuantArgs &a, hipStream_t stream) {
@@ -535,6 +544,8 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
     for (int k = 0; k < kSteps; ++k)  // (past the share: the last step's, not used)
         wf[k] = *reinterpret_cast<const uint4 *>(pw + 1024 * (int64_t)(first + k < steps ? first + k : steps - 1));
     u32x4 piece[kTurns][N];
+    bool again[kTurns];
+    RowStat stat[kTurns];
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
         const int m = w + W * t;
@@ -543,14 +554,22 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
         const int m = w + W * t;
-        if (m >= M) break;
+        again[t] = false;
+        if (m >= M) continue;
         RowStat s{0, 0.0f};
         take_row<ACT>(s, piece[t]);
         s = joined<1>(s);
         put_row<ACT>(rows, m, 64 * steps, lane, kWave, piece[t], s);
-        const double squares = sum_again(a, s) ? joined<1>(squares_of<ACT>(piece[t])) : 0.0;
-        if (lane == 0) scales[m] = row_scale(a, s, squares);
+        if (lane == 0) scales[m] = row_scale(a, s);
+        again[t] = sum_again(a, s);
+        stat[t] = s;
     }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t)
+        if (__builtin_expect(again[t], 0)) {
+            const double squares = joined<1>(squares_of<ACT>(piece[t]));
+            if (lane == 0) scales[w + W * t] = row_scale(a, stat[t], squares);
+        }
     __syncthreads();
     i32x4 acc = {0, 0, 0, 0};  // (rows that are none hold anything, and are not stored)
 #pragma unroll
