@@ -90,15 +90,19 @@ __device__ __forceinline__ bool sum_again(const QuantArgs &a, const RowStat &s) 
     return __builtin_amdgcn_readfirstlane((int)(s.top - 1 < low - 1 || !(s.sum < __builtin_inff())));
 }
 
-__device__ __forceinline__ float row_scale(const QuantArgs &a, const RowStat &s, double squares) {
-    if (s.top >= 0x7f800000u) return __builtin_nanf("");
-    return (float)(__uint_as_float(s.top) / 127.0 / sqrt(squares / (double)a.K + (double)a.eps));
-}
-
-// The sum of W waves' row, in all of them.
-template <int W> __device__ __forceinline__ double joined(double sum) {
+// That scale, by W waves, in all of them.  The row is read again, a value at a time: kept
+// in registers it would take them from every row.
+template <int ACT, int W>
+__device__ __forceinline__ float row_scale_again(const QuantArgs &a, int64_t m, uint32_t top) {
+    const typename Act<ACT>::T *x = static_cast<const typename Act<ACT>::T *>(a.x) + m * a.ldx;
+    double sum = 0.0;
+#pragma nounroll
+    for (int64_t k = threadIdx.x % (W * kWave); k < a.K; k += W * kWave) {
+        const double v = Act<ACT>::ld(x + k);
+        sum = fma(v, v, sum);
+    }
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
     if constexpr (W > 1) {
         __shared__ double all[W];
         if (threadIdx.x % kWave == 0) all[threadIdx.x / kWave] = sum;
@@ -107,7 +111,8 @@ template <int W> __device__ __forceinline__ double joined(double sum) {
 #pragma unroll
         for (int w = 1; w < W; ++w) sum += all[w];
     }
-    return sum;
+    if (top >= 0x7f800000u) return __builtin_nanf("");
+    return (float)(__uint_as_float(top) / 127.0 / sqrt(sum / (double)a.K + (double)a.eps));
 }
 
 // E values' integers as bytes.
@@ -166,19 +171,6 @@ template <int ACT, int N> __device__ __forceinline__ void take_row(RowStat &s, c
     }
 }
 
-template <int ACT, int N> __device__ __forceinline__ double squares_of(const u32x4 (&piece)[N]) {
-    constexpr int E = 16 / Act<ACT>::kBytes;
-    double sum = 0.0;
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        float v[E];
-        piece_values<ACT>(piece, k, v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum = fma((double)v[e], (double)v[e], sum);
-    }
-    return sum;
-}
-
 // The integers of load_row's values, to row r of blocks that have `end` columns.
 template <int ACT, int N>
 __device__ __forceinline__ void put_row(int8_t *blocks, int r, int end, int at, int lanes, const u32x4 (&piece)[N], const RowStat &s) {
@@ -220,8 +212,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     put_row<ACT>(a.q + block_of(m, K), (int)(m % 16), (K + 63) / 64 * 64, lane, kLanes, piece, s);
     if (lane == 0) a.scale[m] = row_scale(a, s);
     if (__builtin_expect(sum_again(a, s), 0)) {
-        const double squares = joined<W>(squares_of<ACT>(piece));
-        if (lane == 0) a.scale[m] = row_scale(a, s, squares);
+        const float scale = row_scale_again<ACT, W>(a, m, s.top);
+        if (lane == 0) a.scale[m] = scale;
     }
 }
 
@@ -247,13 +239,8 @@ __global__ __launch_bounds__(256) void quantize_long_rows_kernel(QuantArgs a) {
     }
     if (tid == 0) a.scale[m] = row_scale(a, s);
     if (__builtin_expect(sum_again(a, s), 0)) {
-        double squares = 0.0;
-        for (int k = 0; k < K; k += kTurn) {
-            load_row<ACT>(x + (int64_t)k * EB, K - k < kTurn ? K - k : kTurn, tid, 256, piece);
-            squares += squares_of<ACT>(piece);
-        }
-        squares = joined<4>(squares);
-        if (tid == 0) a.scale[m] = row_scale(a, s, squares);
+        const float scale = row_scale_again<ACT, 4>(a, m, s.top);
+        if (tid == 0) a.scale[m] = scale;
     }
 }
 
@@ -545,7 +532,7 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
         wf[k] = *reinterpret_cast<const uint4 *>(pw + 1024 * (int64_t)(first + k < steps ? first + k : steps - 1));
     u32x4 piece[kTurns][N];
     bool again[kTurns];
-    RowStat stat[kTurns];
+    uint32_t top[kTurns];
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
         const int m = w + W * t;
@@ -562,13 +549,13 @@ __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8
         put_row<ACT>(rows, m, 64 * steps, lane, kWave, piece[t], s);
         if (lane == 0) scales[m] = row_scale(a, s);
         again[t] = sum_again(a, s);
-        stat[t] = s;
+        top[t] = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.top);
     }
 #pragma unroll
     for (int t = 0; t < kTurns; ++t)
         if (__builtin_expect(again[t], 0)) {
-            const double squares = joined<1>(squares_of<ACT>(piece[t]));
-            if (lane == 0) scales[w + W * t] = row_scale(a, stat[t], squares);
+            const float scale = row_scale_again<ACT, 1>(a, w + W * t, top[t]);
+            if (lane == 0) scales[w + W * t] = scale;
         }
     __syncthreads();
     i32x4 acc = {0, 0, 0, 0};  // (rows that are none hold anything, and are not stored)
