@@ -507,9 +507,26 @@ __global__ __launch_bounds__(W *kWave) void dense_int8_few_kernel(Int8GemmArgs g
 }
 
 // The same for up to kFusedRows rows of up to kFusedK inputs that the outputs do not
-// overwrite, which every workgroup brings to 8 bits itself while its weights are on their way: wave w takes rows w and w + 4 into
-// the LDS.  (5 x 6144 x 2048: a call of 8.4 us, 12.0 in two launches.)
+// overwrite, which every workgroup brings to 8 bits itself while its weights are on their
+// way: wave w takes rows w and w + 4 into the LDS.
+//
+// The limits, by measurements at 200 sizes with weights from HBM.  us of the GPU alone, in
+// two launches and in one; in brackets of a call from Python, at least 9.2 in two and 6.9
+// in one:
+//   2048 x 2048: 1 row 7.0, 4.9; 8 rows 7.5, 7.2; 12 rows (a copy of this for 16) 7.8, 9.6.
+//   4096 inputs (a copy): 1 row 10.4, 7.0; 8 rows 11.1, 13.0; and its registers make 2048
+//   inputs slower, 8 rows 8.2.
+//   8192 outputs, two workgroups a CU, of 2048 inputs: 4 rows 8.6, 7.5 (8.9, 7.4); 8 rows
+//   8.7, 9.9 (8.9, 9.9), the worst below that limit.
+//   16384 outputs, four workgroups a CU, as many as it holds: 8 rows of 512 6.9, 8.2 (9.5,
+//   8.1); 4 of 2048 10.5, 9.8 (10.3, 9.8); 8 of 2048 10.6, 13.0 (10.4, 12.9).
+//   32003: 1 row of 512 7.9, 10.9 (9.5, 10.7); 8 rows of 2048 15.9, 21.6 (15.6, 21.3): every
+//   turn of workgroups brings the rows to 8 bits again.
 constexpr int kFusedRows = 8, kFusedK = 2048;
+
+bool in_one_launch(const Int8GemmArgs &g) {
+    return g.M <= kFusedRows && g.K <= kFusedK && (g.N <= 8192 || (g.N <= 16384 && g.M * g.K <= 8192));
+}
 
 template <int ACT, int OUT>
 __global__ __launch_bounds__(256) void dense_int8_fused_kernel(QuantArgs a, Int8GemmArgs g) {
@@ -607,7 +624,7 @@ hipError_t launch_quantize_rows(const QuantArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_dense_int8_rows(const QuantArgs &a, const Int8GemmArgs &g, bool apart, hipStream_t stream) {
-    if (apart && g.M <= kFusedRows && g.K <= kFusedK) {
+    if (apart && in_one_launch(g)) {
         const dim3 grid((unsigned)((g.N + 15) / 16));
         if (a.act == kBF16 && g.act == kBF16) dense_int8_fused_kernel<kBF16, kBF16><<<grid, 256, 0, stream>>>(a, g);
         else if (a.act == kBF16) dense_int8_fused_kernel<kBF16, kF32><<<grid, 256, 0, stream>>>(a, g);

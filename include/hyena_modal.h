@@ -814,8 +814,9 @@ hm_status hyena_dense_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, con
 /*
  * Both for rows of float32 or bfloat16: hyena_quantize_rows of x, and the products with
  * W.  workspace: hyena_dense_int8_rows_workspace bytes, 256-byte aligned, scratch.  (A few
- * short rows take one launch, else two.)  C may overlap x, whose rows are then brought to
- * 8 bits in a launch of their own; nothing else may overlap.
+ * short rows take one launch where there are not too many outputs, else two.)  C may
+ * overlap x, whose rows are then brought to 8 bits in a launch of their own; nothing
+ * else may overlap.
  */
 hm_status hyena_dense_int8_rows_workspace(int64_t M, int64_t K, size_t *bytes);
 

@@ -304,3 +304,18 @@ def test_outputs_that_take_the_inputs_place(M):
     x = torch.randn(M, 600, generator=g, device="cuda")
     want = op(x.clone(), out=torch.empty(M, 200, dtype=torch.bfloat16, device="cuda"))
     assert torch.equal(op(x, out=x.view(torch.bfloat16).view(-1)[:200 * M].view(M, 200)), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 8192, 2048), (5, 8193, 2048), (4, 16384, 2048), (8, 16384, 1024), (8, 16385, 64),
+                                   (1, 32003, 2048), (8, 32003, 512)])
+def test_few_rows_of_many_outputs(M, N, K):
+    """On both sides of the border between one launch and two, and in the largest of one."""
+    torch = require_gpu()
+    log(f"many outputs {M} {N} {K}")
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    x, w = (torch.randn(r, K, generator=g, device="cuda") for r in (M, N))
+    op = Int8Dense(w)
+    X, sx = quantized64(x.double().cpu().numpy())
+    W, sw = quantized64(w.double().cpu().numpy())
+    ref = X @ W.T * sx[:, None] * sw
+    assert (abs(op(x).double().cpu().numpy() - ref) <= 5 * 2.0 ** -24 * abs(ref)).all()
