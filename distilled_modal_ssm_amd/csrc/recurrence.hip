@@ -512,91 +512,91 @@ __global__ __launch_bounds__(W *kWave, 4) void recurrence_backward_kernel(RecurA
             Lane::get(q[j], s);
 #pragma unroll
             for (int e = 0; e < V; ++e) s[e] = !ALL && j >= live ? 0.0f : a.q ? s[e] * d[e] : d[e];
-    };
+        };
 #pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-        float s[V];
-        given(j, s);
+        for (int j = T - 1; j >= 0; --j) {
+            float s[V];
+            given(j, s);
 #pragma unroll
-        for (int e = 0; e < V; ++e) K[e] = f[j][e] * (s[e] + K[e]);
-    }
-    if constexpr (W > 1) {
+            for (int e = 0; e < V; ++e) K[e] = f[j][e] * (s[e] + K[e]);
+        }
+        if constexpr (W > 1) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) runs[w][lane * V + e] = make_float4(A[e], H[e], K[e], 0.0f);
-        __syncthreads();
-        for (int k = 0; k < w; ++k)
+            for (int e = 0; e < V; ++e) runs[w][lane * V + e] = make_float4(A[e], H[e], K[e], 0.0f);
+            __syncthreads();
+            for (int k = 0; k < w; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float4 r = runs[k][lane * V + e];
+                    h[e] = fmaf(r.x, h[e], r.y);
+                }
+            float pA[V], pK[V];  // the waves behind
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float4 r = runs[k][lane * V + e];
-                h[e] = fmaf(r.x, h[e], r.y);
+                pA[e] = 1.0f;
+                pK[e] = 0.0f;
             }
-        float pA[V], pK[V];  // the waves behind
+            for (int k = W - 1; k > w; --k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            pA[e] = 1.0f;
-            pK[e] = 0.0f;
+                for (int e = 0; e < V; ++e) {
+                    const float4 r = runs[k][lane * V + e];
+                    pK[e] = fmaf(r.x, pK[e], r.z);
+                    pA[e] *= r.x;
+                }
+            if (w == 0) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    K[e] = fmaf(A[e], pK[e], K[e]);
+                    A[e] *= pA[e];
+                }
+            }
+            if (last_run > 0) {
+                float in[V];
+                join<V, W>(a, row_tile, row_tiles, places, last_run - run, W - 1 - w, A, K, back, joined, in);
+#pragma unroll
+                for (int e = 0; e < V; ++e) back[e] = in[e];
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) back[e] = fmaf(pA[e], back[e], pK[e]);
         }
-        for (int k = W - 1; k > w; --k)
+        // the h before every token, in x's place; dq on the way
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            float d[V];
+            Lane::get(dy[j], d);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float4 r = runs[k][lane * V + e];
-                pK[e] = fmaf(r.x, pK[e], r.z);
-                pA[e] *= r.x;
+                const float before = h[e];
+                h[e] = fmaf(f[j][e], h[e], x[j][e]);
+                x[j][e] = before;
+                d[e] = ALL || j < live ? d[e] * h[e] : 0.0f;
             }
-        if (w == 0) {
+            dqr.template store<ALL>(j, d);
+        }
+#pragma unroll
+        for (int j = T - 1; j >= 0; --j) {
+            float s[V], gj[V], vj[V], dg[V], dv[V];
+            // the gate is formed again: kept, it would take the registers of a second workgroup
+            opaque(g[j]);
+            given(j, s);
+            Lane::get(g[j], gj);
+            Lane::get(v[j], vj);
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                K[e] = fmaf(A[e], pK[e], K[e]);
-                A[e] *= pA[e];
+                float ff, i, df, di;
+                gate_grad<GATE, INPUT>(gj[e], ff, i, df, di);
+                const float dh = s[e] + back[e];
+                dg[e] = ALL || j < live ? dh * fmaf(df, x[j][e], di * vj[e]) : 0.0f;
+                dv[e] = ALL || j < live ? dh * i : 0.0f;
+                back[e] = ALL || j < live ? ff * dh : dh;
             }
+            dgr.template store<ALL>(j, dg);
+            dvr.template store<ALL>(j, dv);
         }
-        if (last_run > 0) {
-            float in[V];
-            join<V, W>(a, row_tile, row_tiles, places, last_run - run, W - 1 - w, A, K, back, joined, in);
+        if (run == 0 && w == 0 && mine && a.dstate_in) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) back[e] = in[e];
+            for (int e = 0; e < V; ++e) a.dstate_in[b * a.D + c0 + lane * V + e] = back[e];
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) back[e] = fmaf(pA[e], back[e], pK[e]);
-    }
-    // the h before every token, in x's place; dq on the way
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-        float d[V];
-        Lane::get(dy[j], d);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const float before = h[e];
-            h[e] = fmaf(f[j][e], h[e], x[j][e]);
-            x[j][e] = before;
-            d[e] = ALL || j < live ? d[e] * h[e] : 0.0f;
-        }
-        dqr.template store<ALL>(j, d);
-    }
-#pragma unroll
-    for (int j = T - 1; j >= 0; --j) {
-        float s[V], gj[V], vj[V], dg[V], dv[V];
-        // the gate is formed again: kept, it would take the registers of a second workgroup
-        opaque(g[j]);
-        given(j, s);
-        Lane::get(g[j], gj);
-        Lane::get(v[j], vj);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float ff, i, df, di;
-            gate_grad<GATE, INPUT>(gj[e], ff, i, df, di);
-            const float dh = s[e] + back[e];
-            dg[e] = ALL || j < live ? dh * fmaf(df, x[j][e], di * vj[e]) : 0.0f;
-            dv[e] = ALL || j < live ? dh * i : 0.0f;
-            back[e] = ALL || j < live ? ff * dh : dh;
-        }
-        dgr.template store<ALL>(j, dg);
-        dvr.template store<ALL>(j, dv);
-    }
-    if (run == 0 && w == 0 && mine && a.dstate_in) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) a.dstate_in[b * a.D + c0 + lane * V + e] = back[e];
-    }
     };
     if (n - r0 >= kRun) go(std::true_type{});
     else go(std::false_type{});
