@@ -739,7 +739,8 @@ class _Scratch(dict):
 
     def __init__(self):
         super().__init__()
-        self._locks = {}
+        import torch
+        self.torch, self._locks = torch, {}
 
     def order(self, stream):
         return self._locks.get(stream) or self._locks.setdefault(stream, threading.Lock())
@@ -751,7 +752,7 @@ def _scratch(kept, n, stream, device):
 
     A graph's replays write to the addresses that its capture saw, so a call that torch captures has
     memory of that graph's own, which lives as long as the graph and which no other call is given."""
-    import torch
+    torch = kept.torch
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(n, dtype=torch.uint8, device=device)
     ws = kept.get(stream)
@@ -813,8 +814,10 @@ class ModalHyena:
     def _ws(self):
         return self._buffers or None  # (None before the first)
 
-    def workspace(self, L: int, chunk: int = 0, algo="auto", stream: int = 0):
-        """Scratch memory of a prompt on the current stream, whose hipStream_t is ``stream``, and its bytes."""
+    def workspace(self, L: int, chunk: int = 0, algo="auto", stream=None):
+        """Scratch memory of a prompt on the current stream (whose hipStream_t may be given), and its bytes."""
+        if stream is None:
+            stream = _current_stream(self.device) if self.device.type == "cuda" else 0
         n = hyena_modal_prefill_workspace(self.desc, L, chunk, algo)
         return _scratch(self._buffers, max(n, 256), stream, self.device), n
 
