@@ -96,7 +96,8 @@ class GatedRecurrence:
 
         q (or None), g, v: [B][L][D] views with unit element stride and batch
         rows one after the other.  lengths: int32 [B], tokens of each row (later
-        ones are not read, their y is 0).  state_out may be state_in.
+        ones are not read, their y is 0).  state_out may be state_in; no other
+        output may share memory with an input.
         chunk_states: memory as ``new_chunk_states`` gives it, which a backward
         pass reads.
         """
@@ -133,7 +134,8 @@ class GatedRecurrence:
         q, g, v, lengths as the prompt had them, chunk_states as it left them;
         dy [B][L][D]: the gradient of y; dstate_out float32 [B][D]: that of the
         state after the prompt, or None.  out: the four tensors to write (None
-        for dq without q) instead of new ones.
+        for dq without q) instead of new ones; of them dstate_in alone may be an
+        input (dstate_out).
         """
         shape, lds = self._inputs(q, g, v, lengths)
         ld_dy = self._rows("dy", dy, shape)

@@ -795,15 +795,17 @@ hm_status hyena_int8_bytes(int64_t M, int64_t K, size_t *bytes);
  *   K on set to 0, rows from M on left as they are;  scale [M].
  * Tokens (rows of activations) and output channels (rows of W) alike.
  * 1 <= K <= HM_INT8_MAX_K, M < 2^24, q 16-byte aligned (else HM_ERR_UNSUPPORTED).
+ * Outputs must not overlap x.
  */
 hm_status hyena_quantize_rows(int64_t M, int64_t K, int32_t dtype, const void *x, int64_t ldx,
                               int32_t rms, float eps, int8_t *q, float *scale, void *stream);
 
 /*
  *     C[m][n] = a_scale[m] w_scale[n] sum_k A[m][k] W[n][k],
- * the sum exact in 32-bit integers, C of dtype (hm_dtype) rounded once from
- * float32.  A (M rows) and W (N rows) of K columns as hyena_quantize_rows holds them,
- * 16-byte aligned; what their rows past M and N hold does not matter.  C [M][ldc].
+ * the sum exact in 32-bit integers; sum * a_scale * w_scale in float32, in this order
+ * (infinite where the first product is), then rounded once to dtype (hm_dtype).
+ * A (M rows) and W (N rows) of K columns as hyena_quantize_rows holds them, 16-byte
+ * aligned; what their rows past M and N hold does not matter.  C [M][ldc].
  * 1 <= K <= HM_INT8_MAX_K; M, N < 2^31 - 2^9, and ceil(M / 256) * ceil(N / 256) < 2^20
  * (else HM_ERR_UNSUPPORTED).
  */
@@ -852,6 +854,7 @@ hm_status hyena_dense_int8_rows(int64_t M, int64_t N, int64_t K, int32_t x_dtype
  *             for the drawn token, wherever it comes.
  *   out_tokens    [batch][drafts + 1] int32: the kept drafts, the drawn token, then -1.
  *   out_accepted  [batch] int32: drafts kept.
+ * Outputs must not overlap inputs.
  * Probabilities that are NaN, negative or infinite count as 0.  Weights are
  * compared and summed in float64.  Where max(p - q, 0) is 0 all over, the token
  * is drawn from p; where p is, it is -1.  drafts = 0 draws one token a sequence.
