@@ -847,12 +847,13 @@ class ModalHyena:
     def fft_prefill(self, q, k, v, y=None, stream=None):
         """The prompt through the FFT convolution (no state).  q, k, v: [B][L][ld] views."""
         L = int(q.shape[1])
-        if y is None:
-            y = self.torch.empty((self.B, L, self.D), dtype=self.tdtype, device=self.device)
         ld_in = _row_stride(q, (k, v))
         n = hyena_fft_prefill_workspace(self.desc, L)
-        ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device)
-        hyena_fft_prefill(self.desc, L, q, k, v, ld_in, y, _row_stride(y, ()), ws, n, stream)
+        with _On(self.device, stream) as stream:
+            if y is None:
+                y = self.torch.empty((self.B, L, self.D), dtype=self.tdtype, device=self.device)
+            ws = self.torch.empty(max(n, 256), dtype=self.torch.uint8, device=self.device)
+            hyena_fft_prefill(self.desc, L, q, k, v, ld_in, y, _row_stride(y, ()), ws, n, stream)
         return y
 
     def decode_step(self, q, k, v, state, y=None, stream=None):

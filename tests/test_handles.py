@@ -187,3 +187,31 @@ def test_a_models_products_share_their_scratch(monkeypatch):
     gc.collect()
     again = Int8Dense(torch.zeros(30, 100))
     assert not again._ws
+
+
+def test_fft_prompts_keep_their_scratch_on_their_stream(monkeypatch):
+    """Its memory goes back to torch when the call returns, before its kernels have run: to the stream that runs them."""
+    import numpy as np
+    import torch
+    current = []
+
+    class On:
+        def __init__(self, device, stream):
+            self.stream = 0 if stream is None else stream
+
+        def __enter__(self):
+            current.append(self.stream)
+            return self.stream
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    made, empty = [], torch.empty
+    monkeypatch.setattr(hb, "_On", On)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(list(current)) or empty(*a, **kw))
+    monkeypatch.setattr(hb, "hyena_fft_prefill", lambda *a: made.append(a[-1]))
+    op = hb.ModalHyena(np.zeros((2, 8, 2)), np.zeros((2, 8, 2)), np.zeros(2), 1, 64, "f32", device="cpu")
+    x = torch.zeros(1, 70000, 64)
+    made.clear()
+    op.fft_prefill(x, x, x, stream=7)
+    assert made == [[7], [7], 7]
