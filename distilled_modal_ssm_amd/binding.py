@@ -157,7 +157,10 @@ def _torch_runtime():
     """Loads the HIP runtime that torch brings along, where it is not loaded yet: the library would bring the
     system's, torch its own afterwards, and one process must not run two of them."""
     import importlib.util
-    spec = importlib.util.find_spec("torch")
+    try:
+        spec = importlib.util.find_spec("torch")
+    except ValueError:  # a module that stands in for torch
+        return
     for folder in (spec.submodule_search_locations or ()) if spec is not None else ():
         path = os.path.join(folder, "lib", "libamdhip64.so")
         if os.path.exists(path):

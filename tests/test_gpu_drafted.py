@@ -138,3 +138,32 @@ def test_refusals_and_the_example():
     import drafted_generate
     drafted_generate.main(["--layers", "2", "--width", "64", "--vocab", "200", "--prompt", "20", "--steps", "5",
                            "--batch", "2"])
+
+
+@pytest.mark.parametrize("temperature", [1e-30, 1e-38, 1e-300])
+def test_the_coldest_drafts_are_greedy(temperature):
+    """As at 1e-4: no logit leaves float32's range."""
+    torch = require_gpu()
+    log(f"coldest {temperature}")
+    model = _model(torch, ALL, 128, 400)
+    draft = _model(torch, ("gated",), 64, 400, like=model)
+    prompts = torch.randint(0, 400, (6, 33), generator=torch.Generator().manual_seed(2)).cuda()
+    tokens, _ = model.generate_drafted(prompts, draft, 7, drafts=3, temperature=temperature)
+    logits, _ = model.prefill(torch.cat([prompts, tokens.long()], 1))
+    logits = logits.view(6, 40, 400).float()[:, 32:-1]
+    picked = logits.gather(2, tokens[..., None].long())[..., 0]
+    assert float((logits.max(-1).values - picked).max()) <= 0.1
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_weights_that_are_not_finite_raise(eight):
+    torch = require_gpu()
+    log(f"not finite {eight}")
+    model = _model(torch, ALL, 128, 400)
+    prompts = torch.randint(0, 400, (3, 9), generator=torch.Generator().manual_seed(2)).cuda()
+    model.embedding = model.embedding.clone()
+    model.embedding[prompts[1, -1]] = float("nan")
+    model = model.quantized() if eight else model
+    draft = _model(torch, ("gated",), 64, 400)
+    with pytest.raises(ValueError):
+        model.generate_drafted(prompts, draft, 5, drafts=3)

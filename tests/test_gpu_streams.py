@@ -28,7 +28,13 @@ def _users(torch):
 
     rec_chunks = [rec.new_chunk_states(3000) for _ in range(200)]
     probs = lambda *s: torch.softmax(3 * randn(*s, 70000), -1)  # noqa: E731
+    from distilled_modal_ssm_amd import ModalHyena
+    circle = 0.95 * torch.exp(1j * torch.linspace(0, 3, 16)).view(2, 8)
+    poles, residues = (torch.view_as_real(t.to(torch.complex64)).contiguous() for t in (circle, circle / 8))
+    modal = ModalHyena(poles, residues, torch.ones(2), 1, 128, "f32")
     return {
+        "modal": (lambda x, stream: modal.prefill(*x, stream=stream), lambda: [randn(1, 20000, 128) for _ in range(3)]),
+        "fft": (lambda x, stream: (modal.fft_prefill(*x, stream=stream),), lambda: [randn(1, 20000, 128) for _ in range(3)]),
         "train": (train, lambda: [randn(3, 3000, 300).bfloat16() for _ in range(4)]),
         "dense": (lambda x, stream: (dense(x[0], rms_eps=1e-6, stream=stream),), lambda: [randn(400, 900)]),
         "verify": (lambda x, stream: verify.verify(*x[:3], q=x[3], stream=stream),
@@ -37,7 +43,7 @@ def _users(torch):
     }
 
 
-@pytest.mark.parametrize("user", ["train", "dense", "verify"])
+@pytest.mark.parametrize("user", ["train", "dense", "verify", "modal", "fft"])
 def test_two_streams_at_once(user):
     torch = require_gpu()
     log(f"two streams {user}")
@@ -57,7 +63,7 @@ def test_two_streams_at_once(user):
     assert not torch.equal(want[0][0], want[1][0])
 
 
-@pytest.mark.parametrize("user", ["train", "dense", "verify"])
+@pytest.mark.parametrize("user", ["train", "dense", "verify", "modal", "fft"])
 def test_two_threads_on_one_stream(user):
     torch = require_gpu()
     log(f"two threads {user}")
@@ -99,3 +105,19 @@ def test_chunks_past_a_rows_end_stay(L, act):
         used = -(-n // hb.HM_RECURRENCE_CHUNK)
         assert torch.isfinite(kept[b, :used]).all() and torch.isnan(kept[b, used:]).all(), n
         assert used == 0 or not kept[b, 0].any()
+
+
+def test_streams_by_their_handles():
+    """A stream is given as torch's object or as its hipStream_t, the default one's 0 among them."""
+    torch = require_gpu()
+    log("handles of streams")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for user, (call, new) in _users(torch).items():
+        x = new()
+        want = call(x, None)
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream, 0, torch.cuda.default_stream().cuda_stream):
+            got = call(x, stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), (user, stream)

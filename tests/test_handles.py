@@ -215,3 +215,9 @@ def test_fft_prompts_keep_their_scratch_on_their_stream(monkeypatch):
     made.clear()
     op.fft_prefill(x, x, x, stream=7)
     assert made == [[7], [7], 7]
+
+
+def test_a_module_in_torchs_place(monkeypatch):
+    import types
+    monkeypatch.setitem(sys.modules, "torch", types.ModuleType("torch"))
+    hb._torch_runtime()
