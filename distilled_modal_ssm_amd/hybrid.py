@@ -203,7 +203,8 @@ class HybridLM:
     @_on_device
     def generate_drafted(self, prompts, draft, steps: int, drafts=4, temperature=1.0, generator=None):
         """``steps`` tokens drawn behind every prompt [B][L], distributed as this model's at the given
-        temperature (one below 2^-126 counts as that), with the help of ``draft``, a HybridLM of the same vocabulary.
+        temperature (one below 2^-126 counts as that), with the help of ``draft``, a HybridLM of the same
+        vocabulary.
 
         Returns (tokens [B][steps], rate of drafted tokens that were kept).  Raises ValueError where this
         model's logits for one of them give no probabilities; a draft's that do not are refused.
