@@ -671,9 +671,10 @@ bool read_once(const RecurArgs &a, int tensors) {
 
 // Pairs of bfloat16 channels a lane (4 bytes, as one float32 channel), aligned or not:
 // 65536 x 4095 tokens 602 us against 841 with one, 8 x 2048 x 2047 63 and 79 with inputs
-// in the caches (from HBM 74), backward 128 and 174; 9 x 7095 x 131, two tiles instead of three, 33 and 31.  An odd number only
-// where there is a tile before the last one, and its states (or their gradients) are not
-// replaced before the last tile has read the channel that both have.
+// in the caches (from HBM 74), backward 128 and 174; 9 x 7095 x 131, two tiles instead of
+// three, 33 and 31.  An odd number only where there is a tile before the last one, and its
+// states (or their gradients) are not replaced before the last tile has read the channel
+// that both have.
 bool in_pairs(const RecurArgs &a, const float *from, const float *to) {
     return a.act == kBF16 && (a.D % 2 == 0 || (a.D > 2 * kWave && (from != to || !to)));
 }
